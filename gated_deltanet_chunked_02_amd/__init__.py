@@ -31,6 +31,8 @@ __all__ = [
     "fused_sigmoid_gating_delta_rule", "gdn_chunk_bwd", "gdn_chunk_bwd_workspace_size",
     "chunk_gated_delta_rule_bwd",
     "GdnConvDesc", "gdn_causal_conv1d_fwd", "causal_conv1d", "ACTIVATIONS",
+    "GdnScanDesc", "gdn_selective_scan_fwd", "gdn_selective_scan_workspace_size",
+    "gdn_selective_state_update", "selective_scan", "selective_state_update",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -113,6 +115,7 @@ def load(path: str = LIB_PATH):
     lib.gdn_causal_conv1d_fwd.restype = ctypes.c_int
     lib.gdn_causal_conv1d_fwd.argtypes = [ctypes.POINTER(GdnConvDesc), P, P, P, P, P, P, P, P,
                                           P]
+    ssm.declare(lib)
     _lib = lib
     return lib
 
@@ -563,3 +566,10 @@ def causal_conv1d(x, weight, bias=None, conv_state=None, cache_indices=None,
     if st != 0:
         raise GdnError(st, "gdn_causal_conv1d_fwd")
     return y
+
+
+# the selective state-space calls (they use the helpers above)
+from . import ssm  # noqa: E402
+from .ssm import (GdnScanDesc, gdn_selective_scan_fwd,  # noqa: E402
+                  gdn_selective_scan_workspace_size, gdn_selective_state_update,
+                  selective_scan, selective_state_update)

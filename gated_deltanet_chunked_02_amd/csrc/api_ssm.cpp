@@ -1,0 +1,211 @@
+// C ABI of the selective state-space calls (declared in include/gdn.h): host-side validation,
+// workspace layout and dispatch to the launchers.  No allocation, no synchronisation.
+#include <stdint.h>
+#include <string.h>
+
+#include "gdn.h"
+#include "ssm.h"
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Row strides: 0 is a row after another; a given one is at least a row.
+bool stride_ok(int64_t given, int64_t row, int64_t* out) {
+  *out = given == 0 ? row : given;
+  return given == 0 || (given >= row && given <= (int64_t)1 << 40);
+}
+
+// Descriptor checks shared by the entry points; fills the shape part of the problem, for a
+// packed batch (cu_seqlens given) or a dense one.
+gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->B < 1 || d->T < 0 || d->N < 0 || d->channels < 1 || d->groups < 1 || d->dstate < 1)
+    return GDN_ERR_INVALID_ARG;
+  if (d->channels % d->groups != 0) return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (d->dt_softplus != 0 && d->dt_softplus != 1) return GDN_ERR_INVALID_ARG;
+  if (packed ? d->B != 1 : (d->N != 0 && d->N != d->B)) return GDN_ERR_INVALID_ARG;
+  memset(p, 0, sizeof(*p));
+  const int64_t bcw = (int64_t)d->groups * d->dstate;
+  if (!stride_ok(d->x_stride, d->channels, &p->sx) ||
+      !stride_ok(d->dt_stride, d->channels, &p->sdt) ||
+      !stride_ok(d->z_stride, d->channels, &p->sz) || !stride_ok(d->b_stride, bcw, &p->sb) ||
+      !stride_ok(d->c_stride, bcw, &p->sc))
+    return GDN_ERR_INVALID_ARG;
+  if (d->dstate > 256) return GDN_ERR_UNSUPPORTED;
+  const long long Ttot = (long long)d->B * d->T;
+  p->N = packed ? d->N : d->B;
+  if (Ttot > (1LL << 30) || p->N > (1 << 16) || d->channels > (1 << 20))
+    return GDN_ERR_UNSUPPORTED;
+  p->T = d->T;
+  p->Ttot = (int)Ttot;
+  p->C = d->channels;
+  p->G = d->groups;
+  p->S = d->dstate;
+  p->per = p->C / p->G;
+  p->nblk = (p->per + gdn::kScanLanes - 1) / gdn::kScanLanes;
+  if ((long long)p->G * p->nblk > 65535) return GDN_ERR_UNSUPPORTED;
+  p->f32 = d->dtype == GDN_F32;
+  p->softplus = d->dt_softplus != 0;
+  // the states of 64 channels over the waves of a workgroup: four a lane where that makes at
+  // most four waves, more a lane for larger states
+  p->ns = p->S <= 16 ? 4 : p->S <= 32 ? 8 : 16;
+  p->nw = 1;
+  while (p->nw * p->ns < p->S) p->nw *= 2;
+  p->Sp = p->ns * p->nw;
+  return GDN_OK;
+}
+
+constexpr int kFillWaves = 4096;  // waves that fill 256 CUs (four a SIMD)
+constexpr int kMinChunk = 64;     // shorter chunks are not worth their states
+
+// Chunk length: whole sequences when their (sequence, channel block) pairs fill the GPU, else
+// chunks short enough that they do.
+void plan_chunks(gdn::ScanProblem* p, bool packed) {
+  const long long per_seq = (long long)p->G * p->nblk * p->nw;  // waves of one chunk
+  const long long want = (kFillWaves + per_seq - 1) / per_seq;  // chunks wanted in all
+  p->Lc = gdn::kScanNoSplit;
+  if (p->N > 0 && p->Ttot > 0 && p->N < (packed ? 4 * want : want)) {
+    long long L = (p->Ttot + want - 1) / want;
+    L = (L + gdn::kScanTile - 1) / gdn::kScanTile * gdn::kScanTile;
+    if (L < kMinChunk) L = kMinChunk;
+    if (L < (packed ? p->Ttot : p->T)) p->Lc = (int)L;
+  }
+  p->slots = packed ? p->Ttot / p->Lc + p->N
+                    : p->N * (int)(p->T > p->Lc ? ((long long)p->T + p->Lc - 1) / p->Lc : 1);
+}
+
+struct ScanLayout {
+  size_t bc, hst, dsum, total;
+};
+
+ScanLayout scan_layout(const gdn::ScanProblem& p) {
+  ScanLayout L;
+  size_t o = 0;
+  L.bc = o;
+  o += align_up((size_t)p.Ttot * p.G * 2 * p.Sp * 4);
+  L.hst = o;
+  const bool split = p.Lc != gdn::kScanNoSplit;
+  if (split) o += align_up((size_t)p.slots * p.S * p.C * 4);
+  L.dsum = o;
+  if (split) o += align_up((size_t)p.slots * p.C * 4);
+  L.total = o;
+  return L;
+}
+
+bool looks_packed(const gdn_scan_desc* d) { return d && d->N != 0 && d->N != d->B; }
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* status) {
+  gdn::ScanProblem p;
+  const bool packed = looks_packed(d);
+  const gdn_status s = check_scan(d, packed, &p);
+  if (status) *status = s;
+  if (s != GDN_OK) return 0;
+  plan_chunks(&p, packed);
+  size_t need = scan_layout(p).total;
+  if (!packed && d->B == 1) {  // one sequence may also come as a packed batch of one
+    gdn::ScanProblem q;
+    check_scan(d, false, &q);
+    q.N = 1;
+    plan_chunks(&q, true);
+    const size_t alt = scan_layout(q).total;
+    if (alt > need) need = alt;
+  }
+  return need;
+}
+
+gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm,
+                                  const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* cu_seqlens, void* y, float* ht,
+                                  hipStream_t stream) {
+  gdn::ScanProblem p;
+  const gdn_status s = check_scan(d, cu_seqlens != nullptr, &p);
+  if (s != GDN_OK) return s;
+  if (!A || (p.Ttot > 0 && (!x || !dt || !Bm || !Cm || !y))) return GDN_ERR_INVALID_ARG;
+  const size_t e = p.f32 ? 4 : 2;
+  if (!aligned(x, e) || !aligned(dt, e) || !aligned(z, e) || !aligned(Bm, e) ||
+      !aligned(Cm, e) || !aligned(y, e) || !aligned(A, 4) || !aligned(D, 4) ||
+      !aligned(dt_bias, 4) || !aligned(h0, 4) || !aligned(ht, 4) || !aligned(cu_seqlens, 4))
+    return GDN_ERR_INVALID_ARG;
+  if (p.N == 0) return GDN_OK;
+  plan_chunks(&p, cu_seqlens != nullptr);
+  const ScanLayout L = scan_layout(p);
+  if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
+                      !aligned(d->workspace, kAlign)))
+    return GDN_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(d->workspace);
+  p.bc = reinterpret_cast<float*>(ws + L.bc);
+  p.hst = reinterpret_cast<float*>(ws + L.hst);
+  p.dsum = reinterpret_cast<float*>(ws + L.dsum);
+  p.x = x;
+  p.dt = dt;
+  p.z = z;
+  p.Bm = Bm;
+  p.Cm = Cm;
+  p.A = A;
+  p.D = D;
+  p.bias = dt_bias;
+  p.h0 = h0;
+  p.cu = cu_seqlens;
+  p.y = y;
+  p.ht = ht;
+  return gdn::launch_scan_fwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, const void* x,
+                                      const void* dt, const float* A, const void* Bm,
+                                      const void* Cm, const float* D, const void* z,
+                                      const float* dt_bias, const int32_t* cache_indices,
+                                      const int32_t* out_indices, void* y, hipStream_t stream) {
+  gdn::ScanProblem p;
+  const gdn_status s = check_scan(d, false, &p);
+  if (s != GDN_OK) return s;
+  if (d->T != 1 || d->state_lines < 1) return GDN_ERR_INVALID_ARG;
+  if (!state || !x || !dt || !A || !Bm || !Cm || !y) return GDN_ERR_INVALID_ARG;
+  const size_t e = p.f32 ? 4 : 2;
+  if (!aligned(state, 4) || !aligned(x, e) || !aligned(dt, e) || !aligned(z, e) ||
+      !aligned(Bm, e) || !aligned(Cm, e) || !aligned(y, e) || !aligned(A, 4) ||
+      !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(cache_indices, 4) ||
+      !aligned(out_indices, 4))
+    return GDN_ERR_INVALID_ARG;
+  gdn::ScanStepProblem q;
+  q.B = d->B;
+  q.C = p.C;
+  q.G = p.G;
+  q.S = p.S;
+  q.per = p.per;
+  q.lines = d->state_lines;
+  q.f32 = p.f32;
+  q.softplus = p.softplus;
+  q.vec4 = p.S % 4 == 0 && aligned(state, 16) && aligned(A, 16);
+  q.state = state;
+  q.x = x;
+  q.dt = dt;
+  q.z = z;
+  q.Bm = Bm;
+  q.Cm = Cm;
+  q.A = A;
+  q.D = D;
+  q.bias = dt_bias;
+  q.read = cache_indices;
+  q.write = out_indices;
+  q.sx = p.sx;
+  q.sdt = p.sdt;
+  q.sz = p.sz;
+  q.sb = p.sb;
+  q.sc = p.sc;
+  q.y = y;
+  return gdn::launch_scan_step(q, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+}  // extern "C"

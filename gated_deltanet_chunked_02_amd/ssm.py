@@ -1,0 +1,267 @@
+"""Binding of libgdn's selective state-space calls: argument checks and marshalling only.
+
+    y, ht = selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
+                           initial_state=None, output_final_state=True, cu_seqlens=None)
+    y = selective_state_update(state, x, dt, A, B, C, ..., cache_indices=None,
+                               out_indices=None)
+
+Tensors whose token rows are contiguous and evenly spaced (a slice of a projection's last axis)
+are passed as they are; others are copied first.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import BF16, F32, GdnError, _check_devices, _need, _ptr, load
+
+_FLOATS = None  # filled on first use: importing torch is left to the first call
+
+
+class GdnScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("channels", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dstate", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("dt_softplus", ctypes.c_int32), ("state_lines", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("c_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+def declare(lib):
+    """Argument types of the calls this module makes (run once, when the library is loaded)."""
+    P, S = ctypes.c_void_p, ctypes.c_size_t
+    D, st = ctypes.POINTER(GdnScanDesc), ctypes.POINTER(ctypes.c_int)
+    lib.gdn_selective_scan_workspace_size.restype = S
+    lib.gdn_selective_scan_workspace_size.argtypes = [D, st]
+    lib.gdn_selective_scan_fwd.restype = ctypes.c_int
+    lib.gdn_selective_scan_fwd.argtypes = [D] + [P] * 13
+    lib.gdn_selective_state_update.restype = ctypes.c_int
+    lib.gdn_selective_state_update.argtypes = [D] + [P] * 13
+
+
+def _stream(stream):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def gdn_selective_scan_workspace_size(desc: GdnScanDesc) -> int:
+    st = ctypes.c_int(0)
+    n = load().gdn_selective_scan_workspace_size(ctypes.byref(desc), ctypes.byref(st))
+    if st.value != 0:
+        raise GdnError(st.value, "gdn_selective_scan_workspace_size")
+    return int(n)
+
+
+def gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, y, ht,
+                           stream=None) -> int:
+    """Raw call (tensors, integer device addresses or None); returns the status code."""
+    return int(load().gdn_selective_scan_fwd(
+        ctypes.byref(desc), *map(_ptr, (x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, y, ht)),
+        _stream(stream)))
+
+
+def gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, cache_indices,
+                               out_indices, y, stream=None) -> int:
+    """Raw call (tensors, integer device addresses or None); returns the status code."""
+    return int(load().gdn_selective_state_update(
+        ctypes.byref(desc), *map(_ptr, (state, x, dt, A, B, C, D, z, dt_bias, cache_indices,
+                                        out_indices, y)), _stream(stream)))
+
+
+def _code(t):
+    """The library's code of a tensor's dtype, or None."""
+    global _FLOATS
+    if _FLOATS is None:
+        import torch
+        _FLOATS = {torch.bfloat16: BF16, torch.float32: F32}
+    return _FLOATS.get(t.dtype)
+
+
+def _rows(t, lead):
+    """(t, elements from one row to the next) for a tensor [*lead, ...] whose rows are
+    contiguous and evenly spaced over the leading axes; a contiguous copy of any other."""
+    if t.is_contiguous():
+        return t, 0
+    width, want = 1, 1
+    for n, s in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if n != 1 and s != want:
+            return t.contiguous(), 0
+        want *= n
+        width *= n
+    row = None
+    for n, s in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
+        if n == 1:
+            continue
+        if row is None:
+            row, span = s, s * n
+        elif s != span:
+            return t.contiguous(), 0
+        else:
+            span *= n
+    if row is None:
+        return t, 0
+    return (t, row) if row >= width else (t.contiguous(), 0)
+
+
+def _f32(name, t, shape):
+    import torch
+    if t is None:
+        return None
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.float32, TypeError,
+          "%s must be an fp32 tensor" % name)
+    _need(tuple(t.shape) == shape, ValueError,
+          "%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return t.contiguous()
+
+
+def _indices(name, t, n):
+    import torch
+    if t is None:
+        return None
+    _need(isinstance(t, torch.Tensor) and t.dtype in (torch.int32, torch.int64), TypeError,
+          "%s must be an int32 or int64 tensor" % name)
+    _need(tuple(t.shape) == (n,), ValueError, "%s must be [%d]" % (name, n))
+    return t.to(torch.int32).contiguous()
+
+
+def _operands(x, dt, A, B, C, D, z, dt_bias, lead):
+    """Checks of the operands that the scan and its single-token form share, and the descriptor
+    but for the batch's shape.  ``lead``: axes before the channels."""
+    import torch
+    for name, t in (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C)):
+        _need(isinstance(t, torch.Tensor), TypeError, "%s must be a torch tensor" % name)
+    _need(x.dim() == lead + 1, ValueError,
+          "x must be %s" % ("[B, T, channels]" if lead == 2 else "[B, channels]"))
+    code = _code(x)
+    _need(code is not None, TypeError, "x must be bf16 or fp32, got %s" % x.dtype)
+    shape, ch = tuple(x.shape), x.shape[-1]
+    _need(ch > 0, ValueError, "x must have channels")
+    for name, t in (("dt", dt), ("z", z)):
+        if t is not None:
+            _need(isinstance(t, torch.Tensor) and t.dtype == x.dtype, TypeError,
+                  "%s must be a tensor of x's dtype %s" % (name, x.dtype))
+            _need(tuple(t.shape) == shape, ValueError,
+                  "%s must have x's shape %s" % (name, list(shape)))
+    _need(A.dim() == 2 and A.shape[0] == ch and A.shape[1] > 0, ValueError,
+          "A must be [channels, dstate] with %d channels, got %s" % (ch, list(A.shape)))
+    S = A.shape[1]
+    A = _f32("A", A, (ch, S))
+    for name, t in (("B", B), ("C", C)):
+        _need(t.dtype == x.dtype, TypeError, "%s must have x's dtype %s" % (name, x.dtype))
+        _need(t.dim() == lead + 2 and tuple(t.shape[:lead]) == shape[:lead] and
+              t.shape[-1] == S and t.shape == B.shape, ValueError,
+              "%s must be %s with dstate %d, got %s"
+              % (name, "[B, T, groups, dstate]" if lead == 2 else "[B, groups, dstate]", S,
+                 list(t.shape)))
+    G = B.shape[-2]
+    _need(G > 0 and ch % G == 0, ValueError,
+          "the channels (%d) must be a multiple of the groups (%d)" % (ch, G))
+    D, dt_bias = _f32("D", D, (ch,)), _f32("dt_bias", dt_bias, (ch,))
+    x, sx = _rows(x, lead)
+    dt, sdt = _rows(dt, lead)
+    B, sb = _rows(B, lead)
+    C, sc = _rows(C, lead)
+    sz = 0
+    if z is not None:
+        z, sz = _rows(z, lead)
+    desc = GdnScanDesc(channels=ch, groups=G, dstate=S, dtype=code, x_stride=sx, dt_stride=sdt,
+                       z_stride=sz, b_stride=sb, c_stride=sc)
+    return desc, x, dt, A, B, C, D, z, dt_bias
+
+
+def _sequences(x, cu_seqlens):
+    """(cu_seqlens as int32 or None, number of sequences) of x [B, T, ...]."""
+    import torch
+    if cu_seqlens is None:
+        return None, x.shape[0]
+    _need(isinstance(cu_seqlens, torch.Tensor) and
+          cu_seqlens.dtype in (torch.int32, torch.int64), TypeError,
+          "cu_seqlens must be an int32 or int64 tensor")
+    _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1, ValueError,
+          "cu_seqlens must be 1-D [N + 1]")
+    _need(x.shape[0] == 1, ValueError, "a packed batch (cu_seqlens) needs B == 1")
+    return cu_seqlens.to(torch.int32).contiguous(), cu_seqlens.numel() - 1
+
+
+def _workspace(desc, need, workspace, device):
+    """Points the descriptor at the caller's workspace, or at a new one; returns it."""
+    import torch
+    if workspace is not None:
+        _need(isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and
+              workspace.is_contiguous(), TypeError,
+              "workspace must be a contiguous uint8 tensor")
+    if need:
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty(need, device=device, dtype=torch.uint8)
+        desc.workspace = workspace.data_ptr()
+        desc.workspace_bytes = workspace.numel()
+    return workspace
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
+                   initial_state=None, output_final_state=True, cu_seqlens=None,
+                   workspace=None):
+    """The selective scan on the current stream: per channel c and state s,
+    h = exp(step A) h + step x B, y = (sum_s C h + D x) silu(z), step = dt + dt_bias, through
+    softplus when ``dt_softplus``.
+
+    x, dt, z: [B, T, channels] (bf16 or fp32; z None: no gate); A [channels, dstate] fp32;
+    B, C: [B, T, groups, dstate], shared by channels / groups channels each; D, dt_bias
+    [channels] fp32 or None; initial_state [N, channels, dstate] fp32 or None; cu_seqlens
+    [N + 1] for a packed batch (B == 1).  Returns (y in x's dtype, final state fp32 or None)."""
+    import torch
+    desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 2)
+    cu, N = _sequences(x, cu_seqlens)
+    h0 = _f32("initial_state", initial_state, (N, desc.channels, desc.dstate))
+    dev = x.device
+    _check_devices(dict(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
+                        initial_state=h0, cu_seqlens=cu, workspace=workspace), dev)
+    desc.B, desc.T, desc.N, desc.dt_softplus = x.shape[0], x.shape[1], N, int(bool(dt_softplus))
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    ht = None
+    if output_final_state:
+        ht = torch.empty((N, desc.channels, desc.dstate), device=dev, dtype=torch.float32)
+    if x.shape[0] == 0:
+        return y, ht
+    ws = _workspace(desc, gdn_selective_scan_workspace_size(desc), workspace, dev)  # noqa: F841
+    st = gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, y, ht)
+    if st != 0:
+        raise GdnError(st, "gdn_selective_scan_fwd")
+    return y, ht
+
+
+def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
+                           dt_softplus=False, cache_indices=None, out_indices=None):
+    """One token of each sequence: the selective scan's step on the current stream.
+
+    state: [lines, channels, dstate] fp32, contiguous, updated in place; x, dt, z:
+    [B, channels]; B, C: [B, groups, dstate]; the rest as for selective_scan.  Sequence b reads
+    line cache_indices[b] (b when None) and writes line out_indices[b] (the line it read when
+    None).  Returns y [B, channels] in x's dtype."""
+    import torch
+    desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 1)
+    n = x.shape[0]
+    _need(isinstance(state, torch.Tensor) and state.dtype == torch.float32 and
+          state.is_contiguous(), TypeError, "state must be a contiguous fp32 tensor")
+    _need(state.dim() == 3 and state.shape[0] > 0 and
+          tuple(state.shape[1:]) == (desc.channels, desc.dstate), ValueError,
+          "state must be [lines, %d, %d], got %s" % (desc.channels, desc.dstate,
+                                                     list(state.shape)))
+    read, write = _indices("cache_indices", cache_indices, n), _indices("out_indices",
+                                                                        out_indices, n)
+    _need(read is not None or state.shape[0] >= n, ValueError,
+          "state has fewer lines (%d) than there are sequences (%d)" % (state.shape[0], n))
+    _check_devices(dict(state=state, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
+                        cache_indices=read, out_indices=write), x.device)
+    y = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    if n == 0:
+        return y
+    desc.B, desc.T, desc.N, desc.dt_softplus = n, 1, n, int(bool(dt_softplus))
+    desc.state_lines = state.shape[0]
+    st = gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, read, write, y)
+    if st != 0:
+        raise GdnError(st, "gdn_selective_state_update")
+    return y

@@ -184,6 +184,66 @@ gdn_status gdn_causal_conv1d_fwd(const gdn_conv_desc* d, const void* x, const fl
                                  const int32_t* has_initial_state, const int32_t* cu_seqlens,
                                  void* y, hipStream_t stream);
 
+/* The selective state-space scan, a linear recurrence with a diagonal state next to the delta
+ * rule's matrix state.  For every sequence n, channel c (of group g = c / (channels / groups))
+ * and state s < dstate, from h = h0[n, c, :] (zero when h0 is NULL), for each token t
+ *
+ *     step  = softplus(dt[t, c] + dt_bias[c])        (dt[t, c] + dt_bias[c] without dt_softplus)
+ *     h[s] <- exp(step A[c, s]) h[s] + step x[t, c] B[t, g, s]
+ *     y[t, c] = (sum_s C[t, g, s] h[s] + D[c] x[t, c]) z sigmoid(z),   z = z[t, c]
+ *
+ * and finally ht[n, c, :] = h.  D NULL is zero, dt_bias NULL is zero, z NULL leaves the gate
+ * out.  Decays, states and sums are fp32 whatever the dtype; y is rounded once.
+ *
+ * Layouts (row-major; a token's row is contiguous, the rows *_stride elements apart, over the
+ * whole [B, T] token axis; 0 = rows one after another):
+ *   x, dt, z   [B, T, channels]         dtype (bf16 or f32)
+ *   Bm, Cm     [B, T, groups, dstate]   dtype
+ *   y          [B, T, channels]         dtype, contiguous
+ *   A          [channels, dstate]       f32 (negative in the intended use)
+ *   D, dt_bias [channels]               f32
+ *   h0, ht     [N, channels, dstate]    f32; cu_seqlens [N + 1] int32 as for gdn_chunk_fwd
+ * Any channels, groups dividing it, dstate 1 .. 256.  Pointers are device pointers aligned to
+ * their element; errors are returned before any launch; nothing is synchronised or allocated.
+ * x, dt, A, Bm, Cm, y are required unless B*T = 0 (A always).  h0 and ht may be the same
+ * buffer.  Few or long sequences are split into chunks that run in parallel, so results depend
+ * on the descriptor in their last bits, never on scheduling. */
+typedef struct gdn_scan_desc {
+  int32_t B, T;         /* dense [B, T, ...]; packed: B = 1, T = total tokens               */
+  int32_t N;            /* sequences: B (or 0) for a dense batch, len(cu_seqlens) - 1       */
+  int32_t channels;
+  int32_t groups;       /* groups of channels that share B and C                            */
+  int32_t dstate;       /* states a channel                                                 */
+  int32_t dtype;        /* gdn_dtype of x, dt, z, Bm, Cm, y (and of their gradients)        */
+  int32_t dt_softplus;  /* 0 or 1                                                           */
+  int32_t state_lines;  /* gdn_selective_state_update only: lines of the pool               */
+  int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+  void* workspace;      /* 256-byte aligned, as many bytes as the call's query gives        */
+  size_t workspace_bytes;
+} gdn_scan_desc;
+
+/* Bytes of workspace gdn_selective_scan_fwd needs (dense and packed alike: N other than 0 or B
+ * is a packed batch; B == 1 may be either).  Host-only.  0 and *status set when refused. */
+size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* status);
+
+gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm,
+                                  const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* cu_seqlens, void* y, float* ht,
+                                  hipStream_t stream);
+
+/* The same recurrence for one token of each of d->B sequences (T is 1, N is 0 or B), the states
+ * in a pool: sequence b reads line cache_indices[b] (b when NULL) of state [state_lines,
+ * channels, dstate] and writes line out_indices[b] (the line it read when NULL).  A line read
+ * from outside the pool is a zero start, one written outside it is dropped.  A line that one
+ * sequence writes and another reads or writes in the same call has unspecified contents.  No
+ * workspace. */
+gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, const void* x,
+                                      const void* dt, const float* A, const void* Bm,
+                                      const void* Cm, const float* D, const void* z,
+                                      const float* dt_bias, const int32_t* cache_indices,
+                                      const int32_t* out_indices, void* y, hipStream_t stream);
+
 /* Bytes of workspace the variant chosen by d->variant needs (for AUTO, what AUTO picks when
  * given that much).  The fused variant needs none on a dense batch; on a packed batch of
  * 2 .. 65536 sequences it asks for 4 bytes per sequence (256-byte aligned) to run them

@@ -32,7 +32,9 @@ __all__ = [
     "chunk_gated_delta_rule_bwd",
     "GdnConvDesc", "gdn_causal_conv1d_fwd", "causal_conv1d", "ACTIVATIONS",
     "GdnScanDesc", "gdn_selective_scan_fwd", "gdn_selective_scan_workspace_size",
-    "gdn_selective_state_update", "selective_scan", "selective_state_update",
+    "gdn_selective_scan_bwd", "gdn_selective_scan_bwd_workspace_size",
+    "gdn_selective_state_update", "selective_scan", "selective_scan_bwd",
+    "selective_state_update",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -570,6 +572,7 @@ def causal_conv1d(x, weight, bias=None, conv_state=None, cache_indices=None,
 
 # the selective state-space calls (they use the helpers above)
 from . import ssm  # noqa: E402
-from .ssm import (GdnScanDesc, gdn_selective_scan_fwd,  # noqa: E402
+from .ssm import (GdnScanDesc, gdn_selective_scan_bwd,  # noqa: E402
+                  gdn_selective_scan_bwd_workspace_size, gdn_selective_scan_fwd,
                   gdn_selective_scan_workspace_size, gdn_selective_state_update,
-                  selective_scan, selective_state_update)
+                  selective_scan, selective_scan_bwd, selective_state_update)

@@ -29,7 +29,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["api.cpp", "stages.hip", "fused.hip", "segment.hip", "recurrent.hip", "conv1d.hip",
-           "noalloc.hip", "backward.hip", "api_ssm.cpp", "scan.hip", "scan_step.hip"]
+           "noalloc.hip", "backward.hip", "api_ssm.cpp", "scan.hip",
+           "scan_bwd.hip", "scan_step.hip"]
 ARCH = "gfx950"
 
 

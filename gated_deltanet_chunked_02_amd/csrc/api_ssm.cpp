@@ -98,6 +98,44 @@ ScanLayout scan_layout(const gdn::ScanProblem& p) {
   return L;
 }
 
+// The backward's plan: chunks of kBwdChunk tokens and blocks of 16 states.  A packed batch has
+// more slots than sequences unless it is empty, so it is composed even when no sequence is long.
+void plan_bwd(gdn::ScanProblem* p, bool packed) {
+  p->ns = 4;
+  p->nw = p->S <= 4 ? 1 : p->S <= 8 ? 2 : 4;
+  const int block = p->ns * p->nw;
+  p->Sp = (p->S + block - 1) / block * block;
+  p->Lc = gdn::kBwdChunk;
+  p->slots = p->N == 0 ? 0
+             : packed  ? p->Ttot / p->Lc + p->N
+                       : p->N * (p->T > p->Lc ? (p->T + p->Lc - 1) / p->Lc : 1);
+}
+
+struct BwdLayout {
+  size_t bc, hst, gst, dsum, bcp, dAp, dvp, total;
+};
+
+BwdLayout bwd_layout(const gdn::ScanProblem& p) {
+  BwdLayout L;
+  size_t o = 0;
+  const size_t rows = align_up((size_t)p.Ttot * p.G * 2 * p.Sp * 4);
+  const size_t states = align_up((size_t)p.slots * p.S * p.C * 4);
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
+    return at;
+  };
+  L.bc = take(rows);
+  L.hst = take(states);
+  L.gst = take(states);
+  L.dsum = take((size_t)p.slots * p.C * 4);
+  L.bcp = take((size_t)p.nblk * p.Ttot * p.G * 2 * p.Sp * 4);
+  L.dAp = take(states);
+  L.dvp = take((size_t)p.slots * 2 * p.C * 4);
+  L.total = o;
+  return L;
+}
+
 bool looks_packed(const gdn_scan_desc* d) { return d && d->N != 0 && d->N != d->B; }
 
 }  // namespace
@@ -160,6 +198,79 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
   p.y = y;
   p.ht = ht;
   return gdn::launch_scan_fwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_desc* d, gdn_status* status) {
+  gdn::ScanProblem p;
+  const bool packed = looks_packed(d);
+  const gdn_status s = check_scan(d, packed, &p);
+  if (status) *status = s;
+  if (s != GDN_OK) return 0;
+  // one dense sequence may also come as a packed batch of one, which never has fewer slots
+  const bool one = !packed && d->B == 1;
+  if (one) p.N = 1;
+  plan_bwd(&p, packed || one);
+  return bwd_layout(p).total;
+}
+
+gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm,
+                                  const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* cu_seqlens, const void* dy,
+                                  const float* dht, void* dx, void* ddt, float* dA, void* dB,
+                                  void* dC, float* dD, void* dz, float* ddt_bias, float* dh0,
+                                  hipStream_t stream) {
+  gdn::ScanProblem p;
+  const gdn_status s = check_scan(d, cu_seqlens != nullptr, &p);
+  if (s != GDN_OK) return s;
+  if (!A || !dA) return GDN_ERR_INVALID_ARG;
+  if (p.Ttot > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dB || !dC || (z && !dz)))
+    return GDN_ERR_INVALID_ARG;
+  const size_t e = p.f32 ? 4 : 2;
+  for (const void* q : {x, dt, Bm, Cm, z, dy, (const void*)dx, (const void*)ddt, (const void*)dB,
+                        (const void*)dC, (const void*)dz})
+    if (!aligned(q, e)) return GDN_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)A, (const void*)D, (const void*)dt_bias, (const void*)h0,
+                        (const void*)cu_seqlens, (const void*)dht, (const void*)dA,
+                        (const void*)dD, (const void*)ddt_bias, (const void*)dh0})
+    if (!aligned(q, 4)) return GDN_ERR_INVALID_ARG;
+  plan_bwd(&p, cu_seqlens != nullptr);
+  const BwdLayout L = bwd_layout(p);
+  if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
+                      !aligned(d->workspace, kAlign)))
+    return GDN_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(d->workspace);
+  auto at = [ws](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  p.bc = at(L.bc);
+  p.hst = at(L.hst);
+  p.dsum = at(L.dsum);
+  p.x = x;
+  p.dt = dt;
+  p.z = z;
+  p.Bm = Bm;
+  p.Cm = Cm;
+  p.A = A;
+  p.D = D;
+  p.bias = dt_bias;
+  p.h0 = h0;
+  p.cu = cu_seqlens;
+  gdn::ScanBwd b;
+  b.dy = dy;
+  b.dht = dht;
+  b.gst = at(L.gst);
+  b.bcp = at(L.bcp);
+  b.dAp = at(L.dAp);
+  b.dvp = at(L.dvp);
+  b.dx = dx;
+  b.ddt = ddt;
+  b.dz = dz;
+  b.dB = dB;
+  b.dC = dC;
+  b.dA = dA;
+  b.dD = dD;
+  b.dbias = ddt_bias;
+  b.dh0 = dh0;
+  return gdn::launch_scan_bwd(p, b, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, const void* x,

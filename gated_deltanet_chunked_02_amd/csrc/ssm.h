@@ -47,6 +47,28 @@ hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t st);
 // B and C as padded fp32 rows (p.bc).
 hipError_t launch_scan_pack(const ScanProblem& p, hipStream_t st);
 
+// Backward: the same problem at chunks of kBwdChunk tokens, nw waves of 4 states (blocks of 16
+// states one after another when there are more), plus the gradients.
+constexpr int kBwdChunk = 64;
+struct ScanBwd {
+  const void* dy;
+  const float* dht;  // or null
+  float* gst;        // workspace, as the kernels' arguments
+  float* bcp;
+  float* dAp;
+  float* dvp;
+  void* dx;
+  void* ddt;
+  void* dz;          // null without z
+  void* dB;
+  void* dC;
+  float* dA;
+  float* dD;         // or null
+  float* dbias;      // or null
+  float* dh0;        // or null
+};
+hipError_t launch_scan_bwd(const ScanProblem& p, const ScanBwd& b, hipStream_t st);
+
 struct ScanStepProblem {
   int B, C, G, S, per, lines;
   bool f32, softplus;

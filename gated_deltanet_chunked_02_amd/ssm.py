@@ -2,6 +2,7 @@
 
     y, ht = selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
                            initial_state=None, output_final_state=True, cu_seqlens=None)
+    dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0 = selective_scan_bwd(x, dt, A, B, C, dy, ...)
     y = selective_state_update(state, x, dt, A, B, C, ..., cache_indices=None,
                                out_indices=None)
 
@@ -36,6 +37,10 @@ def declare(lib):
     lib.gdn_selective_scan_workspace_size.argtypes = [D, st]
     lib.gdn_selective_scan_fwd.restype = ctypes.c_int
     lib.gdn_selective_scan_fwd.argtypes = [D] + [P] * 13
+    lib.gdn_selective_scan_bwd_workspace_size.restype = S
+    lib.gdn_selective_scan_bwd_workspace_size.argtypes = [D, st]
+    lib.gdn_selective_scan_bwd.restype = ctypes.c_int
+    lib.gdn_selective_scan_bwd.argtypes = [D] + [P] * 22
     lib.gdn_selective_state_update.restype = ctypes.c_int
     lib.gdn_selective_state_update.argtypes = [D] + [P] * 13
 
@@ -60,6 +65,23 @@ def gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_selective_scan_fwd(
         ctypes.byref(desc), *map(_ptr, (x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, y, ht)),
+        _stream(stream)))
+
+
+def gdn_selective_scan_bwd_workspace_size(desc: GdnScanDesc) -> int:
+    st = ctypes.c_int(0)
+    n = load().gdn_selective_scan_bwd_workspace_size(ctypes.byref(desc), ctypes.byref(st))
+    if st.value != 0:
+        raise GdnError(st.value, "gdn_selective_scan_bwd_workspace_size")
+    return int(n)
+
+
+def gdn_selective_scan_bwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dy, dht, dx, ddt,
+                           dA, dB, dC, dD, dz, ddt_bias, dh0, stream=None) -> int:
+    """Raw call (tensors, integer device addresses or None); returns the status code."""
+    return int(load().gdn_selective_scan_bwd(
+        ctypes.byref(desc), *map(_ptr, (x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dy, dht,
+                                        dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0)),
         _stream(stream)))
 
 
@@ -231,6 +253,42 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_fwd")
     return y, ht
+
+
+def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=False,
+                       initial_state=None, dht=None, cu_seqlens=None, workspace=None):
+    """Gradients of selective_scan's inputs on the current stream, given the gradient ``dy`` of y
+    (x's shape and dtype) and ``dht`` of the final state (fp32, or None: zero); the forward's
+    inputs as there.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinitial_state): dx, ddt,
+    dz, dB, dC in x's dtype, the others in fp32, None where the input is None."""
+    import torch
+    desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 2)
+    cu, N = _sequences(x, cu_seqlens)
+    states = (N, desc.channels, desc.dstate)
+    h0, dht = _f32("initial_state", initial_state, states), _f32("dht", dht, states)
+    _need(isinstance(dy, torch.Tensor) and dy.dtype == x.dtype, TypeError,
+          "dy must be a tensor of x's dtype %s" % x.dtype)
+    _need(dy.shape == x.shape, ValueError, "dy must have x's shape %s" % list(x.shape))
+    dev = x.device
+    _check_devices(dict(x=x, dt=dt, A=A, B=B, C=C, dy=dy, D=D, z=z, dt_bias=dt_bias,
+                        initial_state=h0, dht=dht, cu_seqlens=cu, workspace=workspace), dev)
+    dy = dy.contiguous()
+    desc.B, desc.T, desc.N, desc.dt_softplus = x.shape[0], x.shape[1], N, int(bool(dt_softplus))
+    new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)  # noqa: E731
+    dx, ddt, dA, dB, dC, dD, dz, dbias, dh0 = map(new, (x, dt, A, B, C, D, z, dt_bias, h0))
+    if x.shape[0] == 0:
+        return dx, ddt, dA.zero_(), dB, dC, _zero(dD), dz, _zero(dbias), dh0
+    need = gdn_selective_scan_bwd_workspace_size(desc)
+    ws = _workspace(desc, need, workspace, dev)  # noqa: F841
+    st = gdn_selective_scan_bwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, dy, dht, dx, ddt, dA,
+                                dB, dC, dD, dz, dbias, dh0)
+    if st != 0:
+        raise GdnError(st, "gdn_selective_scan_bwd")
+    return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
+
+
+def _zero(t):
+    return None if t is None else t.zero_()
 
 
 def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,

@@ -232,6 +232,28 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
                                   const float* h0, const int32_t* cu_seqlens, void* y, float* ht,
                                   hipStream_t stream);
 
+/* Bytes of workspace gdn_selective_scan_bwd needs.  Host-only. */
+size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_desc* d, gdn_status* status);
+
+/* The gradient of gdn_selective_scan_fwd: the exact derivative of the recurrence, from the
+ * forward's inputs (nothing of a forward call is kept) and the gradients of its outputs.
+ *   dy                 [B, T, channels] dtype, contiguous
+ *   dht                [N, channels, dstate] f32, or NULL (zero)
+ *   dx, ddt, dz        [B, T, channels] dtype, contiguous (dz required with z)
+ *   dB, dC             [B, T, groups, dstate] dtype, contiguous: summed over the channels that
+ *                      share them in fp32, rounded once
+ *   dA [channels, dstate], dD, ddt_bias [channels], dh0 [N, channels, dstate]  f32; dD, ddt_bias
+ *                      and dh0 may be NULL (not written)
+ * Sums are made in a fixed order (no atomics): the same call gives the same bits.  Gradients of
+ * tokens of a packed batch that no sequence has are unspecified. */
+gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm,
+                                  const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* cu_seqlens, const void* dy,
+                                  const float* dht, void* dx, void* ddt, float* dA, void* dB,
+                                  void* dC, float* dD, void* dz, float* ddt_bias, float* dh0,
+                                  hipStream_t stream);
+
 /* The same recurrence for one token of each of d->B sequences (T is 1, N is 0 or B), the states
  * in a pool: sequence b reads line cache_indices[b] (b when NULL) of state [state_lines,
  * channels, dstate] and writes line out_indices[b] (the line it read when NULL).  A line read

@@ -34,7 +34,9 @@ __all__ = [
     "GdnScanDesc", "gdn_selective_scan_fwd", "gdn_selective_scan_workspace_size",
     "gdn_selective_scan_bwd", "gdn_selective_scan_bwd_workspace_size",
     "gdn_selective_state_update", "selective_scan", "selective_scan_bwd",
-    "selective_state_update",
+    "selective_state_update", "gdn_causal_conv1d_bwd", "gdn_causal_conv1d_bwd_workspace_size",
+    "causal_conv1d_bwd", "GdnNormDesc", "gdn_group_norm_fwd", "gdn_group_norm_bwd",
+    "gdn_group_norm_workspace_size", "group_norm", "group_norm_bwd",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -570,9 +572,12 @@ def causal_conv1d(x, weight, bias=None, conv_state=None, cache_indices=None,
     return y
 
 
-# the selective state-space calls (they use the helpers above)
+# the selective state-space layer's calls (they use the helpers above)
 from . import ssm  # noqa: E402
-from .ssm import (GdnScanDesc, gdn_selective_scan_bwd,  # noqa: E402
-                  gdn_selective_scan_bwd_workspace_size, gdn_selective_scan_fwd,
-                  gdn_selective_scan_workspace_size, gdn_selective_state_update,
-                  selective_scan, selective_scan_bwd, selective_state_update)
+from .ssm import (  # noqa: E402
+    GdnNormDesc, GdnScanDesc, causal_conv1d_bwd, gdn_causal_conv1d_bwd,
+    gdn_causal_conv1d_bwd_workspace_size, gdn_group_norm_bwd, gdn_group_norm_fwd,
+    gdn_group_norm_workspace_size, gdn_selective_scan_bwd,
+    gdn_selective_scan_bwd_workspace_size, gdn_selective_scan_fwd,
+    gdn_selective_scan_workspace_size, gdn_selective_state_update, group_norm, group_norm_bwd,
+    selective_scan, selective_scan_bwd, selective_state_update)

@@ -30,7 +30,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["api.cpp", "stages.hip", "fused.hip", "segment.hip", "recurrent.hip", "conv1d.hip",
            "noalloc.hip", "backward.hip", "api_ssm.cpp", "scan.hip",
-           "scan_bwd.hip", "scan_step.hip"]
+           "scan_bwd.hip", "scan_step.hip", "conv1d_bwd.hip", "group_norm.hip"]
 ARCH = "gfx950"
 
 

@@ -1,9 +1,11 @@
-// C ABI of the selective state-space calls (declared in include/gdn.h): host-side validation,
+// C ABI of the selective state-space layer's calls (the scan, the convolution's backward, the
+// group norm; declared in include/gdn.h): host-side validation,
 // workspace layout and dispatch to the launchers.  No allocation, no synchronisation.
 #include <stdint.h>
 #include <string.h>
 
 #include "gdn.h"
+#include "norm.h"
 #include "ssm.h"
 
 namespace {
@@ -134,6 +136,70 @@ BwdLayout bwd_layout(const gdn::ScanProblem& p) {
   L.dvp = take((size_t)p.slots * 2 * p.C * 4);
   L.total = o;
   return L;
+}
+
+// Token blocks of the convolution's backward: the longest power of two up to 256 tokens that
+// still gives 1024 workgroups (a block costs W - 1 tokens more of reading and a row of partial
+// sums), at least 8.
+void plan_conv_bwd(gdn::ConvBwdProblem* p) {
+  const long long slabs = (p->C / 8 + 255) / 256;
+  p->tokens = 256;
+  while (p->tokens > 8 && (p->Ttot + p->tokens - 1LL) / p->tokens * slabs < 1024)
+    p->tokens >>= 1;
+  p->blocks = (p->Ttot + p->tokens - 1) / p->tokens;
+}
+
+gdn_status check_conv_bwd(const gdn_conv_desc* d, bool packed, gdn::ConvBwdProblem* p) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->B < 1 || d->T < 0 || d->N < 0 || d->channels < 1) return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (d->activation != GDN_ACT_NONE && d->activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
+  if (packed ? d->B != 1 : (d->N != 0 && d->N != d->B)) return GDN_ERR_INVALID_ARG;
+  if (d->width < 2 || d->width > 4 || d->channels % 8 != 0) return GDN_ERR_UNSUPPORTED;
+  const long long Ttot = (long long)d->B * d->T;
+  if (Ttot > (1LL << 30) || (long long)d->channels * 8 > (1LL << 30) || d->N > (1 << 24))
+    return GDN_ERR_UNSUPPORTED;
+  memset(p, 0, sizeof(*p));
+  p->T = d->T;
+  p->Ttot = (int)Ttot;
+  p->N = packed ? d->N : d->B;
+  p->C = d->channels;
+  p->W = d->width;
+  p->f32 = d->dtype == GDN_F32;
+  p->silu = d->activation == GDN_ACT_SILU;
+  plan_conv_bwd(p);
+  if ((long long)p->N * (p->C / 8) >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+gdn_status check_norm(const gdn_norm_desc* d, gdn::NormProblem* p) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->samples < 0 || d->positions < 0 || d->channels < 1 || d->groups < 1 ||
+      d->channels % d->groups != 0 || !(d->eps >= 0.f))
+    return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (d->activation != GDN_ACT_NONE && d->activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
+  // grids of a workgroup for each (sample, group) and for each (sample, piece of a map)
+  if ((long long)d->samples * d->groups > (1 << 23) || d->channels > (1 << 20))
+    return GDN_ERR_UNSUPPORTED;
+  memset(p, 0, sizeof(*p));
+  p->N = d->samples;
+  p->P = d->positions;
+  p->C = d->channels;
+  p->G = d->groups;
+  p->cpg = p->C / p->G;
+  p->f32 = d->dtype == GDN_F32;
+  p->silu = d->activation == GDN_ACT_SILU;
+  p->eps = d->eps;
+  return GDN_OK;
+}
+
+gdn_status norm_space(const gdn_norm_desc* d, bool backward, gdn::NormProblem* p) {
+  const size_t need = gdn::norm_workspace(*p, backward);
+  if (need > 0 && (!d->workspace || d->workspace_bytes < need || !aligned(d->workspace, kAlign)))
+    return GDN_ERR_WORKSPACE;
+  p->ws = static_cast<float*>(d->workspace);
+  return GDN_OK;
 }
 
 bool looks_packed(const gdn_scan_desc* d) { return d && d->N != 0 && d->N != d->B; }
@@ -317,6 +383,116 @@ gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, cons
   q.sc = p.sc;
   q.y = y;
   return gdn::launch_scan_step(q, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_causal_conv1d_bwd_workspace_size(const gdn_conv_desc* d, gdn_status* status) {
+  gdn::ConvBwdProblem p;
+  const gdn_status s = check_conv_bwd(d, d && d->N != 0 && d->N != d->B, &p);
+  if (status) *status = s;
+  return s == GDN_OK ? align_up((size_t)p.blocks * (p.W + 1) * p.C * 4) : 0;
+}
+
+gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const float* weight,
+                                 const float* bias, const void* initial,
+                                 const int32_t* cu_seqlens, const void* dy, const void* dfinal,
+                                 void* dx, float* dweight, float* dbias, void* dinitial,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  gdn::ConvBwdProblem p;
+  const gdn_status s = check_conv_bwd(d, cu_seqlens != nullptr, &p);
+  if (s != GDN_OK) return s;
+  if (!weight || (p.Ttot > 0 && (!x || !dy || !dx))) return GDN_ERR_INVALID_ARG;
+  for (const void* q : {x, initial, dy, dfinal, (const void*)dx, (const void*)dinitial})
+    if (!aligned(q, 16)) return GDN_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)weight, (const void*)bias, (const void*)cu_seqlens,
+                        (const void*)dweight, (const void*)dbias})
+    if (!aligned(q, 4)) return GDN_ERR_INVALID_ARG;
+  if (p.N == 0) {
+    p.blocks = 0;  // no sequence has a token: the parameters' gradients are zero
+    dinitial = nullptr;
+  }
+  const size_t need = align_up((size_t)p.blocks * (p.W + 1) * p.C * 4);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, kAlign)))
+    return GDN_ERR_WORKSPACE;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.init = initial;
+  p.cu = cu_seqlens;
+  p.dy = dy;
+  p.dfinal = dfinal;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.dinit = dinitial;
+  p.part = static_cast<float*>(workspace);
+  return gdn::launch_conv1d_bwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_group_norm_workspace_size(const gdn_norm_desc* d, int32_t backward,
+                                     gdn_status* status) {
+  gdn::NormProblem p;
+  const gdn_status s = check_norm(d, &p);
+  if (status) *status = s;
+  if (s != GDN_OK || p.N == 0 || p.P == 0) return 0;
+  return gdn::norm_workspace(p, backward != 0);
+}
+
+gdn_status gdn_group_norm_fwd(const gdn_norm_desc* d, const void* x, const float* weight,
+                              const float* bias, const void* gate, void* y, float* mean,
+                              float* rstd, hipStream_t stream) {
+  gdn::NormProblem p;
+  gdn_status s = check_norm(d, &p);
+  if (s != GDN_OK) return s;
+  if (p.N == 0 || p.P == 0) return GDN_OK;
+  if (!x || !y) return GDN_ERR_INVALID_ARG;
+  const size_t e = p.f32 ? 4 : 2;
+  if (!aligned(x, e) || !aligned(gate, e) || !aligned(y, e) || !aligned(weight, 4) ||
+      !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return GDN_ERR_INVALID_ARG;
+  s = norm_space(d, false, &p);
+  if (s != GDN_OK) return s;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.gate = gate;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  return gdn::launch_norm_fwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+gdn_status gdn_group_norm_bwd(const gdn_norm_desc* d, const void* x, const float* weight,
+                              const float* bias, const void* gate, const float* mean,
+                              const float* rstd, const void* dy, void* dx, float* dweight,
+                              float* dbias, void* dgate, hipStream_t stream) {
+  gdn::NormProblem p;
+  gdn_status s = check_norm(d, &p);
+  if (s != GDN_OK) return s;
+  const bool empty = p.N == 0 || p.P == 0;
+  if (!empty && (!x || !mean || !rstd || !dy || !dx || (gate && !dgate)))
+    return GDN_ERR_INVALID_ARG;
+  const size_t e = p.f32 ? 4 : 2;
+  for (const void* q : {x, gate, dy, (const void*)dx, (const void*)dgate})
+    if (!aligned(q, e)) return GDN_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)weight, (const void*)bias, (const void*)mean,
+                        (const void*)rstd, (const void*)dweight, (const void*)dbias})
+    if (!aligned(q, 4)) return GDN_ERR_INVALID_ARG;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  if (empty)
+    return gdn::launch_norm_no_params(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+  s = norm_space(d, true, &p);
+  if (s != GDN_OK) return s;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.gate = gate;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.dy = dy;
+  p.dx = dx;
+  p.dgate = dgate;
+  return gdn::launch_norm_bwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 }  // extern "C"

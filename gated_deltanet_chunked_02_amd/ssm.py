@@ -1,10 +1,15 @@
-"""Binding of libgdn's selective state-space calls: argument checks and marshalling only.
+"""Binding of libgdn's calls for a selective state-space layer: argument checks and marshalling
+only.
 
     y, ht = selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
                            initial_state=None, output_final_state=True, cu_seqlens=None)
     dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0 = selective_scan_bwd(x, dt, A, B, C, dy, ...)
     y = selective_state_update(state, x, dt, A, B, C, ..., cache_indices=None,
                                out_indices=None)
+    dx, dweight, dbias, dinitial = causal_conv1d_bwd(x, weight, dy, bias=None, ...)
+    y, mean, rstd = group_norm(x, num_groups, weight=None, bias=None, eps=1e-5,
+                               activation=None, gate=None)
+    dx, dweight, dbias, dgate = group_norm_bwd(dy, x, num_groups, mean, rstd, ...)
 
 Tensors whose token rows are contiguous and evenly spaced (a slice of a projection's last axis)
 are passed as they are; others are copied first.
@@ -13,7 +18,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import BF16, F32, GdnError, _check_devices, _need, _ptr, load
+from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _need, _ptr,
+               _validate_conv, load)
 
 _FLOATS = None  # filled on first use: importing torch is left to the first call
 
@@ -26,6 +32,14 @@ class GdnScanDesc(ctypes.Structure):
                 ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
                 ("z_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
                 ("c_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GdnNormDesc(ctypes.Structure):
+    _fields_ = [("samples", ctypes.c_int32), ("positions", ctypes.c_int32),
+                ("channels", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -43,6 +57,18 @@ def declare(lib):
     lib.gdn_selective_scan_bwd.argtypes = [D] + [P] * 22
     lib.gdn_selective_state_update.restype = ctypes.c_int
     lib.gdn_selective_state_update.argtypes = [D] + [P] * 13
+    V = ctypes.POINTER(GdnConvDesc)
+    lib.gdn_causal_conv1d_bwd_workspace_size.restype = S
+    lib.gdn_causal_conv1d_bwd_workspace_size.argtypes = [V, st]
+    lib.gdn_causal_conv1d_bwd.restype = ctypes.c_int
+    lib.gdn_causal_conv1d_bwd.argtypes = [V] + [P] * 12 + [S, P]
+    M = ctypes.POINTER(GdnNormDesc)
+    lib.gdn_group_norm_workspace_size.restype = S
+    lib.gdn_group_norm_workspace_size.argtypes = [M, ctypes.c_int32, st]
+    lib.gdn_group_norm_fwd.restype = ctypes.c_int
+    lib.gdn_group_norm_fwd.argtypes = [M] + [P] * 8
+    lib.gdn_group_norm_bwd.restype = ctypes.c_int
+    lib.gdn_group_norm_bwd.argtypes = [M] + [P] * 12
 
 
 def _stream(stream):
@@ -323,3 +349,170 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     if st != 0:
         raise GdnError(st, "gdn_selective_state_update")
     return y
+
+
+def gdn_causal_conv1d_bwd_workspace_size(desc: GdnConvDesc) -> int:
+    st = ctypes.c_int(0)
+    n = load().gdn_causal_conv1d_bwd_workspace_size(ctypes.byref(desc), ctypes.byref(st))
+    if st.value != 0:
+        raise GdnError(st.value, "gdn_causal_conv1d_bwd_workspace_size")
+    return int(n)
+
+
+def gdn_causal_conv1d_bwd(desc, x, weight, bias, initial, cu_seqlens, dy, dfinal, dx, dweight,
+                          dbias, dinitial, workspace, workspace_bytes, stream=None) -> int:
+    """Raw call (tensors, integer device addresses or None); returns the status code."""
+    return int(load().gdn_causal_conv1d_bwd(
+        ctypes.byref(desc), *map(_ptr, (x, weight, bias, initial, cu_seqlens, dy, dfinal, dx,
+                                        dweight, dbias, dinitial, workspace)), workspace_bytes,
+        _stream(stream)))
+
+
+def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state=None,
+                      cu_seqlens=None, activation=None, workspace=None):
+    """Gradients of causal_conv1d's inputs on the current stream, given ``dy`` [B, T, C] and
+    ``dfinal_state`` [N, W - 1, C] of the state lines afterwards (None: zero).  initial_state
+    [N, W - 1, C]: the inputs before each sequence, its line before the forward (None: zeros).
+    Returns (dx in x's dtype, dweight [C, W] and dbias [C] fp32, dinitial_state in x's dtype);
+    dbias and dinitial_state are None where the input is None."""
+    import torch
+    _validate_conv(x, weight, bias, None, None, None, cu_seqlens)
+    _need(activation in ACTIVATIONS, ValueError, "activation must be None, 'none' or 'silu'")
+    B, T, C = x.shape
+    W = weight.shape[1]
+    cu, N = _sequences(x, cu_seqlens)
+    _need(isinstance(dy, torch.Tensor) and dy.dtype == x.dtype, TypeError,
+          "dy must be a tensor of x's dtype %s" % x.dtype)
+    _need(dy.shape == x.shape, ValueError, "dy must have x's shape %s" % list(x.shape))
+    lines = dict(initial_state=initial_state, dfinal_state=dfinal_state)
+    for name, t in lines.items():
+        if t is not None:
+            _need(isinstance(t, torch.Tensor) and t.dtype == x.dtype, TypeError,
+                  "%s must be a tensor of x's dtype %s" % (name, x.dtype))
+            _need(tuple(t.shape) == (N, W - 1, C), ValueError,
+                  "%s must be [N, W - 1, C] = %s" % (name, [N, W - 1, C]))
+            lines[name] = t.contiguous()
+    _check_devices(dict(x=x, dy=dy, workspace=workspace, **lines), x.device)
+    weight, dy = weight.contiguous(), dy.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    desc = GdnConvDesc(B=B, T=T, N=N, channels=C, width=W, dtype=_code(x),
+                       activation=ACTIVATIONS[activation], state_lines=0)
+    dev = x.device
+    dx = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    dweight = torch.empty(weight.shape, device=dev, dtype=torch.float32)
+    dbias = None if bias is None else torch.empty(C, device=dev, dtype=torch.float32)
+    first = lines["initial_state"]
+    dinit = None if first is None else torch.empty(first.shape, device=dev, dtype=x.dtype)
+    if B == 0:
+        return dx, dweight.zero_(), _zero(dbias), dinit
+    need = gdn_causal_conv1d_bwd_workspace_size(desc)
+    ws = _workspace(desc, 0, workspace, dev)
+    if need and (ws is None or ws.numel() < need):
+        ws = torch.empty(need, device=dev, dtype=torch.uint8)
+    st = gdn_causal_conv1d_bwd(desc, x, weight, bias, first, cu, dy, lines["dfinal_state"], dx,
+                               dweight, dbias, dinit, ws, 0 if ws is None else ws.numel())
+    if st != 0:
+        raise GdnError(st, "gdn_causal_conv1d_bwd")
+    return dx, dweight, dbias, dinit
+
+
+def gdn_group_norm_workspace_size(desc: GdnNormDesc, backward=False) -> int:
+    st = ctypes.c_int(0)
+    n = load().gdn_group_norm_workspace_size(ctypes.byref(desc), int(bool(backward)),
+                                             ctypes.byref(st))
+    if st.value != 0:
+        raise GdnError(st.value, "gdn_group_norm_workspace_size")
+    return int(n)
+
+
+def gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, stream=None) -> int:
+    """Raw call (tensors, integer device addresses or None); returns the status code."""
+    return int(load().gdn_group_norm_fwd(
+        ctypes.byref(desc), *map(_ptr, (x, weight, bias, gate, y, mean, rstd)),
+        _stream(stream)))
+
+
+def gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight, dbias, dgate,
+                       stream=None) -> int:
+    """Raw call (tensors, integer device addresses or None); returns the status code."""
+    return int(load().gdn_group_norm_bwd(
+        ctypes.byref(desc), *map(_ptr, (x, weight, bias, gate, mean, rstd, dy, dx, dweight,
+                                        dbias, dgate)), _stream(stream)))
+
+
+def _norm_operands(x, num_groups, weight, bias, eps, activation, gate):
+    import torch
+    _need(isinstance(x, torch.Tensor), TypeError, "x must be a torch tensor")
+    code = _code(x)
+    _need(code is not None, TypeError, "x must be bf16 or fp32, got %s" % x.dtype)
+    _need(x.dim() >= 2 and x.shape[-1] > 0, ValueError,
+          "x must be [samples, channels] or [samples, ..., channels]")
+    _need(activation in ACTIVATIONS, ValueError, "activation must be None, 'none' or 'silu'")
+    C = x.shape[-1]
+    _need(isinstance(num_groups, int) and num_groups > 0 and C % num_groups == 0, ValueError,
+          "num_groups must divide the %d channels, got %r" % (C, num_groups))
+    _need(eps >= 0, ValueError, "eps must not be negative")
+    weight, bias = _f32("weight", weight, (C,)), _f32("bias", bias, (C,))
+    if gate is not None:
+        _need(isinstance(gate, torch.Tensor) and gate.dtype == x.dtype, TypeError,
+              "gate must be a tensor of x's dtype %s" % x.dtype)
+        _need(gate.shape == x.shape, ValueError, "gate must have x's shape %s" % list(x.shape))
+        gate = gate.contiguous()
+    positions = 1
+    for n in x.shape[1:-1]:
+        positions *= n
+    desc = GdnNormDesc(samples=x.shape[0], positions=positions, channels=C, groups=num_groups,
+                       dtype=code, activation=ACTIVATIONS[activation], eps=eps)
+    return desc, x.contiguous(), weight, bias, gate
+
+
+def group_norm(x, num_groups, weight=None, bias=None, eps=1e-5, activation=None, gate=None,
+               workspace=None):
+    """Channels-last group norm with an activation or a gate on the current stream.
+
+    x: [samples, channels] (a token's heads: every row by itself) or [samples, ..., channels]
+    (statistics over a sample's positions and a group's channels), bf16 or fp32; weight, bias
+    [channels] fp32 or None; gate: x's shape and dtype, or None.  y = act(u) without a gate and
+    u act(gate) with one, u the normalised, scaled and shifted x.  Returns (y, mean, rstd), mean
+    and rstd [samples, num_groups] fp32."""
+    import torch
+    desc, x, weight, bias, gate = _norm_operands(x, num_groups, weight, bias, eps, activation,
+                                                 gate)
+    dev = x.device
+    _check_devices(dict(x=x, weight=weight, bias=bias, gate=gate, workspace=workspace), dev)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    mean = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
+    rstd = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
+    ws = _workspace(desc, gdn_group_norm_workspace_size(desc), workspace, dev)  # noqa: F841
+    st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd)
+    if st != 0:
+        raise GdnError(st, "gdn_group_norm_fwd")
+    return y, mean, rstd
+
+
+def group_norm_bwd(dy, x, num_groups, mean, rstd, weight=None, bias=None, activation=None,
+                   gate=None, workspace=None):
+    """Gradients of group_norm's inputs on the current stream, from dy, the forward's inputs and
+    its mean and rstd.  Returns (dx, dweight, dbias, dgate): dx and dgate in x's dtype, dweight
+    and dbias [channels] fp32; None where the input is None."""
+    import torch
+    desc, x, weight, bias, gate = _norm_operands(x, num_groups, weight, bias, 0.0, activation,
+                                                 gate)
+    _need(isinstance(dy, torch.Tensor) and dy.dtype == x.dtype, TypeError,
+          "dy must be a tensor of x's dtype %s" % x.dtype)
+    _need(dy.shape == x.shape, ValueError, "dy must have x's shape %s" % list(x.shape))
+    _need(mean is not None and rstd is not None, TypeError, "mean and rstd are required")
+    mean = _f32("mean", mean, (x.shape[0], num_groups))
+    rstd = _f32("rstd", rstd, (x.shape[0], num_groups))
+    dev = x.device
+    _check_devices(dict(x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate,
+                        workspace=workspace), dev)
+    dy = dy.contiguous()
+    new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)  # noqa: E731
+    dx, dweight, dbias, dgate = map(new, (x, weight, bias, gate))
+    ws = _workspace(desc, gdn_group_norm_workspace_size(desc, True), workspace, dev)  # noqa: F841
+    st = gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight, dbias,
+                            dgate)
+    if st != 0:
+        raise GdnError(st, "gdn_group_norm_bwd")
+    return dx, dweight, dbias, dgate

@@ -1,6 +1,8 @@
 /*
  * libgdn — chunked Gated DeltaNet on AMD Instinct MI355X (gfx950): the forward pass, its
- * backward pass, the decode operator with in-kernel gates and the causal conv1d before it.
+ * backward pass, the decode operator with in-kernel gates and the causal conv1d before it; and
+ * the operators of a selective state-space layer: the scan for prompts, its gradient and its
+ * single-token form, the conv1d's gradient, and the group norm after a mixing layer.
  *
  * The operation (one call): for every sequence n and value head h, with q/k head
  * hk = h / (H / Hg), starting from S = h0[n, h]^T (zero when h0 is NULL), for each token t
@@ -265,6 +267,59 @@ gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, cons
                                       const void* Cm, const float* D, const void* z,
                                       const float* dt_bias, const int32_t* cache_indices,
                                       const int32_t* out_indices, void* y, hipStream_t stream);
+
+/* The gradient of gdn_causal_conv1d_fwd.  With x~ each sequence's inputs behind the W - 1 before
+ * it (initial [N, W - 1, C] dtype: its state line as it was before the forward, or NULL: zeros),
+ * given dy and dfinal, the gradient of the state line afterwards ([N, W - 1, C] dtype, or NULL:
+ * zero), it writes
+ *   dx       [B, T, C]      dtype
+ *   dweight  [C, W], dbias [C]   f32 sums over all tokens (NULL: not written)
+ *   dinitial [N, W - 1, C]  dtype, the gradient of initial (NULL: not written)
+ * d->state_lines is ignored; shapes, checks and the rest as for the forward (x, dy, dx, initial,
+ * dfinal and dinitial 16-byte aligned).  Sums are made in a fixed order.  The workspace (256-byte
+ * aligned, gdn_causal_conv1d_bwd_workspace_size bytes) is required when B*T > 0. */
+size_t gdn_causal_conv1d_bwd_workspace_size(const gdn_conv_desc* d, gdn_status* status);
+
+gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const float* weight,
+                                 const float* bias, const void* initial,
+                                 const int32_t* cu_seqlens, const void* dy, const void* dfinal,
+                                 void* dx, float* dweight, float* dbias, void* dinitial,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Group norm of channels-last data with an activation or a gate: the norm of a token's heads after
+ * a mixing layer (positions = 1), or of a feature map's channel groups.  For sample n and group g
+ * of channels / groups consecutive channels, over the sample's positions and the group's channels,
+ *
+ *   mean = E[x],  rstd = (E[(x - mean)^2] + eps)^-1/2,  u = (x - mean) rstd weight[c] + bias[c]
+ *   y = act(u) without a gate, u act(gate) with one
+ *
+ * x, gate, y [samples, positions, channels] dtype (bf16 or f32), contiguous; weight, bias
+ * [channels] f32 or NULL (ones, zeros); mean, rstd [samples, groups] f32, written unless NULL (the
+ * backward needs them).  Statistics are fp32 sums about the mean.  Any channels, groups dividing
+ * it; pointers aligned to their element (vectors are used where 16 bytes fit). */
+typedef struct gdn_norm_desc {
+  int32_t samples, positions, channels, groups;
+  int32_t dtype;       /* gdn_dtype of x, gate, y, dy, dx, dgate */
+  int32_t activation;  /* gdn_activation */
+  float eps;           /* >= 0 */
+  void* workspace;     /* 256-byte aligned, as many bytes as the query gives (0 for many shapes) */
+  size_t workspace_bytes;
+} gdn_norm_desc;
+
+/* Bytes of workspace of the forward (backward = 0) or the backward (1).  Host-only. */
+size_t gdn_group_norm_workspace_size(const gdn_norm_desc* d, int32_t backward,
+                                     gdn_status* status);
+
+gdn_status gdn_group_norm_fwd(const gdn_norm_desc* d, const void* x, const float* weight,
+                              const float* bias, const void* gate, void* y, float* mean,
+                              float* rstd, hipStream_t stream);
+
+/* Its gradient, from the forward's inputs, mean and rstd, and dy: dx, dgate (with a gate) in
+ * dtype; dweight, dbias [channels] f32 sums over samples and positions (NULL: not written). */
+gdn_status gdn_group_norm_bwd(const gdn_norm_desc* d, const void* x, const float* weight,
+                              const float* bias, const void* gate, const float* mean,
+                              const float* rstd, const void* dy, void* dx, float* dweight,
+                              float* dbias, void* dgate, hipStream_t stream);
 
 /* Bytes of workspace the variant chosen by d->variant needs (for AUTO, what AUTO picks when
  * given that much).  The fused variant needs none on a dense batch; on a packed batch of

@@ -22,6 +22,8 @@ bool stride_ok(int64_t given, int64_t row, int64_t* out) {
   return given == 0 || (given >= row && given <= (int64_t)1 << 40);
 }
 
+constexpr int kLongestTile = 64;  // tokens that a chunk length is a multiple of, at most
+
 // Descriptor checks shared by the entry points; fills the shape part of the problem, for a
 // packed batch (cu_seqlens given) or a dense one.
 gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) {
@@ -54,29 +56,50 @@ gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) 
   if ((long long)p->G * p->nblk > 65535) return GDN_ERR_UNSUPPORTED;
   p->f32 = d->dtype == GDN_F32;
   p->softplus = d->dt_softplus != 0;
-  // the states of 64 channels over the waves of a workgroup: four a lane where that makes at
-  // most four waves, more a lane for larger states
-  p->ns = p->S <= 16 ? 4 : p->S <= 32 ? 8 : 16;
-  p->nw = 1;
-  while (p->nw * p->ns < p->S) p->nw *= 2;
-  p->Sp = p->ns * p->nw;
+  // tokens whose rows lie within 2 GiB of the first one's, for every tensor
+  int64_t row = p->C;
+  for (int64_t v : {p->sx, p->sdt, p->sz})
+    if (v > row) row = v;
+  const int64_t reach = (((int64_t)1 << 31) - 1) / (row * (p->f32 ? 4 : 2)) - 1;
+  if (reach < 4 * kLongestTile) return GDN_ERR_UNSUPPORTED;
+  p->reach = (int)(reach > (1 << 30) ? 1 << 30 : reach / kLongestTile * kLongestTile);
   return GDN_OK;
 }
 
-constexpr int kFillWaves = 4096;  // waves that fill 256 CUs (four a SIMD)
-constexpr int kMinChunk = 64;     // shorter chunks are not worth their states
+// How the forward runs: states a lane and waves a workgroup (ns nw >= dstate), and the chunk
+// length.  Measured with 16 states (workgroups: sequences times 64-channel blocks):
+//   * from one workgroup a CU on, whole sequences are quicker than chunks, which cost a second
+//     pass: 8 x 2048 tokens of 4096 channels take 339 us whole and 483 us in chunks of 256; 2
+//     states a lane then give the waves that 4 would not (339 against 365 us).  A packed batch
+//     is split at twice its mean length, so that one long sequence does not run alone;
+//   * below that the sequences are split into chunks that fill the GPU, at least 128 tokens
+//     long: 1 x 8192 tokens take 735 us whole, 272 us in chunks of 256 (281 at 512, 291 at 128).
+constexpr int kUnits = 256;        // CUs
+constexpr int kFillWaves = 8192;   // waves wanted of a split batch
+constexpr int kMinChunk = 128;
 
-// Chunk length: whole sequences when their (sequence, channel block) pairs fill the GPU, else
-// chunks short enough that they do.
-void plan_chunks(gdn::ScanProblem* p, bool packed) {
-  const long long per_seq = (long long)p->G * p->nblk * p->nw;  // waves of one chunk
-  const long long want = (kFillWaves + per_seq - 1) / per_seq;  // chunks wanted in all
+void plan_fwd(gdn::ScanProblem* p, bool packed) {
+  const long long blocks = (long long)p->G * p->nblk;
+  const bool whole = p->N * blocks >= kUnits;
+  p->ns = p->S <= 8 || (whole && p->S <= 16) ? 2 : p->S <= 32 ? 4 : p->S <= 128 ? 8 : 16;
+  p->nw = p->ns == 2 ? 2 : p->ns == 16 ? 16 : 4;
+  while (p->nw * p->ns < p->S) p->nw *= 2;
+  p->Sp = p->ns * p->nw;
   p->Lc = gdn::kScanNoSplit;
-  if (p->N > 0 && p->Ttot > 0 && p->N < (packed ? 4 * want : want)) {
-    long long L = (p->Ttot + want - 1) / want;
+  if (p->N > 0 && p->Ttot > 0) {
+    const long long longest = packed ? p->Ttot : p->T;
+    long long L = longest;
+    if (!whole) {
+      const long long chunks = (kFillWaves + blocks * p->nw - 1) / (blocks * p->nw);
+      L = (p->Ttot + chunks - 1) / chunks;
+    } else if (packed) {
+      L = 2LL * ((p->Ttot + p->N - 1) / p->N);
+    }
     L = (L + gdn::kScanTile - 1) / gdn::kScanTile * gdn::kScanTile;
     if (L < kMinChunk) L = kMinChunk;
-    if (L < (packed ? p->Ttot : p->T)) p->Lc = (int)L;
+    // a chunk's rows are reached with 31-bit offsets
+    if (L > p->reach) L = p->reach;
+    if (2 * L <= longest || longest > p->reach) p->Lc = (int)L;
   }
   p->slots = packed ? p->Ttot / p->Lc + p->N
                     : p->N * (int)(p->T > p->Lc ? ((long long)p->T + p->Lc - 1) / p->Lc : 1);
@@ -214,13 +237,13 @@ size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* sta
   const gdn_status s = check_scan(d, packed, &p);
   if (status) *status = s;
   if (s != GDN_OK) return 0;
-  plan_chunks(&p, packed);
+  plan_fwd(&p, packed);
   size_t need = scan_layout(p).total;
   if (!packed && d->B == 1) {  // one sequence may also come as a packed batch of one
     gdn::ScanProblem q;
     check_scan(d, false, &q);
     q.N = 1;
-    plan_chunks(&q, true);
+    plan_fwd(&q, true);
     const size_t alt = scan_layout(q).total;
     if (alt > need) need = alt;
   }
@@ -242,7 +265,7 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
       !aligned(dt_bias, 4) || !aligned(h0, 4) || !aligned(ht, 4) || !aligned(cu_seqlens, 4))
     return GDN_ERR_INVALID_ARG;
   if (p.N == 0) return GDN_OK;
-  plan_chunks(&p, cu_seqlens != nullptr);
+  plan_fwd(&p, cu_seqlens != nullptr);
   const ScanLayout L = scan_layout(p);
   if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
                       !aligned(d->workspace, kAlign)))

@@ -42,16 +42,19 @@ struct ScanArgs {
   long sx, sdt, sz;
   ChunkMap map;
   int C, G, S, per, nblk, Sp;
+  int nb;  // channel blocks in all (G nblk)
   int softplus, split;
 };
 
-// B and C of every token and group as padded fp32 rows, so that the scan reads them through the
-// scalar cache whatever their type, alignment, strides and number.
+// B and C of every token and group as padded fp32 rows [G][Sp / ns][Ttot][2][ns], so that the
+// scan reads them through the scalar cache whatever their type, alignment, strides and number: a
+// wave's ns states of consecutive tokens are one contiguous piece.
 template <typename E>
 __global__ __launch_bounds__(256) void k_scan_pack(const E* Bm, const E* Cm, long sb, long sc,
-                                                   float* bc, int Ttot, int G, int S, int Sp) {
+                                                   float* bc, int Ttot, int G, int S, int Sp,
+                                                   int ns) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  const int row = 2 * Sp;
+  const int row = 2 * Sp;  // a thread reads row element k of token t, group g
   if (i >= (long)Ttot * G * row) return;
   const int k = (int)(i % row);
   const long tg = i / row;
@@ -60,8 +63,26 @@ __global__ __launch_bounds__(256) void k_scan_pack(const E* Bm, const E* Cm, lon
   const int s = k < Sp ? k : k - Sp;
   float v = 0.f;
   if (s < S) v = (float)(k < Sp ? Bm[t * sb + (long)g * S + s] : Cm[t * sc + (long)g * S + s]);
-  bc[i] = v;
+  const long block = (long)g * (Sp / ns) + s / ns;
+  bc[((block * Ttot + t) * 2 + (k >= Sp)) * ns + s % ns] = v;
 }
+
+// What the 16 / NS tokens of a step need: their B and C rows (32 values, two 64-byte scalar loads)
+// and their (step, step x) from LDS.
+template <int NS>
+struct Step {
+  static constexpr int TOKENS = 16 / NS;
+  float bc[32];
+  float2 v[TOKENS];
+  __device__ __forceinline__ void load(const float* rows, const float2 (*sd)[kScanLanes],
+                                       int lane) {
+    const scalar_row r = as_scalar(rows);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) bc[i] = r[i];
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i) v[i] = sd[i][lane];
+  }
+};
 
 // What a lane works on: its channel (clamped, so that every lane has one) and whether it is the
 // lane that owns it.
@@ -69,42 +90,66 @@ struct Lane {
   int g, c;
   bool live;
 };
-__device__ __forceinline__ Lane lane_channel(int per, int nblk) {
+__device__ __forceinline__ Lane lane_channel(int block, int per, int nblk) {
   Lane l;
-  l.g = blockIdx.y / nblk;
-  const int cl = (blockIdx.y - l.g * nblk) * kScanLanes + lane_id();
+  l.g = block / nblk;
+  const int cl = (block - l.g * nblk) * kScanLanes + lane_id();
   l.live = cl < per;
   l.c = l.g * per + min(cl, per - 1);
   return l;
 }
 
-// One chunk's outputs from its start state; the last chunk writes the final state.
-template <int NS, int NW, typename E>
-__global__ __launch_bounds__(64 * NW) void k_scan_out(ScanArgs a) {
+// One chunk's outputs from its start state (OUT; the last chunk writes the final state), or its
+// own end state from a zero start and its sum of steps (a sequence's last chunk has no successor
+// and is skipped).
+//
+// A tile goes through three stages: its owners load x, dt, z and put (step, step x) into LDS; all
+// waves take its tokens through their states and put their share of sum_s C h into LDS; its owners
+// add the shares up and store y.  Between two barriers a wave does the first stage of the next
+// tile, the second of this one and the third of the last, all independent, so there is one
+// barrier a tile; loads are issued a tile before they are needed.
+template <int NS, int NW, bool OUT, bool GATED, typename E>
+__global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
   constexpr int TPW = TT / NW;  // tokens of a tile that a wave prepares and finishes
-  __shared__ float2 sd[TT][kScanLanes];  // (step, step * x)
-  __shared__ float yp[NW][TT][kScanLanes];
-  const int slot = blockIdx.x;
+  __shared__ float2 sd[2][TT][kScanLanes];
+  __shared__ float yp[OUT ? 2 : 1][OUT ? NW : 1][OUT ? TT : 1][kScanLanes];
+  const int slot = blockIdx.x / a.nb;
   const Chunk ch = chunk_of(a.map, slot);
-  if (!ch.ok) return;
+  if (!ch.ok || (!OUT && ch.i == ch.count - 1)) return;
   const int lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const Lane l = lane_channel(a.per, a.nblk);
-  const E* x = static_cast<const E*>(a.x) + l.c;
-  const E* dt = static_cast<const E*>(a.dt) + l.c;
-  const E* z = static_cast<const E*>(a.z) + l.c;
-  E* y = static_cast<E*>(a.y) + l.c;
+  const Lane l = lane_channel(blockIdx.x - slot * a.nb, a.per, a.nblk);
+  Column<E> x, dt, z, y;
+  x.open(a.x, ch.t0, a.sx, ch.len, a.C, l.c, true);
+  dt.open(a.dt, ch.t0, a.sdt, ch.len, a.C, l.c, true);
+  if (GATED) z.open(a.z, ch.t0, a.sz, ch.len, a.C, l.c, true);
+  if (OUT) y.open(a.y, ch.t0, a.C, ch.len, a.C, l.c, l.live);
   const float bias = a.bias ? a.bias[l.c] : 0.f;
   const float Dc = a.D ? a.D[l.c] : 0.f;
+  const uint32_t mask = a.softplus ? 0xFFFFFFFFu : 0u;
   const int s0 = w * NS;
+  const float* rows = a.bc + (((long)l.g * NW + w) * a.map.Ttot + ch.t0) * 2 * NS;
+  const int tiles = (ch.len + TT - 1) / TT;
 
-  float A2[NS], h[NS];
+  uint32_t rx[TPW], rd[TPW], rz[TPW];
+  auto fetch = [&](int tile) {  // past the chunk: its last token
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      const int r = min(tile * TT + w * TPW + i, ch.len - 1);
+      rx[i] = x.load(r);
+      rd[i] = dt.load(r);
+      if (GATED) rz[i] = z.load(r);
+    }
+  };
+  if (tiles > 0) fetch(0);
+
+  float A2[NS], h[NS], sum = 0.f;
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     const int s = s0 + k;
     A2[k] = s < a.S ? a.A[(long)l.c * a.S + s] * kLog2e : 0.f;
     h[k] = 0.f;
-    if (s < a.S) {
+    if (OUT && s < a.S) {
       if (a.split)
         h[k] = a.hst[((long)slot * a.S + s) * a.C + l.c];
       else if (a.h0)
@@ -112,137 +157,125 @@ __global__ __launch_bounds__(64 * NW) void k_scan_out(ScanArgs a) {
     }
   }
 
-  E rx[TPW], rd[TPW], rz[TPW];
-  auto fetch = [&](int tile) {  // this wave's tokens of a tile (past the chunk: its last one)
+  // of the newest prepared tile and of the one before
+  float xv[TPW] = {}, zv[TPW] = {}, xl[TPW] = {}, zl[TPW] = {};
+  auto prepare = [&](int tile) {
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
-      const long r = ch.t0 + min(tile * TT + w * TPW + i, ch.len - 1);
-      rx[i] = x[r * a.sx];
-      rd[i] = dt[r * a.sdt];
-      if (a.z) rz[i] = z[r * a.sz];
+      xv[i] = Column<E>::wide(rx[i]);
+      if (GATED) zv[i] = Column<E>::wide(rz[i]);
+      const float v = step_f32(Column<E>::wide(rd[i]) + bias, mask);
+      sd[tile & 1][w * TPW + i][lane] = make_float2(v, v * xv[i]);
+    }
+    fetch(tile + 1);
+  };
+  auto token = [&](int p, int t, const float2& v, const float* b, const float* c) {
+    float s = 0.f;
+    if (!OUT) sum += v.x;
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      h[k] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[k]), h[k], v.y * b[k]);
+      if (OUT) s = k ? fmaf(c[k], h[k], s) : c[k] * h[k];
+    }
+    if (OUT) yp[p][w][t][lane] = s;
+  };
+  float share[TPW][NW];  // of y, of this wave's tokens, from every wave
+  auto gather = [&](int p) {
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+#pragma unroll
+      for (int k = 0; k < NW; ++k) share[i][k] = yp[p][k][w * TPW + i][lane];
     }
   };
-  const int tiles = (ch.len + TT - 1) / TT;
-  if (tiles > 0) fetch(0);
-  for (int tile = 0; tile < tiles; ++tile) {
-    float xv[TPW], zv[TPW];
-#pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      xv[i] = (float)rx[i];
-      zv[i] = a.z ? (float)rz[i] : 0.f;
-      float v = (float)rd[i] + bias;
-      if (a.softplus) v = softplus_f32(v);
-      sd[w * TPW + i][lane] = make_float2(v, v * xv[i]);
-    }
-    if (tile + 1 < tiles) fetch(tile + 1);
-    __syncthreads();
-    const int m = min(TT, ch.len - tile * TT);
-    const float* row = a.bc + ((long)(ch.t0 + tile * TT) * a.G + l.g) * (2 * a.Sp) + s0;
-    const long step = (long)a.G * (2 * a.Sp);
-    auto token = [&](int t) {
-      const scalar_row b = as_scalar(row + t * step);
-      const scalar_row c = as_scalar(row + t * step + a.Sp);
-      const float2 v = sd[t][lane];
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-        h[k] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[k]), h[k], v.y * b[k]);
-        s = fmaf(c[k], h[k], s);
-      }
-      yp[w][t][lane] = s;
-    };
-    if (m == TT) {
-#pragma unroll
-      for (int t = 0; t < TT; ++t) token(t);
-    } else {
-      for (int t = 0; t < m; ++t) token(t);
-    }
-    __syncthreads();
+  auto finish = [&](int tile, const float* xs, const float* zs) {
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int t = w * TPW + i;
-      if (t < m) {
-        float s = Dc * xv[i];
+      float s = Dc * xs[i];
 #pragma unroll
-        for (int k = 0; k < NW; ++k) s += yp[k][t][lane];
-        if (a.z) s *= zv[i] * sigmoid_f32(zv[i]);
-        if (l.live) y[(long)(ch.t0 + tile * TT + t) * a.C] = (E)s;
-      }
-    }
-  }
-  if (a.ht && ch.i == ch.count - 1 && l.live) {
-#pragma unroll
-    for (int k = 0; k < NS; ++k)
-      if (s0 + k < a.S) a.ht[((long)ch.n * a.C + l.c) * a.S + s0 + k] = h[k];
-  }
-}
-
-// One chunk's own end state (from a zero start) and its sum of steps; a sequence's last chunk
-// has no successor and is skipped.
-template <int NS, int NW, typename E>
-__global__ __launch_bounds__(64 * NW) void k_scan_state(ScanArgs a) {
-  constexpr int TPW = TT / NW;
-  __shared__ float2 sd[2][TT][kScanLanes];
-  const int slot = blockIdx.x;
-  const Chunk ch = chunk_of(a.map, slot);
-  if (!ch.ok || ch.i == ch.count - 1) return;
-  const int lane = lane_id();
-  const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const Lane l = lane_channel(a.per, a.nblk);
-  const E* x = static_cast<const E*>(a.x) + l.c;
-  const E* dt = static_cast<const E*>(a.dt) + l.c;
-  const float bias = a.bias ? a.bias[l.c] : 0.f;
-  const int s0 = w * NS;
-  float A2[NS], h[NS], sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    A2[k] = s0 + k < a.S ? a.A[(long)l.c * a.S + s0 + k] * kLog2e : 0.f;
-    h[k] = 0.f;
-  }
-  E rx[TPW], rd[TPW];
-  auto fetch = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      const long r = ch.t0 + min(tile * TT + w * TPW + i, ch.len - 1);
-      rx[i] = x[r * a.sx];
-      rd[i] = dt[r * a.sdt];
+      for (int k = 0; k < NW; ++k) s += share[i][k];
+      if (GATED) s *= zs[i] * sigmoid_f32(zs[i]);
+      if (tile >= 0 && tile * TT + t < ch.len) y.store(tile * TT + t, s);
     }
   };
-  const int tiles = (ch.len + TT - 1) / TT;
-  if (tiles > 0) fetch(0);
-  for (int tile = 0; tile < tiles; ++tile) {
-    float2(*buf)[kScanLanes] = sd[tile & 1];
+
+  // Scalar loads and LDS reads share one counter, and scalar loads return in no order: waiting for
+  // one read is waiting for all of them.  So a step's reads of both kinds are issued together, a
+  // step ahead (the first step's and the shares' right after the barrier, ahead of the next tile's
+  // preparation), and waited for once.
+  const int full = ch.len / TT;
+  if (tiles > 0) prepare(0);
+  for (int tile = 0; tile < full; ++tile) {
+    const int p = tile & 1;
+    const float* row = rows + (long)tile * TT * 2 * NS;
+    constexpr int N = Step<NS>::TOKENS;
+    Step<NS> buf[2];
+    __syncthreads();
+    buf[0].load(row, sd[p], lane);
+    if (OUT) gather(p ^ 1);  // of no tile, and not used, before the first one
+    __builtin_amdgcn_sched_barrier(0);
+    float px[TPW], pz[TPW];
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
-      float v = (float)rd[i] + bias;
-      if (a.softplus) v = softplus_f32(v);
-      buf[w * TPW + i][lane] = make_float2(v, v * (float)rx[i]);
+      px[i] = xl[i];
+      xl[i] = xv[i];
+      if (GATED) {
+        pz[i] = zl[i];
+        zl[i] = zv[i];
+      }
     }
-    if (tile + 1 < tiles) fetch(tile + 1);
-    __syncthreads();
-    const int m = min(TT, ch.len - tile * TT);
-    const float* row = a.bc + ((long)(ch.t0 + tile * TT) * a.G + l.g) * (2 * a.Sp) + s0;
-    const long step = (long)a.G * (2 * a.Sp);
-    auto token = [&](int t) {
-      const scalar_row b = as_scalar(row + t * step);
-      const float2 v = buf[t][lane];
-      sum += v.x;
+    prepare(tile + 1);  // past the last tile: never used
+    if (OUT) finish(tile - 1, px, pz);
 #pragma unroll
-      for (int k = 0; k < NS; ++k)
-        h[k] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[k]), h[k], v.y * b[k]);
-    };
-    if (m == TT) {
+    for (int step = 0; step < TT / N; ++step) {
+      if (step + 1 < TT / N)
+        buf[(step + 1) & 1].load(row + (step + 1) * 32, sd[p] + (step + 1) * N, lane);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) token(t);
-    } else {
-      for (int t = 0; t < m; ++t) token(t);
+      for (int i = 0; i < N; ++i) {
+        const Step<NS>& q = buf[step & 1];
+        token(p, step * N + i, q.v[i], q.bc + i * 2 * NS, q.bc + i * 2 * NS + NS);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  if (!l.live) return;
+  if (full < tiles) {  // the chunk's last tokens
+    const int p = full & 1;
+    __syncthreads();
+    if (OUT) {
+      gather(p ^ 1);
+      finish(full - 1, xl, zl);
 #pragma unroll
-  for (int k = 0; k < NS; ++k)
-    if (s0 + k < a.S) a.hst[((long)slot * a.S + s0 + k) * a.C + l.c] = h[k];
-  if (w == 0) a.dsum[(long)slot * a.C + l.c] = sum;
+      for (int i = 0; i < TPW; ++i) {
+        xl[i] = xv[i];
+        if (GATED) zl[i] = zv[i];
+      }
+    }
+    for (int t = 0; t < ch.len - full * TT; ++t) {
+      float b[2 * NS];
+      const scalar_row r = as_scalar(rows + (long)(full * TT + t) * 2 * NS);
+#pragma unroll
+      for (int i = 0; i < 2 * NS; ++i) b[i] = r[i];
+      token(p, t, sd[p][t][lane], b, b + NS);
+    }
+  }
+  if (OUT && tiles > 0) {
+    __syncthreads();
+    gather((tiles - 1) & 1);
+    finish(tiles - 1, xl, zl);
+  }
+  if (!l.live || (OUT && (!a.ht || ch.i != ch.count - 1))) return;
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    const int s = s0 + k;
+    if (s < a.S) {
+      if (OUT)
+        a.ht[((long)ch.n * a.C + l.c) * a.S + s] = h[k];
+      else
+        a.hst[((long)slot * a.S + s) * a.C + l.c] = h[k];
+    }
+  }
+  if (!OUT && w == 0) a.dsum[(long)slot * a.C + l.c] = sum;
 }
 
 // Start states in place of the chunks' own end states: one thread per (sequence, state,
@@ -278,26 +311,32 @@ __global__ __launch_bounds__(256) void k_scan_combine(ScanArgs a) {
 
 template <int NS, int NW, typename E>
 hipError_t launch_cfg(const ScanProblem& p, const ScanArgs& a, hipStream_t st) {
-  const dim3 grid(p.slots, p.G * p.nblk);
+  // workgroups in a row (and so on XCDs in turn) are a chunk's channel blocks: chunks of unlike
+  // lengths then load the XCDs alike
+  const unsigned grid = (unsigned)p.slots * a.nb;
   if (a.split) {
-    k_scan_state<NS, NW, E><<<grid, 64 * NW, 0, st>>>(a);
+    k_scan<NS, NW, false, false, E><<<grid, 64 * NW, 0, st>>>(a);
     k_scan_combine<<<dim3(p.N * p.S, (p.C + 255) / 256), 256, 0, st>>>(a);
   }
-  k_scan_out<NS, NW, E><<<grid, 64 * NW, 0, st>>>(a);
+  if (a.z)
+    k_scan<NS, NW, true, true, E><<<grid, 64 * NW, 0, st>>>(a);
+  else
+    k_scan<NS, NW, true, false, E><<<grid, 64 * NW, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename E>
 hipError_t launch_e(const ScanProblem& p, const ScanArgs& a, hipStream_t st) {
-  if (p.ns == 4) {
-    if (p.nw == 1) return launch_cfg<4, 1, E>(p, a, st);
-    if (p.nw == 2) return launch_cfg<4, 2, E>(p, a, st);
-    return launch_cfg<4, 4, E>(p, a, st);
+  switch (p.ns * 100 + p.nw) {
+    case 202: return launch_cfg<2, 2, E>(p, a, st);
+    case 204: return launch_cfg<2, 4, E>(p, a, st);
+    case 208: return launch_cfg<2, 8, E>(p, a, st);
+    case 404: return launch_cfg<4, 4, E>(p, a, st);
+    case 408: return launch_cfg<4, 8, E>(p, a, st);
+    case 808: return launch_cfg<8, 8, E>(p, a, st);
+    case 816: return launch_cfg<8, 16, E>(p, a, st);
+    default: return launch_cfg<16, 16, E>(p, a, st);
   }
-  if (p.ns == 8) return launch_cfg<8, 4, E>(p, a, st);
-  if (p.nw == 4) return launch_cfg<16, 4, E>(p, a, st);
-  if (p.nw == 8) return launch_cfg<16, 8, E>(p, a, st);
-  return launch_cfg<16, 16, E>(p, a, st);
 }
 
 }  // namespace
@@ -308,10 +347,10 @@ hipError_t launch_scan_pack(const ScanProblem& p, hipStream_t st) {
   const unsigned grid = (unsigned)((n + 255) / 256);
   if (p.f32)
     k_scan_pack<float><<<grid, 256, 0, st>>>((const float*)p.Bm, (const float*)p.Cm, p.sb, p.sc,
-                                             p.bc, p.Ttot, p.G, p.S, p.Sp);
+                                             p.bc, p.Ttot, p.G, p.S, p.Sp, p.ns);
   else
     k_scan_pack<bf16><<<grid, 256, 0, st>>>((const bf16*)p.Bm, (const bf16*)p.Cm, p.sb, p.sc,
-                                            p.bc, p.Ttot, p.G, p.S, p.Sp);
+                                            p.bc, p.Ttot, p.G, p.S, p.Sp, p.ns);
   return hipGetLastError();
 }
 
@@ -340,6 +379,7 @@ hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t st) {
   a.S = p.S;
   a.per = p.per;
   a.nblk = p.nblk;
+  a.nb = p.G * p.nblk;
   a.Sp = p.Sp;
   a.softplus = p.softplus;
   a.split = p.Lc != kScanNoSplit;

@@ -22,6 +22,8 @@
 // The sums over the 64 lanes of a wave are the awkward part: dB and dC need one for each (token,
 // state).  A transposing butterfly merges two registers into one at every step (lanes keep the
 // half of the pair that their lane bit names), so 64 sums cost 63 merges, and end one to a lane.
+#include <type_traits>
+
 #include "ssm_device.h"
 
 namespace gdn {
@@ -56,6 +58,7 @@ struct BwdArgs {
   long sx, sdt, sz;
   ChunkMap map;
   int C, G, S, per, nblk, Sp;
+  int nb;  // channel blocks in all (G nblk)
   int softplus, split;
 };
 
@@ -63,73 +66,138 @@ struct Lane {
   int g, blk, c;
   bool live;
 };
-__device__ __forceinline__ Lane lane_channel(int per, int nblk) {
+__device__ __forceinline__ Lane lane_channel(int block, int per, int nblk) {
   Lane l;
-  l.g = blockIdx.y / nblk;
-  l.blk = blockIdx.y - l.g * nblk;
+  l.g = block / nblk;
+  l.blk = block - l.g * nblk;
   const int cl = l.blk * kScanLanes + lane_id();
   l.live = cl < per;
   l.c = l.g * per + min(cl, per - 1);
   return l;
 }
 
-// Adds the lanes that differ in lane bit BIT: lanes without the bit keep p0's sums, lanes with it
-// p1's (for BIT 4 the partner is the mirrored lane of its eight, which pairs the same halves).
+// The transposing butterfly's merges: lanes that differ in one lane bit add up, and of the pair's
+// two registers the lanes without the bit keep p0's sums, those with it p1's.
+//
+// Bits 3 and 2, four merges at a time: a 16-lane row's 4-lane banks are where the bits change, so a
+// DPP addition of p0 for all lanes and one of p1 that writes only the banks with the bit make a
+// merge in two instructions (a selection before an addition takes three).  Bit 2 adds the mirrored
+// lane of its eight, which pairs the same halves.  A DPP operand must not have been written by the
+// two instructions before: hence the s_nop.
+#define GDN_MERGE4(CTRL, BANKS)                                                        \
+  asm("s_nop 1\n\t"                                                                    \
+      "v_add_f32_dpp %0, %4, %4 " CTRL " row_mask:0xf bank_mask:0xf\n\t"               \
+      "v_add_f32_dpp %1, %5, %5 " CTRL " row_mask:0xf bank_mask:0xf\n\t"               \
+      "v_add_f32_dpp %2, %6, %6 " CTRL " row_mask:0xf bank_mask:0xf\n\t"               \
+      "v_add_f32_dpp %3, %7, %7 " CTRL " row_mask:0xf bank_mask:0xf\n\t"               \
+      "v_add_f32_dpp %0, %8, %8 " CTRL " row_mask:0xf bank_mask:" BANKS "\n\t"         \
+      "v_add_f32_dpp %1, %9, %9 " CTRL " row_mask:0xf bank_mask:" BANKS "\n\t"         \
+      "v_add_f32_dpp %2, %10, %10 " CTRL " row_mask:0xf bank_mask:" BANKS "\n\t"       \
+      "v_add_f32_dpp %3, %11, %11 " CTRL " row_mask:0xf bank_mask:" BANKS              \
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])                             \
+      : "v"(p0[0]), "v"(p0[1]), "v"(p0[2]), "v"(p0[3]), "v"(p1[0]), "v"(p1[1]),        \
+        "v"(p1[2]), "v"(p1[3]))
+__device__ __forceinline__ void merge4_bit3(const float* p0, const float* p1, float* r) {
+  GDN_MERGE4("row_ror:8", "0xc");
+}
+__device__ __forceinline__ void merge4_bit2(const float* p0, const float* p1, float* r) {
+  GDN_MERGE4("row_half_mirror", "0xa");
+}
+#undef GDN_MERGE4
+
+// One merge over lane bit 5, 4, 1 or 0.
 template <int BIT>
 __device__ __forceinline__ float merge(float p0, float p1) {
-  if constexpr (BIT == 32) {
+  if constexpr (BIT == 5) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(p0), __float_as_uint(p1),
                                                     false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  } else if constexpr (BIT == 16) {
+  } else if constexpr (BIT == 4) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(p0), __float_as_uint(p1),
                                                     false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
   } else {
-    constexpr int ctrl = BIT == 8 ? 0x128 : BIT == 4 ? 0x141 : BIT == 2 ? 0x4E : 0xB1;
-    const bool hi = (lane_id() & BIT) != 0;
+    constexpr int ctrl = BIT == 1 ? 0x4E : 0xB1;
+    const bool hi = (lane_id() & (1 << BIT)) != 0;
     const float keep = hi ? p1 : p0, give = hi ? p0 : p1;
     return keep + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(give), ctrl, 0xf,
                                                              0xf, true));
   }
 }
 
-// What a token's owner wave makes of its inputs.
-struct Token {
-  float x, step, slope, dy, z, e;
+// A lane's columns of the inputs from a chunk's first token on.
+template <typename E, bool GATED>
+struct Inputs {
+  Column<E> x, dt, z, dy;
+  float bias;
+  uint32_t mask;
+  int last;  // the chunk's last token
+  __device__ __forceinline__ void open(const BwdArgs& a, const Chunk& ch, const Lane& l) {
+    x.open(a.x, ch.t0, a.sx, ch.len, a.C, l.c, true);
+    dt.open(a.dt, ch.t0, a.sdt, ch.len, a.C, l.c, true);
+    if (GATED) z.open(a.z, ch.t0, a.sz, ch.len, a.C, l.c, true);
+    dy.open(a.dy, ch.t0, a.C, ch.len, a.C, l.c, true);
+    bias = a.bias ? a.bias[l.c] : 0.f;
+    mask = a.softplus ? 0xFFFFFFFFu : 0u;
+    last = ch.len - 1;
+  }
 };
-template <typename E>
-__device__ __forceinline__ Token make_token(E x, E dt, E dy, E z, float bias, bool softplus,
-                                            bool gate) {
-  Token k;
-  k.x = (float)x;
-  const float raw = (float)dt + bias;
-  k.step = softplus ? softplus_f32(raw) : raw;
-  k.slope = softplus ? sigmoid_f32(raw) : 1.f;
-  k.dy = (float)dy;
-  k.z = gate ? (float)z : 0.f;
-  k.e = gate ? k.dy * (k.z * sigmoid_f32(k.z)) : k.dy;
-  return k;
-}
 
-template <int NW, typename E>
+// A token's inputs as loaded (bits, to be widened when they are needed).
+template <typename E, bool GATED>
+struct Raw {
+  uint32_t x, dt, z, dy;
+  __device__ __forceinline__ void load(const Inputs<E, GATED>& in, int r) {
+    r = min(r, in.last);  // past the chunk: its last token
+    x = in.x.load(r);
+    dt = in.dt.load(r);
+    if (GATED) z = in.z.load(r);
+    dy = in.dy.load(r);
+  }
+  // e = dy silu(z)
+  __device__ __forceinline__ float e() const {
+    const float d = Column<E>::wide(dy);
+    if (!GATED) return d;
+    const float v = Column<E>::wide(z);
+    return d * (v * sigmoid_f32(v));
+  }
+};
+
+// The B and C rows of four tokens, through the scalar cache.
+struct Rows4 {
+  float v[4 * 2 * NS];
+  __device__ __forceinline__ void load(const float* rows, int t) {
+    const scalar_row r = as_scalar(rows + t * 2 * NS);
+#pragma unroll
+    for (int i = 0; i < 4 * 2 * NS; ++i) v[i] = r[i];
+  }
+  __device__ __forceinline__ float b(int i, int k) const { return v[i * 2 * NS + k]; }
+  __device__ __forceinline__ float c(int i, int k) const { return v[i * 2 * NS + NS + k]; }
+};
+
+template <int NW, bool GATED, typename E>
 __global__ __launch_bounds__(64 * NW) void k_scan_bwd_state(BwdArgs a) {
   constexpr int TPW = BT / NW;
-  __shared__ float4 sv[2][BT][kScanLanes];  // (step, step x, e, -)
-  const int slot = blockIdx.x;
+  __shared__ float sv[2][3][BT][kScanLanes];  // step, step x, e
+  const int slot = blockIdx.x / a.nb;
   const Chunk ch = chunk_of(a.map, slot);
   if (!ch.ok) return;
   const int lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const Lane l = lane_channel(a.per, a.nblk);
-  const E* x = static_cast<const E*>(a.x) + l.c;
-  const E* dt = static_cast<const E*>(a.dt) + l.c;
-  const E* z = static_cast<const E*>(a.z) + l.c;
-  const E* dy = static_cast<const E*>(a.dy) + l.c;
-  const float bias = a.bias ? a.bias[l.c] : 0.f;
+  const Lane l = lane_channel(blockIdx.x - slot * a.nb, a.per, a.nblk);
+  Inputs<E, GATED> in;
+  in.open(a, ch, l);
   const int tiles = (ch.len + BT - 1) / BT;
   for (int sb = 0; sb < a.Sp; sb += NS * NW) {
     const int s0 = sb + w * NS;
+    const float* rows =
+        a.bc + (((long)l.g * (a.Sp / NS) + s0 / NS) * a.map.Ttot + ch.t0) * 2 * NS;
+    Raw<E, GATED> raw[TPW];
+    auto fetch = [&](int tile) {
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) raw[i].load(in, tile * BT + w * TPW + i);
+    };
+    if (tiles > 0) fetch(0);
     float A2[NS], h[NS], P[NS], g[NS], sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
@@ -137,48 +205,44 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd_state(BwdArgs a) {
       h[k] = g[k] = 0.f;
       P[k] = 1.f;
     }
-    E rx[TPW], rd[TPW], rz[TPW], ry[TPW];
-    auto fetch = [&](int tile) {
-#pragma unroll
-      for (int i = 0; i < TPW; ++i) {
-        const long r = ch.t0 + min(tile * BT + w * TPW + i, ch.len - 1);
-        rx[i] = x[r * a.sx];
-        rd[i] = dt[r * a.sdt];
-        ry[i] = dy[r * a.C];
-        if (a.z) rz[i] = z[r * a.sz];
-      }
-    };
-    if (tiles > 0) fetch(0);
     for (int tile = 0; tile < tiles; ++tile) {
-      float4(*buf)[kScanLanes] = sv[tile & 1];
+      float(*buf)[BT][kScanLanes] = sv[tile & 1];
 #pragma unroll
       for (int i = 0; i < TPW; ++i) {
-        const Token k = make_token<E>(rx[i], rd[i], ry[i], rz[i], bias, a.softplus, a.z);
-        buf[w * TPW + i][lane] = make_float4(k.step, k.step * k.x, k.e, 0.f);
+        const float v = step_f32(Column<E>::wide(raw[i].dt) + in.bias, in.mask);
+        buf[0][w * TPW + i][lane] = v;
+        buf[1][w * TPW + i][lane] = v * Column<E>::wide(raw[i].x);
+        buf[2][w * TPW + i][lane] = raw[i].e();
       }
-      if (tile + 1 < tiles) fetch(tile + 1);
+      fetch(tile + 1);
       __syncthreads();
       const int m = min(BT, ch.len - tile * BT);
-      const float* row = a.bc + ((long)(ch.t0 + tile * BT) * a.G + l.g) * (2 * a.Sp) + s0;
-      const long step = (long)a.G * (2 * a.Sp);
-      auto token = [&](int t) {
-        const scalar_row b = as_scalar(row + t * step);
-        const scalar_row c = as_scalar(row + t * step + a.Sp);
-        const float4 v = buf[t][lane];
-        sum += v.x;
+      const float* row = rows + (long)tile * BT * 2 * NS;
+      auto token = [&](int t, auto b, auto c) {
+        const float v = buf[0][t][lane], dx = buf[1][t][lane], e = buf[2][t][lane];
+        sum += v;
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
-          const float d = __builtin_amdgcn_exp2f(v.x * A2[k]);
-          h[k] = fmaf(d, h[k], v.y * b[k]);
+          const float d = __builtin_amdgcn_exp2f(v * A2[k]);
+          h[k] = fmaf(d, h[k], dx * b(k));
           P[k] *= d;
-          g[k] = fmaf(P[k], v.z * c[k], g[k]);
+          g[k] = fmaf(P[k], e * c(k), g[k]);
         }
       };
       if (m == BT) {
+        Rows4 r0, r1;
+        r0.load(row, 0);
+        r1.load(row, 4);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < BT; ++t) token(t);
+        for (int t = 0; t < BT; ++t)
+          token(t, [&](int k) { return t < 4 ? r0.b(t & 3, k) : r1.b(t & 3, k); },
+                [&](int k) { return t < 4 ? r0.c(t & 3, k) : r1.c(t & 3, k); });
       } else {
-        for (int t = 0; t < m; ++t) token(t);
+        for (int t = 0; t < m; ++t) {
+          const scalar_row r = as_scalar(row + t * 2 * NS);
+          token(t, [&](int k) { return r[k]; }, [&](int k) { return r[NS + k]; });
+        }
       }
     }
     if (l.live) {
@@ -231,17 +295,18 @@ __global__ __launch_bounds__(256) void k_scan_bwd_combine(BwdArgs a) {
 
 // One chunk's gradients.  MULTI: more states than the waves hold at once; the sums over states
 // are then carried over the state blocks in LDS.
-template <int NW, bool MULTI, typename E>
+template <int NW, bool MULTI, bool GATED, typename E>
 __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
   constexpr int TPW = BT / NW;
-  __shared__ float4 sv[2][BT][kScanLanes];
-  __shared__ float part[3][NW][BT][kScanLanes];  // sum_s B g, sum_s A q, sum_s C h of a tile
-  __shared__ float acc[MULTI ? 3 : 1][MULTI ? kBwdChunk : 1][kScanLanes];
-  const int slot = blockIdx.x;
+  constexpr int PLANES = GATED ? 3 : 2;
+  __shared__ float sv[2][3][BT][kScanLanes];          // step, step x, e
+  __shared__ float part[PLANES][NW][BT][kScanLanes];  // sum_s B g, sum_s A q, sum_s C h of a tile
+  __shared__ float acc[MULTI ? PLANES : 1][MULTI ? kBwdChunk : 1][kScanLanes];
+  const int slot = blockIdx.x / a.nb;
   const Chunk ch = chunk_of(a.map, slot);
   const int lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane(wave_id());
-  const Lane l = lane_channel(a.per, a.nblk);
+  const Lane l = lane_channel(blockIdx.x - slot * a.nb, a.per, a.nblk);
   float* dv = a.dvp + (long)slot * 2 * a.C + l.c;
   if (!ch.ok) {  // an unused slot adds nothing
     if (l.live) {
@@ -250,74 +315,76 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
     }
     return;
   }
-  const E* x = static_cast<const E*>(a.x) + l.c;
-  const E* dt = static_cast<const E*>(a.dt) + l.c;
-  const E* z = static_cast<const E*>(a.z) + l.c;
-  const E* dy = static_cast<const E*>(a.dy) + l.c;
-  E* dx = static_cast<E*>(a.dx) + l.c;
-  E* ddt = static_cast<E*>(a.ddt) + l.c;
-  E* dz = static_cast<E*>(a.dz) + l.c;
-  const float bias = a.bias ? a.bias[l.c] : 0.f;
+  Inputs<E, GATED> in;
+  in.open(a, ch, l);
   const float Dc = a.D ? a.D[l.c] : 0.f;
   const int tiles = (ch.len + BT - 1) / BT;
-  const long step = (long)a.G * (2 * a.Sp);
+  // a lane without a channel adds zeros to the sums over lanes: zero boundaries and inputs
+  const float alive = l.live ? 1.f : 0.f;
   float sumD = 0.f, sumb = 0.f;
 
   for (int sb = 0; sb < a.Sp; sb += NS * NW) {
     const int s0 = sb + w * NS;
     const bool last_sb = !MULTI || sb + NS * NW >= a.Sp;
-    const float* rows = a.bc + ((long)ch.t0 * a.G + l.g) * (2 * a.Sp) + s0;
+    const float* rows =
+        a.bc + (((long)l.g * (a.Sp / NS) + s0 / NS) * a.map.Ttot + ch.t0) * 2 * NS;
     float A2[NS], h[NS], carry[NS], dA[NS], ck[KT][NS];
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
       const int s = s0 + k;
       A2[k] = s < a.S ? a.A[(long)l.c * a.S + s] * kLog2e : 0.f;
       h[k] = carry[k] = dA[k] = 0.f;
-      // a lane without a channel adds zeros to the sums over lanes: zero boundaries and inputs
       if (s < a.S && l.live) {
-        const long in = ((long)slot * a.S + s) * a.C + l.c;
+        const long at = ((long)slot * a.S + s) * a.C + l.c;
         const long out = ((long)ch.n * a.C + l.c) * a.S + s;
-        h[k] = a.split ? a.hst[in] : a.h0 ? a.h0[out] : 0.f;
-        carry[k] = a.split ? a.gst[in] : a.dht ? a.dht[out] : 0.f;
+        h[k] = a.split ? a.hst[at] : a.h0 ? a.h0[out] : 0.f;
+        carry[k] = a.split ? a.gst[at] : a.dht ? a.dht[out] : 0.f;
       }
     }
 
     // the states at the tiles' starts
+#pragma unroll
+    for (int j = 0; j < KT; ++j) {
+#pragma unroll
+      for (int k = 0; k < NS; ++k) ck[j][k] = h[k];
+    }
     {
-      E rx[TPW], rd[TPW];
+      uint32_t rx[TPW], rd[TPW];
       auto fetch = [&](int tile) {
 #pragma unroll
         for (int i = 0; i < TPW; ++i) {
-          const long r = ch.t0 + min(tile * BT + w * TPW + i, ch.len - 1);
-          rx[i] = x[r * a.sx];
-          rd[i] = dt[r * a.sdt];
+          const int r = min(tile * BT + w * TPW + i, in.last);
+          rx[i] = in.x.load(r);
+          rd[i] = in.dt.load(r);
         }
       };
       if (tiles > 1) fetch(0);
-#pragma unroll
-      for (int k = 0; k < NS; ++k) ck[0][k] = h[k];
       for (int tile = 0; tile + 1 < tiles; ++tile) {
-        float4(*buf)[kScanLanes] = sv[tile & 1];
+        float(*buf)[BT][kScanLanes] = sv[tile & 1];
+        const float* row = rows + tile * BT * 2 * NS;
+        Rows4 r0, r1;
+        r0.load(row, 0);
+        r1.load(row, 4);
 #pragma unroll
         for (int i = 0; i < TPW; ++i) {
-          float v = (float)rd[i] + bias;
-          if (a.softplus) v = softplus_f32(v);
-          buf[w * TPW + i][lane] = make_float4(v, l.live ? v * (float)rx[i] : 0.f, 0.f, 0.f);
+          const float v = step_f32(Column<E>::wide(rd[i]) + in.bias, in.mask);
+          buf[0][w * TPW + i][lane] = v;
+          buf[1][w * TPW + i][lane] = v * Column<E>::wide(rx[i]) * alive;
         }
-        if (tile + 2 < tiles) fetch(tile + 1);
+        fetch(tile + 1);
         __syncthreads();
-        const float* row = rows + (long)tile * BT * step;
 #pragma unroll
         for (int t = 0; t < BT; ++t) {
-          const scalar_row b = as_scalar(row + t * step);
-          const float4 v = buf[t][lane];
+          const float v = buf[0][t][lane], dx = buf[1][t][lane];
 #pragma unroll
           for (int k = 0; k < NS; ++k)
-            h[k] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[k]), h[k], v.y * b[k]);
+            h[k] = fmaf(__builtin_amdgcn_exp2f(v * A2[k]), h[k],
+                        dx * (t < 4 ? r0.b(t & 3, k) : r1.b(t & 3, k)));
         }
 #pragma unroll
         for (int j = 1; j < KT; ++j)
           if (j == tile + 1) {
+            asm volatile("");  // a branch for the whole wave, not a selection for every value
 #pragma unroll
             for (int k = 0; k < NS; ++k) ck[j][k] = h[k];
           }
@@ -325,96 +392,118 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
       __syncthreads();
     }
 
-    E rx[TPW], rd[TPW], rz[TPW], ry[TPW];
+    Raw<E, GATED> raw[TPW];
     auto fetch = [&](int tile) {
 #pragma unroll
-      for (int i = 0; i < TPW; ++i) {
-        const long r = ch.t0 + min(tile * BT + w * TPW + i, ch.len - 1);
-        rx[i] = x[r * a.sx];
-        rd[i] = dt[r * a.sdt];
-        ry[i] = dy[r * a.C];
-        if (a.z) rz[i] = z[r * a.sz];
-      }
+      for (int i = 0; i < TPW; ++i) raw[i].load(in, tile * BT + w * TPW + i);
     };
     if (tiles > 0) fetch(tiles - 1);
     for (int tile = tiles - 1; tile >= 0; --tile) {
-      Token own[TPW];
+      const int m = min(BT, ch.len - tile * BT);
+      const float* row = rows + tile * BT * 2 * NS;
+      Raw<E, GATED> own[TPW];
+      float sig[TPW];  // sigmoid(z)
 #pragma unroll
       for (int i = 0; i < TPW; ++i) {
-        own[i] = make_token<E>(rx[i], rd[i], ry[i], rz[i], bias, a.softplus, a.z);
-        sv[0][w * TPW + i][lane] =
-            l.live ? make_float4(own[i].step, own[i].step * own[i].x, own[i].e, 0.f)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        own[i] = raw[i];
+        const float v = step_f32(Column<E>::wide(own[i].dt) + in.bias, in.mask);
+        const float d = Column<E>::wide(own[i].dy);
+        if (GATED) sig[i] = sigmoid_f32(Column<E>::wide(own[i].z));
+        const float e = GATED ? d * (Column<E>::wide(own[i].z) * sig[i]) : d;
+        sv[0][0][w * TPW + i][lane] = v;
+        sv[0][1][w * TPW + i][lane] = v * Column<E>::wide(own[i].x) * alive;
+        sv[0][2][w * TPW + i][lane] = e * alive;
       }
       if (tile > 0) fetch(tile - 1);
       __syncthreads();
-      const int m = min(BT, ch.len - tile * BT);
-      const float* row = rows + (long)tile * BT * step;
 
-      float start[NS], hs[BT][NS], as[BT][NS];
+      float start[NS];
 #pragma unroll
-      for (int j = 0; j < KT; ++j)
+      for (int k = 0; k < NS; ++k) start[k] = ck[0][k];
+#pragma unroll
+      for (int j = 1; j < KT; ++j)
         if (j == tile) {
+          asm volatile("");
 #pragma unroll
           for (int k = 0; k < NS; ++k) start[k] = ck[j][k];
         }
+      // the tile's states and decays again, then its tokens backwards, two at a time; FULL: all its
+      // tokens are the chunk's.  A token's products for dB and dC (4 states each) merge over the
+      // lanes as they come: lane bit 3 takes dB or dC, bit 2 the state's upper bit, bit 4 its
+      // lower one, bits 5 1 0 the token's bits 0 1 2
+      float all = 0.f;
+      auto body = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        float hs[BT][NS], as[BT][NS];
+        Rows4 r0, r1;
+        r0.load(row, 0);
+        if (FULL || m > 4) r1.load(row, 4);
 #pragma unroll
-      for (int t = 0; t < BT; ++t) {
-        if (t < m) {
-          const scalar_row b = as_scalar(row + t * step);
-          const float4 v = sv[0][t][lane];
+        for (int t = 0; t < BT; ++t) {
+          if (FULL || t < m) {
+            const float v = sv[0][0][t][lane], dx = sv[0][1][t][lane];
 #pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            as[t][k] = __builtin_amdgcn_exp2f(v.x * A2[k]);
-            hs[t][k] = fmaf(as[t][k], t ? hs[t ? t - 1 : 0][k] : start[k], v.y * b[k]);
+            for (int k = 0; k < NS; ++k) {
+              as[t][k] = __builtin_amdgcn_exp2f(v * A2[k]);
+              hs[t][k] = fmaf(as[t][k], t ? hs[t ? t - 1 : 0][k] : start[k],
+                              dx * (t < 4 ? r0.b(t & 3, k) : r1.b(t & 3, k)));
+            }
           }
         }
-      }
-      // tokens backwards; their 8 products a token (4 states of dB, 4 of dC) merge over the
-      // lanes as they come: lane bits 5 4 3 take the product's index, bits 2 1 0 the token's
-      // bits 0 1 2
-      float m2[2], m1[2], m0[2], all = 0.f;
-      m2[0] = m2[1] = m1[0] = m1[1] = m0[0] = m0[1] = 0.f;
+        float m1[2], m0[2];
+        m1[0] = m1[1] = m0[0] = m0[1] = 0.f;
 #pragma unroll
-      for (int t = BT - 1; t >= 0; --t) {
-        float token_sum = 0.f;
-        if (t < m) {
-          const scalar_row b = as_scalar(row + t * step);
-          const scalar_row c = as_scalar(row + t * step + a.Sp);
-          const float4 v = sv[0][t][lane];
-          float u = 0.f, q1 = 0.f, yy = 0.f, pb[NS], pc[NS];
+        for (int t1 = BT - 1; t1 >= 0; t1 -= 2) {
+          float x2[2][4];  // of the pair's tokens, merged over lane bit 3
 #pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            const float g = fmaf(v.z, c[k], carry[k]);
-            const float ah = as[t][k] * (t ? hs[t ? t - 1 : 0][k] : start[k]);
-            const float q = g * ah;
-            dA[k] = fmaf(v.x, q, dA[k]);
-            q1 = fmaf(q, A2[k], q1);
-            u = fmaf(g, b[k], u);
-            yy = fmaf(hs[t][k], c[k], yy);
-            pb[k] = g * v.y;
-            pc[k] = v.z * hs[t][k];
-            carry[k] = as[t][k] * g;
+          for (int t = t1; t > t1 - 2; --t) {
+            float* to = x2[t & 1];
+            if (FULL || t < m) {
+              const float v = sv[0][0][t][lane], dx = sv[0][1][t][lane], e = sv[0][2][t][lane];
+              float u = 0.f, q1 = 0.f, yy = 0.f, pb[NS], pc[NS];
+#pragma unroll
+              for (int k = 0; k < NS; ++k) {
+                const float b = t < 4 ? r0.b(t & 3, k) : r1.b(t & 3, k);
+                const float c = t < 4 ? r0.c(t & 3, k) : r1.c(t & 3, k);
+                const float g = fmaf(e, c, carry[k]);
+                const float ah = as[t][k] * (t ? hs[t ? t - 1 : 0][k] : start[k]);
+                const float q = g * ah;
+                dA[k] = fmaf(v, q, dA[k]);
+                q1 = k ? fmaf(q, A2[k], q1) : q * A2[k];
+                u = k ? fmaf(g, b, u) : g * b;
+                if (GATED) yy = k ? fmaf(hs[t][k], c, yy) : hs[t][k] * c;
+                pb[k] = g * dx;
+                pc[k] = e * hs[t][k];
+                carry[k] = as[t][k] * g;
+              }
+              part[0][w][t][lane] = u;
+              part[1][w][t][lane] = q1;
+              if (GATED) part[PLANES - 1][w][t][lane] = yy;
+              merge4_bit3(pb, pc, to);
+            } else {
+              to[0] = to[1] = to[2] = to[3] = 0.f;
+            }
           }
-          part[0][w][t][lane] = u;
-          part[1][w][t][lane] = q1;
-          part[2][w][t][lane] = yy;
-          const float r0 = merge<32>(pb[0], pc[0]), r1 = merge<32>(pb[1], pc[1]);
-          const float r2 = merge<32>(pb[2], pc[2]), r3 = merge<32>(pb[3], pc[3]);
-          token_sum = merge<8>(merge<16>(r0, r2), merge<16>(r1, r3));
-        }
-        m2[t & 1] = token_sum;
-        if ((t & 1) == 0) {
-          m1[(t >> 1) & 1] = merge<4>(m2[0], m2[1]);
-          if ((t & 2) == 0) {
-            m0[(t >> 2) & 1] = merge<2>(m1[0], m1[1]);
-            if (t == 0) all = merge<1>(m0[0], m0[1]);
+          // states 0, 1 of the even and the odd token against their states 2, 3
+          const float lo[4] = {x2[0][0], x2[0][1], x2[1][0], x2[1][1]};
+          const float hi[4] = {x2[0][2], x2[0][3], x2[1][2], x2[1][3]};
+          float y4[4];
+          merge4_bit2(lo, hi, y4);
+          const int j = (t1 >> 1) & 3;  // the pair
+          m1[j & 1] = merge<5>(merge<4>(y4[0], y4[1]), merge<4>(y4[2], y4[3]));
+          if ((j & 1) == 0) {
+            m0[j >> 1] = merge<1>(m1[0], m1[1]);
+            if (j == 0) all = merge<0>(m0[0], m0[1]);
           }
         }
-      }
+      };
+      if (m == BT)
+        body(std::true_type());
+      else
+        body(std::false_type());
       {
-        const int t = ((lane >> 2) & 1) | (lane & 2) | ((lane & 1) << 2);
-        const int k = (lane >> 3) & 3, kind = lane >> 5;
+        const int t = ((lane >> 5) & 1) | (lane & 2) | ((lane & 1) << 2);
+        const int k = ((lane >> 1) & 2) | ((lane >> 4) & 1), kind = (lane >> 3) & 1;
         if (t < m)
           a.bcp[(((long)l.blk * a.map.Ttot + ch.t0 + tile * BT + t) * a.G + l.g) * (2 * a.Sp) +
                 kind * a.Sp + s0 + k] = all;
@@ -429,7 +518,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
           for (int k = 0; k < NW; ++k) {
             u += part[0][k][t][lane];
             q1 += part[1][k][t][lane];
-            yy += part[2][k][t][lane];
+            if (GATED) yy += part[PLANES - 1][k][t][lane];
           }
           if constexpr (MULTI) {
             float* p = &acc[0][tile * BT + t][lane];
@@ -437,28 +526,31 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
             if (sb > 0) {
               u += p[0];
               q1 += p[plane];
-              yy += p[2 * plane];
+              if (GATED) yy += p[(PLANES - 1) * plane];
             }
             if (!last_sb) {
               p[0] = u;
               p[plane] = q1;
-              p[2 * plane] = yy;
+              if (GATED) p[(PLANES - 1) * plane] = yy;
             }
           }
           if (last_sb) {
-            const Token& o = own[i];
             const long r = (long)(ch.t0 + tile * BT + t) * a.C;
-            // A q was summed with A log2(e)
-            const float gd = fmaf(q1, 0.6931471805599453f, o.x * u) * o.slope;
-            sumD = fmaf(o.x, o.e, sumD);
+            const float xv = Column<E>::wide(own[i].x);
+            // only this wave writes these, with its next tile
+            const float step = sv[0][0][t][lane], e = sv[0][2][t][lane];
+            // A q was summed with A log2(e); the slope of softplus is the sigmoid
+            float gd = fmaf(q1, 0.6931471805599453f, xv * u);
+            if (in.mask) gd *= sigmoid_f32(Column<E>::wide(own[i].dt) + in.bias);
+            sumD = fmaf(xv, e, sumD);
             sumb += gd;
             if (l.live) {
-              dx[r] = (E)fmaf(o.step, u, Dc * o.e);
-              ddt[r] = (E)gd;
-              if (a.z) {
-                const float sg = sigmoid_f32(o.z);
-                dz[r] = (E)(o.dy * fmaf(Dc, o.x, yy) * (sg * fmaf(o.z, 1.f - sg, 1.f)));
-              }
+              static_cast<E*>(a.dx)[r + l.c] = (E)fmaf(step, u, Dc * e);
+              static_cast<E*>(a.ddt)[r + l.c] = (E)gd;
+              if (GATED)
+                static_cast<E*>(a.dz)[r + l.c] =
+                    (E)(Column<E>::wide(own[i].dy) * fmaf(Dc, xv, yy) *
+                        (sig[i] * fmaf(Column<E>::wide(own[i].z), 1.f - sig[i], 1.f)));
             }
           }
         }
@@ -532,17 +624,25 @@ __global__ __launch_bounds__(256) void k_scan_bwd_params(const float* dAp, const
 
 template <int NW, bool MULTI, typename E>
 hipError_t launch_cfg(const ScanProblem& p, const ScanBwd& b, const BwdArgs& a, hipStream_t st) {
-  const dim3 grid(p.slots, p.G * p.nblk);
+  // workgroups in a row (and so on XCDs in turn) are a chunk's channel blocks: chunks of unlike
+  // lengths then load the XCDs alike
+  const unsigned grid = (unsigned)p.slots * a.nb;
   if (p.slots == 0) {  // no sequences: the parameters' gradients are zero
     k_scan_bwd_params<<<dim3((p.C + 255) / 256, p.S + 2), 256, 0, st>>>(
         b.dAp, b.dvp, b.dA, b.dD, b.dbias, 0, p.C, p.S);
     return hipGetLastError();
   }
   if (a.split) {
-    k_scan_bwd_state<NW, E><<<grid, 64 * NW, 0, st>>>(a);
+    if (a.z)
+      k_scan_bwd_state<NW, true, E><<<grid, 64 * NW, 0, st>>>(a);
+    else
+      k_scan_bwd_state<NW, false, E><<<grid, 64 * NW, 0, st>>>(a);
     k_scan_bwd_combine<<<dim3(p.N * p.S, (p.C + 255) / 256, 2), 256, 0, st>>>(a);
   }
-  k_scan_bwd<NW, MULTI, E><<<grid, 64 * NW, 0, st>>>(a);
+  if (a.z)
+    k_scan_bwd<NW, MULTI, true, E><<<grid, 64 * NW, 0, st>>>(a);
+  else
+    k_scan_bwd<NW, MULTI, false, E><<<grid, 64 * NW, 0, st>>>(a);
   const long n = (long)p.Ttot * p.G * 2 * p.Sp;
   if (n > 0)
     k_scan_bwd_bc<E><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
@@ -597,6 +697,7 @@ hipError_t launch_scan_bwd(const ScanProblem& p, const ScanBwd& b, hipStream_t s
   a.S = p.S;
   a.per = p.per;
   a.nblk = p.nblk;
+  a.nb = p.G * p.nblk;
   a.Sp = p.Sp;
   a.softplus = p.softplus;
   a.split = p.slots > p.N;  // otherwise every sequence is one chunk

@@ -23,6 +23,7 @@ struct ScanProblem {
   int per, nblk;       // channels a group, 64-channel blocks a group
   int Sp;              // states of a padded fp32 row of B or C (ns * nw)
   int ns, nw;          // states a lane, waves a workgroup
+  int reach;           // tokens whose rows lie within 2 GiB of the first one's
   int Lc, slots;       // chunk length (kScanNoSplit: whole sequences), chunk slots
   bool f32, softplus;
   const void* x;
@@ -36,7 +37,7 @@ struct ScanProblem {
   const float* h0;     // [N, C, S] or null
   const int32_t* cu;   // [N + 1] or null
   int64_t sx, sdt, sz, sb, sc;  // elements from one token's row to the next
-  float* bc;           // workspace: [Ttot, G, 2, Sp], B then C in fp32, padded with zeros
+  float* bc;           // workspace: [G, Sp / ns, Ttot, 2, ns], B and C in fp32, padded with zeros
   float* hst;          // workspace: [slots, S, C], each chunk's own end state, then its start
   float* dsum;         // workspace: [slots, C], each chunk's sum of steps
   void* y;

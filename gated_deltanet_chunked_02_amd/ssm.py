@@ -18,10 +18,13 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _need, _ptr,
-               _validate_conv, load)
+import torch
+from torch import Tensor
 
-_FLOATS = None  # filled on first use: importing torch is left to the first call
+from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _need, _validate_conv,
+               load)
+
+_CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
 class GdnScanDesc(ctypes.Structure):
@@ -72,10 +75,19 @@ def declare(lib):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _current(device):
+    """The raw current stream of a device (a tenth of the time the Stream object takes)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device.index)
+
+
+def _addresses(tensors):
+    return [t if t is None or type(t) is int else t.data_ptr() for t in tensors]
 
 
 def gdn_selective_scan_workspace_size(desc: GdnScanDesc) -> int:
@@ -90,7 +102,7 @@ def gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 
                            stream=None) -> int:
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_selective_scan_fwd(
-        ctypes.byref(desc), *map(_ptr, (x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, y, ht)),
+        ctypes.byref(desc), *_addresses((x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, y, ht)),
         _stream(stream)))
 
 
@@ -106,7 +118,7 @@ def gdn_selective_scan_bwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 
                            dA, dB, dC, dD, dz, ddt_bias, dh0, stream=None) -> int:
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_selective_scan_bwd(
-        ctypes.byref(desc), *map(_ptr, (x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dy, dht,
+        ctypes.byref(desc), *_addresses((x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, dy, dht,
                                         dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0)),
         _stream(stream)))
 
@@ -115,98 +127,115 @@ def gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, cache
                                out_indices, y, stream=None) -> int:
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_selective_state_update(
-        ctypes.byref(desc), *map(_ptr, (state, x, dt, A, B, C, D, z, dt_bias, cache_indices,
+        ctypes.byref(desc), *_addresses((state, x, dt, A, B, C, D, z, dt_bias, cache_indices,
                                         out_indices, y)), _stream(stream)))
 
 
 def _code(t):
     """The library's code of a tensor's dtype, or None."""
-    global _FLOATS
-    if _FLOATS is None:
-        import torch
-        _FLOATS = {torch.bfloat16: BF16, torch.float32: F32}
-    return _FLOATS.get(t.dtype)
+    return _CODES.get(t.dtype)
 
 
 def _rows(t, lead):
     """(t, elements from one row to the next) for a tensor [*lead, ...] whose rows are
-    contiguous and evenly spaced over the leading axes; a contiguous copy of any other."""
+    contiguous and evenly spaced over its one or two leading axes; a contiguous copy of any
+    other (0: rows one after another)."""
     if t.is_contiguous():
         return t, 0
-    width, want = 1, 1
-    for n, s in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if n != 1 and s != want:
+    shape, stride = t.shape, t.stride()
+    width = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        n = shape[i]
+        if n != 1 and stride[i] != width:
             return t.contiguous(), 0
-        want *= n
         width *= n
-    row = None
-    for n, s in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
-        if n == 1:
-            continue
-        if row is None:
-            row, span = s, s * n
-        elif s != span:
+    if lead == 1:
+        row = stride[0]
+    elif shape[1] == 1:
+        row = stride[0]
+    else:
+        row = stride[1]
+        if shape[0] != 1 and stride[0] != row * shape[1]:
             return t.contiguous(), 0
-        else:
-            span *= n
-    if row is None:
-        return t, 0
     return (t, row) if row >= width else (t.contiguous(), 0)
 
 
+def _on(device, **named):
+    """Every tensor given on ``device``, a CUDA (HIP) device (see _check_devices)."""
+    if device.type == "cuda":
+        for t in named.values():
+            if t is not None and t.device != device:
+                break
+        else:
+            return
+    _check_devices(named, device)
+
+
 def _f32(name, t, shape):
-    import torch
     if t is None:
         return None
-    _need(isinstance(t, torch.Tensor) and t.dtype == torch.float32, TypeError,
-          "%s must be an fp32 tensor" % name)
-    _need(tuple(t.shape) == shape, ValueError,
-          "%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if not isinstance(t, Tensor) or t.dtype != torch.float32:
+        raise TypeError("%s must be an fp32 tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     return t.contiguous()
 
 
 def _indices(name, t, n):
-    import torch
     if t is None:
         return None
-    _need(isinstance(t, torch.Tensor) and t.dtype in (torch.int32, torch.int64), TypeError,
-          "%s must be an int32 or int64 tensor" % name)
-    _need(tuple(t.shape) == (n,), ValueError, "%s must be [%d]" % (name, n))
+    if not isinstance(t, Tensor) or t.dtype not in (torch.int32, torch.int64):
+        raise TypeError("%s must be an int32 or int64 tensor" % name)
+    if t.shape != (n,):
+        raise ValueError("%s must be [%d]" % (name, n))
     return t.to(torch.int32).contiguous()
+
+
+def _like(name, t, x):
+    """A tensor of x's shape and dtype, or None."""
+    if t is None:
+        return
+    if not isinstance(t, Tensor) or t.dtype != x.dtype:
+        raise TypeError("%s must be a tensor of x's dtype %s" % (name, x.dtype))
+    if t.shape != x.shape:
+        raise ValueError("%s must have x's shape %s, got %s" % (name, list(x.shape),
+                                                                list(t.shape)))
 
 
 def _operands(x, dt, A, B, C, D, z, dt_bias, lead):
     """Checks of the operands that the scan and its single-token form share, and the descriptor
     but for the batch's shape.  ``lead``: axes before the channels."""
-    import torch
     for name, t in (("x", x), ("dt", dt), ("A", A), ("B", B), ("C", C)):
-        _need(isinstance(t, torch.Tensor), TypeError, "%s must be a torch tensor" % name)
-    _need(x.dim() == lead + 1, ValueError,
-          "x must be %s" % ("[B, T, channels]" if lead == 2 else "[B, channels]"))
-    code = _code(x)
-    _need(code is not None, TypeError, "x must be bf16 or fp32, got %s" % x.dtype)
-    shape, ch = tuple(x.shape), x.shape[-1]
-    _need(ch > 0, ValueError, "x must have channels")
-    for name, t in (("dt", dt), ("z", z)):
-        if t is not None:
-            _need(isinstance(t, torch.Tensor) and t.dtype == x.dtype, TypeError,
-                  "%s must be a tensor of x's dtype %s" % (name, x.dtype))
-            _need(tuple(t.shape) == shape, ValueError,
-                  "%s must have x's shape %s" % (name, list(shape)))
-    _need(A.dim() == 2 and A.shape[0] == ch and A.shape[1] > 0, ValueError,
-          "A must be [channels, dstate] with %d channels, got %s" % (ch, list(A.shape)))
+        if not isinstance(t, Tensor):
+            raise TypeError("%s must be a torch tensor" % name)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != lead + 1:
+        raise ValueError("x must be %s" % ("[B, T, channels]" if lead == 2 else "[B, channels]"))
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("x must be bf16 or fp32, got %s" % dtype)
+    ch = shape[-1]
+    if ch == 0:
+        raise ValueError("x must have channels")
+    _like("dt", dt, x)
+    _like("z", z, x)
+    if A.dim() != 2 or A.shape[0] != ch or A.shape[1] == 0:
+        raise ValueError("A must be [channels, dstate] with %d channels, got %s"
+                         % (ch, list(A.shape)))
     S = A.shape[1]
     A = _f32("A", A, (ch, S))
+    rows = B.shape
     for name, t in (("B", B), ("C", C)):
-        _need(t.dtype == x.dtype, TypeError, "%s must have x's dtype %s" % (name, x.dtype))
-        _need(t.dim() == lead + 2 and tuple(t.shape[:lead]) == shape[:lead] and
-              t.shape[-1] == S and t.shape == B.shape, ValueError,
-              "%s must be %s with dstate %d, got %s"
-              % (name, "[B, T, groups, dstate]" if lead == 2 else "[B, groups, dstate]", S,
-                 list(t.shape)))
-    G = B.shape[-2]
-    _need(G > 0 and ch % G == 0, ValueError,
-          "the channels (%d) must be a multiple of the groups (%d)" % (ch, G))
+        if t.dtype != dtype:
+            raise TypeError("%s must have x's dtype %s" % (name, dtype))
+        if t.shape != rows or len(rows) != lead + 2 or rows[:lead] != shape[:lead] or \
+                rows[-1] != S:
+            raise ValueError("%s must be %s with dstate %d, got %s" % (
+                name, "[B, T, groups, dstate]" if lead == 2 else "[B, groups, dstate]", S,
+                list(t.shape)))
+    G = rows[lead]
+    if G == 0 or ch % G:
+        raise ValueError("the channels (%d) must be a multiple of the groups (%d)" % (ch, G))
     D, dt_bias = _f32("D", D, (ch,)), _f32("dt_bias", dt_bias, (ch,))
     x, sx = _rows(x, lead)
     dt, sdt = _rows(dt, lead)
@@ -215,14 +244,13 @@ def _operands(x, dt, A, B, C, D, z, dt_bias, lead):
     sz = 0
     if z is not None:
         z, sz = _rows(z, lead)
-    desc = GdnScanDesc(channels=ch, groups=G, dstate=S, dtype=code, x_stride=sx, dt_stride=sdt,
-                       z_stride=sz, b_stride=sb, c_stride=sc)
+    # B, T, N, dt_softplus and state_lines are the caller's
+    desc = GdnScanDesc(0, 0, 0, ch, G, S, code, 0, 0, sx, sdt, sz, sb, sc, None, 0)
     return desc, x, dt, A, B, C, D, z, dt_bias
 
 
 def _sequences(x, cu_seqlens):
     """(cu_seqlens as int32 or None, number of sequences) of x [B, T, ...]."""
-    import torch
     if cu_seqlens is None:
         return None, x.shape[0]
     _need(isinstance(cu_seqlens, torch.Tensor) and
@@ -236,7 +264,6 @@ def _sequences(x, cu_seqlens):
 
 def _workspace(desc, need, workspace, device):
     """Points the descriptor at the caller's workspace, or at a new one; returns it."""
-    import torch
     if workspace is not None:
         _need(isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and
               workspace.is_contiguous(), TypeError,
@@ -260,13 +287,12 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
     B, C: [B, T, groups, dstate], shared by channels / groups channels each; D, dt_bias
     [channels] fp32 or None; initial_state [N, channels, dstate] fp32 or None; cu_seqlens
     [N + 1] for a packed batch (B == 1).  Returns (y in x's dtype, final state fp32 or None)."""
-    import torch
     desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 2)
     cu, N = _sequences(x, cu_seqlens)
     h0 = _f32("initial_state", initial_state, (N, desc.channels, desc.dstate))
     dev = x.device
-    _check_devices(dict(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
-                        initial_state=h0, cu_seqlens=cu, workspace=workspace), dev)
+    _on(dev, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, initial_state=h0,
+        cu_seqlens=cu, workspace=workspace)
     desc.B, desc.T, desc.N, desc.dt_softplus = x.shape[0], x.shape[1], N, int(bool(dt_softplus))
     y = torch.empty(x.shape, device=dev, dtype=x.dtype)
     ht = None
@@ -275,7 +301,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
     if x.shape[0] == 0:
         return y, ht
     ws = _workspace(desc, gdn_selective_scan_workspace_size(desc), workspace, dev)  # noqa: F841
-    st = gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, y, ht)
+    st = gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, y, ht,
+                                _current(dev))
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_fwd")
     return y, ht
@@ -287,17 +314,15 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_soft
     (x's shape and dtype) and ``dht`` of the final state (fp32, or None: zero); the forward's
     inputs as there.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinitial_state): dx, ddt,
     dz, dB, dC in x's dtype, the others in fp32, None where the input is None."""
-    import torch
     desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 2)
     cu, N = _sequences(x, cu_seqlens)
     states = (N, desc.channels, desc.dstate)
     h0, dht = _f32("initial_state", initial_state, states), _f32("dht", dht, states)
-    _need(isinstance(dy, torch.Tensor) and dy.dtype == x.dtype, TypeError,
-          "dy must be a tensor of x's dtype %s" % x.dtype)
-    _need(dy.shape == x.shape, ValueError, "dy must have x's shape %s" % list(x.shape))
+    _need(dy is not None, TypeError, "dy is required")
+    _like("dy", dy, x)
     dev = x.device
-    _check_devices(dict(x=x, dt=dt, A=A, B=B, C=C, dy=dy, D=D, z=z, dt_bias=dt_bias,
-                        initial_state=h0, dht=dht, cu_seqlens=cu, workspace=workspace), dev)
+    _on(dev, x=x, dt=dt, A=A, B=B, C=C, dy=dy, D=D, z=z, dt_bias=dt_bias, initial_state=h0,
+        dht=dht, cu_seqlens=cu, workspace=workspace)
     dy = dy.contiguous()
     desc.B, desc.T, desc.N, desc.dt_softplus = x.shape[0], x.shape[1], N, int(bool(dt_softplus))
     new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)  # noqa: E731
@@ -307,7 +332,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_soft
     need = gdn_selective_scan_bwd_workspace_size(desc)
     ws = _workspace(desc, need, workspace, dev)  # noqa: F841
     st = gdn_selective_scan_bwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, dy, dht, dx, ddt, dA,
-                                dB, dC, dD, dz, dbias, dh0)
+                                dB, dC, dD, dz, dbias, dh0, _current(dev))
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_bwd")
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
@@ -325,27 +350,28 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     [B, channels]; B, C: [B, groups, dstate]; the rest as for selective_scan.  Sequence b reads
     line cache_indices[b] (b when None) and writes line out_indices[b] (the line it read when
     None).  Returns y [B, channels] in x's dtype."""
-    import torch
     desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 1)
     n = x.shape[0]
-    _need(isinstance(state, torch.Tensor) and state.dtype == torch.float32 and
-          state.is_contiguous(), TypeError, "state must be a contiguous fp32 tensor")
-    _need(state.dim() == 3 and state.shape[0] > 0 and
-          tuple(state.shape[1:]) == (desc.channels, desc.dstate), ValueError,
-          "state must be [lines, %d, %d], got %s" % (desc.channels, desc.dstate,
-                                                     list(state.shape)))
+    if not isinstance(state, Tensor) or state.dtype != torch.float32 or \
+            not state.is_contiguous():
+        raise TypeError("state must be a contiguous fp32 tensor")
+    if state.dim() != 3 or state.shape[0] == 0 or state.shape[1:] != A.shape:
+        raise ValueError("state must be [lines, %d, %d], got %s"
+                         % (desc.channels, desc.dstate, list(state.shape)))
     read, write = _indices("cache_indices", cache_indices, n), _indices("out_indices",
                                                                         out_indices, n)
     _need(read is not None or state.shape[0] >= n, ValueError,
           "state has fewer lines (%d) than there are sequences (%d)" % (state.shape[0], n))
-    _check_devices(dict(state=state, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
-                        cache_indices=read, out_indices=write), x.device)
-    y = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    dev = x.device
+    _on(dev, state=state, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
+        cache_indices=read, out_indices=write)
+    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
     if n == 0:
         return y
     desc.B, desc.T, desc.N, desc.dt_softplus = n, 1, n, int(bool(dt_softplus))
     desc.state_lines = state.shape[0]
-    st = gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, read, write, y)
+    st = gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, read, write, y,
+                                    _current(dev))
     if st != 0:
         raise GdnError(st, "gdn_selective_state_update")
     return y
@@ -363,7 +389,7 @@ def gdn_causal_conv1d_bwd(desc, x, weight, bias, initial, cu_seqlens, dy, dfinal
                           dbias, dinitial, workspace, workspace_bytes, stream=None) -> int:
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_causal_conv1d_bwd(
-        ctypes.byref(desc), *map(_ptr, (x, weight, bias, initial, cu_seqlens, dy, dfinal, dx,
+        ctypes.byref(desc), *_addresses((x, weight, bias, initial, cu_seqlens, dy, dfinal, dx,
                                         dweight, dbias, dinitial, workspace)), workspace_bytes,
         _stream(stream)))
 
@@ -375,15 +401,13 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
     [N, W - 1, C]: the inputs before each sequence, its line before the forward (None: zeros).
     Returns (dx in x's dtype, dweight [C, W] and dbias [C] fp32, dinitial_state in x's dtype);
     dbias and dinitial_state are None where the input is None."""
-    import torch
     _validate_conv(x, weight, bias, None, None, None, cu_seqlens)
     _need(activation in ACTIVATIONS, ValueError, "activation must be None, 'none' or 'silu'")
     B, T, C = x.shape
     W = weight.shape[1]
     cu, N = _sequences(x, cu_seqlens)
-    _need(isinstance(dy, torch.Tensor) and dy.dtype == x.dtype, TypeError,
-          "dy must be a tensor of x's dtype %s" % x.dtype)
-    _need(dy.shape == x.shape, ValueError, "dy must have x's shape %s" % list(x.shape))
+    _need(dy is not None, TypeError, "dy is required")
+    _like("dy", dy, x)
     lines = dict(initial_state=initial_state, dfinal_state=dfinal_state)
     for name, t in lines.items():
         if t is not None:
@@ -392,7 +416,7 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
             _need(tuple(t.shape) == (N, W - 1, C), ValueError,
                   "%s must be [N, W - 1, C] = %s" % (name, [N, W - 1, C]))
             lines[name] = t.contiguous()
-    _check_devices(dict(x=x, dy=dy, workspace=workspace, **lines), x.device)
+    _on(x.device, x=x, dy=dy, workspace=workspace, **lines)
     weight, dy = weight.contiguous(), dy.contiguous()
     bias = None if bias is None else bias.contiguous()
     desc = GdnConvDesc(B=B, T=T, N=N, channels=C, width=W, dtype=_code(x),
@@ -410,7 +434,8 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
     if need and (ws is None or ws.numel() < need):
         ws = torch.empty(need, device=dev, dtype=torch.uint8)
     st = gdn_causal_conv1d_bwd(desc, x, weight, bias, first, cu, dy, lines["dfinal_state"], dx,
-                               dweight, dbias, dinit, ws, 0 if ws is None else ws.numel())
+                               dweight, dbias, dinit, ws, 0 if ws is None else ws.numel(),
+                               _current(dev))
     if st != 0:
         raise GdnError(st, "gdn_causal_conv1d_bwd")
     return dx, dweight, dbias, dinit
@@ -428,7 +453,7 @@ def gdn_group_norm_workspace_size(desc: GdnNormDesc, backward=False) -> int:
 def gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, stream=None) -> int:
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_group_norm_fwd(
-        ctypes.byref(desc), *map(_ptr, (x, weight, bias, gate, y, mean, rstd)),
+        ctypes.byref(desc), *_addresses((x, weight, bias, gate, y, mean, rstd)),
         _stream(stream)))
 
 
@@ -436,12 +461,11 @@ def gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight,
                        stream=None) -> int:
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     return int(load().gdn_group_norm_bwd(
-        ctypes.byref(desc), *map(_ptr, (x, weight, bias, gate, mean, rstd, dy, dx, dweight,
+        ctypes.byref(desc), *_addresses((x, weight, bias, gate, mean, rstd, dy, dx, dweight,
                                         dbias, dgate)), _stream(stream)))
 
 
 def _norm_operands(x, num_groups, weight, bias, eps, activation, gate):
-    import torch
     _need(isinstance(x, torch.Tensor), TypeError, "x must be a torch tensor")
     code = _code(x)
     _need(code is not None, TypeError, "x must be bf16 or fp32, got %s" % x.dtype)
@@ -453,10 +477,8 @@ def _norm_operands(x, num_groups, weight, bias, eps, activation, gate):
           "num_groups must divide the %d channels, got %r" % (C, num_groups))
     _need(eps >= 0, ValueError, "eps must not be negative")
     weight, bias = _f32("weight", weight, (C,)), _f32("bias", bias, (C,))
+    _like("gate", gate, x)
     if gate is not None:
-        _need(isinstance(gate, torch.Tensor) and gate.dtype == x.dtype, TypeError,
-              "gate must be a tensor of x's dtype %s" % x.dtype)
-        _need(gate.shape == x.shape, ValueError, "gate must have x's shape %s" % list(x.shape))
         gate = gate.contiguous()
     positions = 1
     for n in x.shape[1:-1]:
@@ -475,16 +497,15 @@ def group_norm(x, num_groups, weight=None, bias=None, eps=1e-5, activation=None,
     [channels] fp32 or None; gate: x's shape and dtype, or None.  y = act(u) without a gate and
     u act(gate) with one, u the normalised, scaled and shifted x.  Returns (y, mean, rstd), mean
     and rstd [samples, num_groups] fp32."""
-    import torch
     desc, x, weight, bias, gate = _norm_operands(x, num_groups, weight, bias, eps, activation,
                                                  gate)
     dev = x.device
-    _check_devices(dict(x=x, weight=weight, bias=bias, gate=gate, workspace=workspace), dev)
+    _on(dev, x=x, weight=weight, bias=bias, gate=gate, workspace=workspace)
     y = torch.empty(x.shape, device=dev, dtype=x.dtype)
     mean = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
     rstd = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc), workspace, dev)  # noqa: F841
-    st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd)
+    st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, _current(dev))
     if st != 0:
         raise GdnError(st, "gdn_group_norm_fwd")
     return y, mean, rstd
@@ -495,24 +516,22 @@ def group_norm_bwd(dy, x, num_groups, mean, rstd, weight=None, bias=None, activa
     """Gradients of group_norm's inputs on the current stream, from dy, the forward's inputs and
     its mean and rstd.  Returns (dx, dweight, dbias, dgate): dx and dgate in x's dtype, dweight
     and dbias [channels] fp32; None where the input is None."""
-    import torch
     desc, x, weight, bias, gate = _norm_operands(x, num_groups, weight, bias, 0.0, activation,
                                                  gate)
-    _need(isinstance(dy, torch.Tensor) and dy.dtype == x.dtype, TypeError,
-          "dy must be a tensor of x's dtype %s" % x.dtype)
-    _need(dy.shape == x.shape, ValueError, "dy must have x's shape %s" % list(x.shape))
+    _need(dy is not None, TypeError, "dy is required")
+    _like("dy", dy, x)
     _need(mean is not None and rstd is not None, TypeError, "mean and rstd are required")
     mean = _f32("mean", mean, (x.shape[0], num_groups))
     rstd = _f32("rstd", rstd, (x.shape[0], num_groups))
     dev = x.device
-    _check_devices(dict(x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate,
-                        workspace=workspace), dev)
+    _on(dev, x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate,
+        workspace=workspace)
     dy = dy.contiguous()
     new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)  # noqa: E731
     dx, dweight, dbias, dgate = map(new, (x, weight, bias, gate))
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc, True), workspace, dev)  # noqa: F841
     st = gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight, dbias,
-                            dgate)
+                            dgate, _current(dev))
     if st != 0:
         raise GdnError(st, "gdn_group_norm_bwd")
     return dx, dweight, dbias, dgate

@@ -165,7 +165,7 @@ BwdLayout bwd_layout(const gdn::ScanProblem& p) {
 // still gives 1024 workgroups (a block costs W - 1 tokens more of reading and a row of partial
 // sums), at least 8.
 void plan_conv_bwd(gdn::ConvBwdProblem* p) {
-  const long long slabs = (p->C / 8 + 255) / 256;
+  const long long slabs = (p->C / 4 + 255) / 256;
   p->tokens = 256;
   while (p->tokens > 8 && (p->Ttot + p->tokens - 1LL) / p->tokens * slabs < 1024)
     p->tokens >>= 1;
@@ -191,7 +191,7 @@ gdn_status check_conv_bwd(const gdn_conv_desc* d, bool packed, gdn::ConvBwdProbl
   p->f32 = d->dtype == GDN_F32;
   p->silu = d->activation == GDN_ACT_SILU;
   plan_conv_bwd(p);
-  if ((long long)p->N * (p->C / 8) >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
+  if ((long long)p->N * (p->C / 4) >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 
@@ -378,6 +378,8 @@ gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, cons
       !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(cache_indices, 4) ||
       !aligned(out_indices, 4))
     return GDN_ERR_INVALID_ARG;
+  // one workgroup for each 16 channels of a sequence, at most
+  if ((long long)d->B * ((p.C + 15) / 16) >= (1LL << 24)) return GDN_ERR_UNSUPPORTED;
   gdn::ScanStepProblem q;
   q.B = d->B;
   q.C = p.C;
@@ -388,6 +390,7 @@ gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, cons
   q.f32 = p.f32;
   q.softplus = p.softplus;
   q.vec4 = p.S % 4 == 0 && aligned(state, 16) && aligned(A, 16);
+  q.wide = q.vec4 && p.sb % 4 == 0 && p.sc % 4 == 0 && aligned(Bm, 4 * e) && aligned(Cm, 4 * e);
   q.state = state;
   q.x = x;
   q.dt = dt;

@@ -6,7 +6,7 @@
 //              final state where x~[e] is one of its last W - 1 entries
 //   dw[i]    = sum_t du[t] x~[t + i],   dbias = sum_t du[t]
 //
-// One thread per 8 channels and a block of tokens, walked in order with the last W - 1 inputs
+// One thread per 4 channels and a block of tokens, walked in order with the last W - 1 inputs
 // and du in registers: x and dy are read once (but for the W - 1 tokens after a block, whose du
 // its last outputs need), dx is written once.  Each block leaves its share of dw and dbias as a
 // partial sum; a second kernel adds them in order.
@@ -19,7 +19,8 @@ namespace gdn {
 
 namespace {
 
-constexpr int kVec = 8;
+constexpr int kVec = 4;    // channels a thread: 8 would take 183 registers (2 waves a SIMD)
+constexpr int kGroup = 4;  // tokens whose loads are issued together
 constexpr int kThreads = 256;
 
 struct Span {
@@ -54,9 +55,9 @@ template <int W, typename E>
 __device__ __forceinline__ void load_input(const ConvBwdProblem& p, int n, int bos, int t, int c0,
                                            float* v) {
   if (t >= bos) {
-    Vec8<E>::load(static_cast<const E*>(p.x) + (long)t * p.C + c0, v);
+    Vec4<E>::load(static_cast<const E*>(p.x) + (long)t * p.C + c0, v);
   } else if (p.init) {
-    Vec8<E>::load(static_cast<const E*>(p.init) +
+    Vec4<E>::load(static_cast<const E*>(p.init) +
                       ((long)n * (W - 1) + (W - 1) + (t - bos)) * p.C + c0, v);
   } else {
 #pragma unroll
@@ -120,8 +121,11 @@ __global__ __launch_bounds__(kThreads) void k_conv1d_bwd(ConvBwdProblem p) {
 #pragma unroll
       for (int v = 0; v < kVec; ++v) du[i][v] = 0.f;
     }
-    // the initial window sits one place late: the first step moves it
-    for (int tt = t; tt < end + W - 1; ++tt) {
+    // the initial window sits one place late: a step moves it before it takes a token in
+    const E* xs = static_cast<const E*>(p.x) + c0;
+    const E* dys = static_cast<const E*>(p.dy) + c0;
+    E* dxs = static_cast<E*>(p.dx) + c0;
+    auto shift = [&]() {
 #pragma unroll
       for (int i = 0; i + 1 < W; ++i) {
 #pragma unroll
@@ -130,48 +134,86 @@ __global__ __launch_bounds__(kThreads) void k_conv1d_bwd(ConvBwdProblem p) {
           du[i][v] = du[i + 1][v];
         }
       }
-      if (tt < last) {
-        float dy[kVec];
-        Vec8<E>::load(static_cast<const E*>(p.x) + (long)tt * p.C + c0, win[W - 1]);
-        Vec8<E>::load(static_cast<const E*>(p.dy) + (long)tt * p.C + c0, dy);
-        make_du<W>(w, b, win, dy, p.silu, du[W - 1]);
-        if (tt < end) {
+    };
+    auto take = [&](const typename Vec4<E>::raw& rx, const typename Vec4<E>::raw& rd, bool own) {
+      float dy[kVec];
+      Vec4<E>::wide(rx, win[W - 1]);
+      Vec4<E>::wide(rd, dy);
+      make_du<W>(w, b, win, dy, p.silu, du[W - 1]);
+      if (own) {
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            db[v] += du[W - 1][v];
+        for (int v = 0; v < kVec; ++v) {
+          db[v] += du[W - 1][v];
 #pragma unroll
-            for (int i = 0; i < W; ++i) dw[i][v] = fmaf(du[W - 1][v], win[i][v], dw[i][v]);
-          }
+          for (int i = 0; i < W; ++i) dw[i][v] = fmaf(du[W - 1][v], win[i][v], dw[i][v]);
         }
+      }
+    };
+    auto emit = [&](int o, bool tail) {  // dx[o] = sum_i w[i] du[o + W - 1 - i]
+      float out[kVec];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        out[v] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) out[v] = fmaf(w[i][v], du[W - 1 - i][v], out[v]);
+      }
+      const int j = o - (sp.eos - (W - 1));  // its place among the final state's entries
+      if (tail && p.dfinal && j >= 0) {
+        float f[kVec];
+        Vec4<E>::load(static_cast<const E*>(p.dfinal) + ((long)n * (W - 1) + j) * p.C + c0, f);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) out[v] += f[v];
+      }
+      Vec4<E>::store(dxs + (long)o * p.C, out);
+    };
+    int tt = t;
+    for (; tt < min(t + W - 1, end); ++tt) {  // the first tokens end no output of this block
+      shift();
+      take(Vec4<E>::load_raw(xs + (long)tt * p.C), Vec4<E>::load_raw(dys + (long)tt * p.C), true);
+    }
+    // whole groups, the next group's loads issued before this one computes
+    const int groups = (end - tt) / kGroup;
+    typename Vec4<E>::raw rx[kGroup], rd[kGroup];
+    auto fetch = [&](int at) {
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        rx[i] = Vec4<E>::load_raw(xs + (long)(at + i) * p.C);
+        rd[i] = Vec4<E>::load_raw(dys + (long)(at + i) * p.C);
+      }
+    };
+    if (groups > 0) fetch(tt);
+    for (int gi = 0; gi < groups; ++gi, tt += kGroup) {
+      typename Vec4<E>::raw cx[kGroup], cd[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        cx[i] = rx[i];
+        cd[i] = rd[i];
+      }
+      if (gi + 1 < groups) fetch(tt + kGroup);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        shift();
+        take(cx[i], cd[i], true);
+        emit(tt + i - (W - 1), false);  // before the sequence's last W - 1 tokens
+      }
+    }
+    for (; tt < end + W - 1; ++tt) {
+      shift();
+      if (tt < last) {
+        take(Vec4<E>::load_raw(xs + (long)tt * p.C), Vec4<E>::load_raw(dys + (long)tt * p.C),
+             tt < end);
       } else {
 #pragma unroll
         for (int v = 0; v < kVec; ++v) du[W - 1][v] = 0.f;
       }
-      const int o = tt - (W - 1);  // dx[o] = sum_i w[i] du[o + W - 1 - i]
-      if (o >= t && o < end) {
-        float out[kVec];
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-          out[v] = 0.f;
-#pragma unroll
-          for (int i = 0; i < W; ++i) out[v] = fmaf(w[i][v], du[W - 1 - i][v], out[v]);
-        }
-        const int j = o - (sp.eos - (W - 1));  // its place among the final state's entries
-        if (p.dfinal && j >= 0) {
-          float f[kVec];
-          Vec8<E>::load(static_cast<const E*>(p.dfinal) + ((long)n * (W - 1) + j) * p.C + c0, f);
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) out[v] += f[v];
-        }
-        Vec8<E>::store(static_cast<E*>(p.dx) + (long)o * p.C + c0, out);
-      }
+      if (tt - (W - 1) >= t && tt - (W - 1) < end) emit(tt - (W - 1), true);
     }
     t = end;
   }
   float* part = p.part + (long)blockIdx.x * (W + 1) * p.C + c0;
 #pragma unroll
-  for (int i = 0; i < W; ++i) Vec8<float>::store(part + (long)i * p.C, dw[i]);
-  Vec8<float>::store(part + (long)W * p.C, db);
+  for (int i = 0; i < W; ++i) Vec4<float>::store(part + (long)i * p.C, dw[i]);
+  Vec4<float>::store(part + (long)W * p.C, db);
 }
 
 // The gradient of the W - 1 inputs before each sequence: e < W - 1 of x~.
@@ -197,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_conv1d_dinit(ConvBwdProblem p) {
 #pragma unroll
   for (int e = 0; e < W - 1; ++e)
     if (p.dfinal && e >= len)
-      Vec8<E>::load(static_cast<const E*>(p.dfinal) + ((long)n * (W - 1) + e - len) * p.C + c0,
+      Vec4<E>::load(static_cast<const E*>(p.dfinal) + ((long)n * (W - 1) + e - len) * p.C + c0,
                     acc[e]);
 #pragma unroll
   for (int i = 0; i + 1 < W; ++i)
@@ -210,8 +252,8 @@ __global__ __launch_bounds__(kThreads) void k_conv1d_dinit(ConvBwdProblem p) {
       for (int i = 0; i + 1 < W; ++i)
 #pragma unroll
         for (int v = 0; v < kVec; ++v) win[i][v] = win[i + 1][v];
-      Vec8<E>::load(static_cast<const E*>(p.x) + (long)(sp.bos + t) * p.C + c0, win[W - 1]);
-      Vec8<E>::load(static_cast<const E*>(p.dy) + (long)(sp.bos + t) * p.C + c0, dy);
+      Vec4<E>::load(static_cast<const E*>(p.x) + (long)(sp.bos + t) * p.C + c0, win[W - 1]);
+      Vec4<E>::load(static_cast<const E*>(p.dy) + (long)(sp.bos + t) * p.C + c0, dy);
       make_du<W>(w, b, win, dy, p.silu, du);
 #pragma unroll
       for (int e = 0; e < W - 1; ++e)  // tap i = e - t
@@ -223,37 +265,19 @@ __global__ __launch_bounds__(kThreads) void k_conv1d_dinit(ConvBwdProblem p) {
   }
 #pragma unroll
   for (int e = 0; e < W - 1; ++e)
-    Vec8<E>::store(static_cast<E*>(p.dinit) + ((long)n * (W - 1) + e) * p.C + c0, acc[e]);
+    Vec4<E>::store(static_cast<E*>(p.dinit) + ((long)n * (W - 1) + e) * p.C + c0, acc[e]);
 }
 
-// dw and dbias from the blocks' partial sums: a workgroup takes 64 channels of one row, its four
-// waves every fourth block.
-__global__ __launch_bounds__(256) void k_conv1d_sum(const float* part, float* dweight,
-                                                    float* dbias, int blocks, int C, int W) {
-  __shared__ float s[4][64];
-  const int lane = lane_id(), w = wave_id();
-  const int c = blockIdx.x * 64 + lane, row = blockIdx.y;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (c < C) {
-    const float* q = part + (long)row * C + c;
-    const long step = (long)(W + 1) * C;
-    int i = w;
-    for (; i + 12 < blocks; i += 16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += q[(long)(i + 4 * j) * step];
-    }
-    for (; i < blocks; i += 4) v[0] += q[(long)i * step];
-  }
-  s[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
-  __syncthreads();
-  if (w == 0 && c < C) {
-    const float r = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
-    if (row < W) {
-      if (dweight) dweight[(long)c * W + row] = r;
-    } else if (dbias) {
-      dbias[c] = r;
-    }
-  }
+// dw and dbias from the blocks' partial sums [blocks][W + 1][C].
+__global__ __launch_bounds__(kColumnThreads) void k_conv1d_sum(const float* part, float* dweight,
+                                                               float* dbias, int blocks, int C,
+                                                               int W) {
+  const int row = blockIdx.y;
+  float* to = row < W ? dweight : dbias;
+  if (!to) return;
+  const int c = blockIdx.x * 64 + lane_id();
+  const float r = column_sum(part + (long)row * C, (long)(W + 1) * C, blocks, c, C);
+  if (threadIdx.x < 64 && c < C) to[row < W ? (long)c * W + row : c] = r;
 }
 
 template <int W, typename E>
@@ -266,7 +290,7 @@ hipError_t launch_w(const ConvBwdProblem& p, hipStream_t st) {
     k_conv1d_dinit<W, E><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
   }
   if (p.dweight || p.dbias)
-    k_conv1d_sum<<<dim3((p.C + 63) / 64, W + 1), 256, 0, st>>>(p.part, p.dweight, p.dbias,
+    k_conv1d_sum<<<dim3((p.C + 63) / 64, W + 1), kColumnThreads, 0, st>>>(p.part, p.dweight, p.dbias,
                                                                p.blocks, p.C, W);
   return hipGetLastError();
 }

@@ -529,29 +529,14 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_apply(NormProblem p, MapP
   }
 }
 
-// dw and db from rows [rows][2][C] of partial sums: 64 channels a workgroup, its four waves every
-// fourth row.
-__global__ __launch_bounds__(kThreads) void k_norm_params(const float* ws, float* dw, float* db,
-                                                          long rows, int C) {
-  __shared__ float s[4][64];
-  const int lane = lane_id(), w = wave_id();
-  const int c = blockIdx.x * 64 + lane;
+// dw and db from rows [rows][2][C] of partial sums.
+__global__ __launch_bounds__(kColumnThreads) void k_norm_params(const float* ws, float* dw,
+                                                                float* db, long rows, int C) {
   float* to = blockIdx.y == 0 ? dw : db;
   if (!to) return;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (c < C) {
-    const float* q = ws + (long)blockIdx.y * C + c;
-    const long step = 2L * C;
-    long i = w;
-    for (; i + 12 < rows; i += 16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += q[(i + 4 * j) * step];
-    }
-    for (; i < rows; i += 4) v[0] += q[i * step];
-  }
-  s[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
-  __syncthreads();
-  if (w == 0 && c < C) to[c] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+  const int c = blockIdx.x * 64 + lane_id();
+  const float r = column_sum(ws + (long)blockIdx.y * C, 2L * C, rows, c, C);
+  if (threadIdx.x < 64 && c < C) to[c] = r;
 }
 
 // --- one workgroup for each (sample, group) ----------------------------------------------------
@@ -697,7 +682,7 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t st) {
     else if (k == 2) k_norm_rows_bwd<E, VEC, 2><<<grid, kThreads, 0, st>>>(p, r);
     else k_norm_rows_bwd<E, VEC, 4><<<grid, kThreads, 0, st>>>(p, r);
     if (p.dweight || p.dbias)
-      k_norm_params<<<dim3((p.C + 63) / 64, 2), kThreads, 0, st>>>(
+      k_norm_params<<<dim3((p.C + 63) / 64, 2), kColumnThreads, 0, st>>>(
           p.ws, p.dweight, p.dbias, (long)grid.x * (kThreads / r.lps / r.gp), p.C);
     return hipGetLastError();
   }
@@ -708,7 +693,7 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t st) {
   k_norm_bwd_join<<<p.N * p.G, kThreads, 0, st>>>(p, q, sums);
   k_norm_bwd_apply<E, VEC><<<grid, kThreads, 0, st>>>(p, q, sums);
   if (p.dweight || p.dbias)
-    k_norm_params<<<dim3((p.C + 63) / 64, 2), kThreads, 0, st>>>(p.ws, p.dweight, p.dbias,
+    k_norm_params<<<dim3((p.C + 63) / 64, 2), kColumnThreads, 0, st>>>(p.ws, p.dweight, p.dbias,
                                                                  (long)p.N * q.slabs, p.C);
   return hipGetLastError();
 }
@@ -756,7 +741,7 @@ hipError_t launch_norm_fwd(const NormProblem& p, hipStream_t st) {
 
 hipError_t launch_norm_no_params(const NormProblem& p, hipStream_t st) {
   if (!p.dweight && !p.dbias) return hipSuccess;
-  k_norm_params<<<dim3((p.C + 63) / 64, 2), kThreads, 0, st>>>(nullptr, p.dweight, p.dbias, 0,
+  k_norm_params<<<dim3((p.C + 63) / 64, 2), kColumnThreads, 0, st>>>(nullptr, p.dweight, p.dbias, 0,
                                                                p.C);
   return hipGetLastError();
 }

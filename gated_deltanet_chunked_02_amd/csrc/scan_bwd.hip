@@ -598,28 +598,19 @@ __global__ __launch_bounds__(256) void k_scan_bwd_bc(const float* bcp, E* dB, E*
   (k < Sp ? dB : dC)[(i / row) * S + s] = (E)v;
 }
 
-// Sums over the chunk slots of rows [slots][rows][C]: dA (transposed to [C, S]) or dD and
+// Sums over the chunk slots of rows [slots][rows][C]: dA (transposed to [C, S]), dD and
 // d(dt_bias).
-__global__ __launch_bounds__(256) void k_scan_bwd_params(const float* dAp, const float* dvp,
-                                                         float* dA, float* dD, float* dbias,
-                                                         int slots, int C, int S) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(kColumnThreads) void k_scan_bwd_params(
+    const float* dAp, const float* dvp, float* dA, float* dD, float* dbias, int slots, int C,
+    int S) {
   const int s = blockIdx.y;  // S rows of dA, then dD, d(dt_bias)
-  if (c >= C) return;
   const bool vec = s >= S;
-  float* to = !vec ? dA + (long)c * S + s : s == S ? dD : dbias;
+  float* to = !vec ? dA : s == S ? dD : dbias;
   if (!to) return;
-  const float* p = vec ? dvp + (long)(s - S) * C + c : dAp + (long)s * C + c;
-  const long stride = (long)(vec ? 2 : S) * C;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  int i = 0;
-  for (; i + 4 <= slots; i += 4) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += p[(long)(i + j) * stride];
-  }
-  for (; i < slots; ++i) v[0] += p[(long)i * stride];
-  const float r = (v[0] + v[1]) + (v[2] + v[3]);
-  if (vec) to[c] = r; else *to = r;
+  const int c = blockIdx.x * 64 + lane_id();
+  const float r = vec ? column_sum(dvp + (long)(s - S) * C, 2L * C, slots, c, C)
+                      : column_sum(dAp + (long)s * C, (long)S * C, slots, c, C);
+  if (threadIdx.x < 64 && c < C) to[vec ? c : (long)c * S + s] = r;
 }
 
 template <int NW, bool MULTI, typename E>
@@ -628,7 +619,7 @@ hipError_t launch_cfg(const ScanProblem& p, const ScanBwd& b, const BwdArgs& a, 
   // lengths then load the XCDs alike
   const unsigned grid = (unsigned)p.slots * a.nb;
   if (p.slots == 0) {  // no sequences: the parameters' gradients are zero
-    k_scan_bwd_params<<<dim3((p.C + 255) / 256, p.S + 2), 256, 0, st>>>(
+    k_scan_bwd_params<<<dim3((p.C + 63) / 64, p.S + 2), kColumnThreads, 0, st>>>(
         b.dAp, b.dvp, b.dA, b.dD, b.dbias, 0, p.C, p.S);
     return hipGetLastError();
   }
@@ -647,7 +638,7 @@ hipError_t launch_cfg(const ScanProblem& p, const ScanBwd& b, const BwdArgs& a, 
   if (n > 0)
     k_scan_bwd_bc<E><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
         b.bcp, (E*)b.dB, (E*)b.dC, p.Ttot, p.G, p.S, p.Sp, p.nblk);
-  k_scan_bwd_params<<<dim3((p.C + 255) / 256, p.S + 2), 256, 0, st>>>(
+  k_scan_bwd_params<<<dim3((p.C + 63) / 64, p.S + 2), kColumnThreads, 0, st>>>(
       b.dAp, b.dvp, b.dA, b.dD, b.dbias, p.slots, p.C, p.S);
   return hipGetLastError();
 }

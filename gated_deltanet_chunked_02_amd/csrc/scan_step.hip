@@ -4,94 +4,160 @@
 //   h' = exp(step A) h + step x B,   y = (sum_s C h' + D x) silu(z)
 //
 // so the pool's bytes bound it.  LPC lanes share a channel and read VEC states each (16 bytes
-// when S is a multiple of 4 and the pool and A are aligned to that), so a wave's loads of the pool and of A are contiguous; y is summed
-// over the LPC lanes.
+// when S is a multiple of 4 and the pool and A are aligned to that), so a wave's loads of the pool
+// and of A are contiguous; y is summed over the LPC lanes.  A workgroup keeps to its channels for
+// `seqs` sequences, so A is loaded once for them, and every sequence's loads are issued before the
+// one before it computes.
 #include "ssm_device.h"
 
 namespace gdn {
 
 namespace {
 
-template <typename E, int VEC, int LPC>
-__global__ __launch_bounds__(256) void k_scan_step(ScanStepProblem p) {
+// VEC values of B or C (WIDE: their rows are aligned to VEC values).
+template <typename E, int VEC, bool WIDE>
+__device__ __forceinline__ void load_bc(const E* p, float* v) {
+  if constexpr (WIDE && VEC == 4) {
+    typedef E vec __attribute__((ext_vector_type(4)));
+    const vec r = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = (float)r[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = (float)p[k];
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_states(const float* p, float* v) {
+  if constexpr (VEC == 4) {
+    const f32x4 r = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = r[k];
+  } else {
+    v[0] = p[0];
+  }
+}
+
+// NV: vectors of states a lane holds (LPC VEC NV >= S).
+template <typename E, int VEC, int LPC, int NV, bool WIDE>
+__global__ __launch_bounds__(256) void k_scan_step(ScanStepProblem p, int seqs) {
   constexpr int CPB = 256 / LPC;  // channels of a workgroup
-  const int b = blockIdx.y + gridDim.y * blockIdx.z;
-  if (b >= p.B) return;
-  const int c = blockIdx.x * CPB + (int)threadIdx.x / LPC;
+  const int blocks = (p.C + CPB - 1) / CPB;
+  const int group = blockIdx.x / blocks;  // of sequences
+  const int c = (blockIdx.x - group * blocks) * CPB + (int)threadIdx.x / LPC;
   const int l = threadIdx.x % LPC;
   if (c >= p.C) return;  // LPC divides 64: a channel's lanes leave together
   const int g = c / p.per;
-  const int rl = p.read ? p.read[b] : b;
-  const int wl = p.write ? p.write[b] : rl;
-  const float* hin = rl >= 0 && rl < p.lines ? p.state + ((long)rl * p.C + c) * p.S : nullptr;
-  float* hout = wl >= 0 && wl < p.lines ? p.state + ((long)wl * p.C + c) * p.S : nullptr;
-  const E* Bm = static_cast<const E*>(p.Bm) + b * p.sb + (long)g * p.S;
-  const E* Cm = static_cast<const E*>(p.Cm) + b * p.sc + (long)g * p.S;
-  const float* A = p.A + (long)c * p.S;
-  const float x = (float)static_cast<const E*>(p.x)[b * p.sx + c];
-  float step = (float)static_cast<const E*>(p.dt)[b * p.sdt + c] + (p.bias ? p.bias[c] : 0.f);
-  if (p.softplus) step = softplus_f32(step);
-  const float dx = step * x;
-  float y = 0.f;
-  for (int s = l * VEC; s < p.S; s += LPC * VEC) {
-    float h[VEC], av[VEC];
-    if constexpr (VEC == 4) {
-      const float4 a4 = *reinterpret_cast<const float4*>(A + s);
-      const float4 h4 = hin ? *reinterpret_cast<const float4*>(hin + s) : make_float4(0, 0, 0, 0);
-      av[0] = a4.x; av[1] = a4.y; av[2] = a4.z; av[3] = a4.w;
-      h[0] = h4.x; h[1] = h4.y; h[2] = h4.z; h[3] = h4.w;
-    } else {
-      av[0] = A[s];
-      h[0] = hin ? hin[s] : 0.f;
-    }
+  float A2[NV][VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      h[k] = fmaf(__builtin_amdgcn_exp2f(step * (av[k] * kLog2e)), h[k], dx * (float)Bm[s + k]);
-      y = fmaf((float)Cm[s + k], h[k], y);
-    }
-    if (hout) {
-      if constexpr (VEC == 4)
-        *reinterpret_cast<float4*>(hout + s) = make_float4(h[0], h[1], h[2], h[3]);
-      else
-        hout[s] = h[0];
-    }
+  for (int j = 0; j < NV; ++j) {
+    const int s = (j * LPC + l) * VEC;
+    if (s < p.S) load_states<VEC>(p.A + (long)c * p.S + s, A2[j]);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) A2[j][k] = s < p.S ? A2[j][k] * kLog2e : 0.f;
   }
+  const float bias = p.bias ? p.bias[c] : 0.f, Dc = p.D ? p.D[c] : 0.f;
+
+  struct In {
+    float h[NV][VEC], b[NV][VEC], c[NV][VEC], x, dt, z;
+    float* to;
+  };
+  auto load = [&](int b, In& in) {
+    const int rl = p.read ? p.read[b] : b;
+    const int wl = p.write ? p.write[b] : rl;
+    const float* from =
+        rl >= 0 && rl < p.lines ? p.state + ((long)rl * p.C + c) * p.S : nullptr;
+    in.to = wl >= 0 && wl < p.lines ? p.state + ((long)wl * p.C + c) * p.S : nullptr;
+    const E* Bm = static_cast<const E*>(p.Bm) + b * p.sb + (long)g * p.S;
+    const E* Cm = static_cast<const E*>(p.Cm) + b * p.sc + (long)g * p.S;
 #pragma unroll
-  for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor(y, o);
-  if (l == 0) {
-    if (p.D) y = fmaf(p.D[c], x, y);
-    if (p.z) {
-      const float z = (float)static_cast<const E*>(p.z)[b * p.sz + c];
-      y *= z * sigmoid_f32(z);
+    for (int j = 0; j < NV; ++j) {
+      const int s = (j * LPC + l) * VEC;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) in.h[j][k] = in.b[j][k] = in.c[j][k] = 0.f;
+      if (s < p.S) {
+        if (from) load_states<VEC>(from + s, in.h[j]);
+        load_bc<E, VEC, WIDE>(Bm + s, in.b[j]);
+        load_bc<E, VEC, WIDE>(Cm + s, in.c[j]);
+      }
     }
-    static_cast<E*>(p.y)[(long)b * p.C + c] = (E)y;
+    in.x = (float)static_cast<const E*>(p.x)[b * p.sx + c];
+    in.dt = (float)static_cast<const E*>(p.dt)[b * p.sdt + c];
+    in.z = p.z ? (float)static_cast<const E*>(p.z)[b * p.sz + c] : 0.f;
+  };
+  const int first = group * seqs, end = min(first + seqs, p.B);
+  In in;
+  load(first, in);
+  for (int b = first; b < end; ++b) {
+    In next;
+    if (b + 1 < end) load(b + 1, next);
+    float step = in.dt + bias;
+    if (p.softplus) step = softplus_f32(step);
+    const float dx = step * in.x;
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int s = (j * LPC + l) * VEC;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        in.h[j][k] = fmaf(__builtin_amdgcn_exp2f(step * A2[j][k]), in.h[j][k], dx * in.b[j][k]);
+        if (s < p.S) y = fmaf(in.c[j][k], in.h[j][k], y);
+      }
+      if (in.to && s < p.S) {
+        if constexpr (VEC == 4)
+          *reinterpret_cast<f32x4*>(in.to + s) =
+              f32x4{in.h[j][0], in.h[j][1], in.h[j][2], in.h[j][3]};
+        else
+          in.to[s] = in.h[j][0];
+      }
+    }
+#pragma unroll
+    for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor(y, o);
+    if (l == 0) {
+      y = fmaf(Dc, in.x, y);
+      if (p.z) y *= in.z * sigmoid_f32(in.z);
+      static_cast<E*>(p.y)[(long)b * p.C + c] = (E)y;
+    }
+    in = next;
   }
 }
 
-template <typename E, int VEC, int LPC>
+template <typename E, int VEC, int LPC, int NV, bool WIDE>
 hipError_t launch_cfg(const ScanStepProblem& p, hipStream_t st) {
-  const int by = p.B < 32768 ? p.B : 32768;
-  const dim3 grid((p.C + 256 / LPC - 1) / (256 / LPC), by, (p.B + by - 1) / by);
-  k_scan_step<E, VEC, LPC><<<grid, 256, 0, st>>>(p);
+  const int blocks = (p.C + 256 / LPC - 1) / (256 / LPC);
+  // four sequences a workgroup share its A where that leaves eight workgroups a CU
+  const int seqs = (long)blocks * p.B >= 4 * 2048 ? 4 : 1;
+  k_scan_step<E, VEC, LPC, NV, WIDE>
+      <<<(unsigned)blocks * ((p.B + seqs - 1) / seqs), 256, 0, st>>>(p, seqs);
   return hipGetLastError();
 }
 
-template <typename E, int VEC>
+template <typename E, int VEC, bool WIDE>
 hipError_t launch_vec(const ScanStepProblem& p, hipStream_t st) {
-  const int q = p.S / VEC;  // the largest power of two of lanes that all have states
-  if (q >= 16) return launch_cfg<E, VEC, 16>(p, st);
-  if (q >= 8) return launch_cfg<E, VEC, 8>(p, st);
-  if (q >= 4) return launch_cfg<E, VEC, 4>(p, st);
-  if (q >= 2) return launch_cfg<E, VEC, 2>(p, st);
-  return launch_cfg<E, VEC, 1>(p, st);
+  // lanes a channel: the smallest power of two that holds the vectors, at most 16
+  const int q = (p.S + VEC - 1) / VEC;
+  if (q <= 1) return launch_cfg<E, VEC, 1, 1, WIDE>(p, st);
+  if (q <= 2) return launch_cfg<E, VEC, 2, 1, WIDE>(p, st);
+  if (q <= 4) return launch_cfg<E, VEC, 4, 1, WIDE>(p, st);
+  if (q <= 8) return launch_cfg<E, VEC, 8, 1, WIDE>(p, st);
+  if (q <= 16) return launch_cfg<E, VEC, 16, 1, WIDE>(p, st);
+  if (q <= 32) return launch_cfg<E, VEC, 16, 2, WIDE>(p, st);
+  if (VEC == 4 || q <= 64) return launch_cfg<E, VEC, 16, 4, WIDE>(p, st);  // dstate <= 256
+  if constexpr (VEC == 1) return launch_cfg<E, 1, 16, 16, false>(p, st);
+  return hipErrorInvalidValue;
+}
+
+template <typename E>
+hipError_t launch_e(const ScanStepProblem& p, hipStream_t st) {
+  if (!p.vec4) return launch_vec<E, 1, false>(p, st);
+  return p.wide ? launch_vec<E, 4, true>(p, st) : launch_vec<E, 4, false>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_scan_step(const ScanStepProblem& p, hipStream_t st) {
-  if (p.vec4)
-    return p.f32 ? launch_vec<float, 4>(p, st) : launch_vec<bf16, 4>(p, st);
-  return p.f32 ? launch_vec<float, 1>(p, st) : launch_vec<bf16, 1>(p, st);
+  return p.f32 ? launch_e<float>(p, st) : launch_e<bf16>(p, st);
 }
 
 }  // namespace gdn

@@ -74,6 +74,7 @@ struct ScanStepProblem {
   int B, C, G, S, per, lines;
   bool f32, softplus;
   bool vec4;  // a channel's states and A come 16 bytes at a time
+  bool wide;  // and so may four values of B and C rows
   float* state;  // [lines, C, S]
   const void* x;
   const void* dt;

@@ -80,6 +80,32 @@ __device__ __forceinline__ scalar_row as_scalar(const float* p) {
   return (scalar_row)(uintptr_t)p;
 }
 
+// Column c's sum over `rows` rows of partial sums `stride` apart, in a fixed order: the workgroup's
+// 16 waves take every 16th row each, four loads ahead, and are added in order.  The first wave has
+// the sum; every wave calls it, lane by lane for its 64 columns.
+constexpr int kColumnThreads = 1024;
+__device__ __forceinline__ float column_sum(const float* p, long stride, long rows, int c, int C) {
+  __shared__ float s[kColumnThreads / 64][64];
+  constexpr int WAVES = kColumnThreads / 64;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < C) {
+    long i = wave_id();
+    for (; i + 3 * WAVES < rows; i += 4 * WAVES) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += p[(i + j * WAVES) * stride + c];
+    }
+    for (; i < rows; i += WAVES) v[0] += p[i * stride + c];
+  }
+  s[wave_id()][lane_id()] = (v[0] + v[1]) + (v[2] + v[3]);
+  __syncthreads();
+  float r = 0.f;
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) r += s[k][lane_id()];
+  }
+  return r;
+}
+
 // The chunk of a slot (see ScanProblem).
 struct Chunk {
   int n, i, count;     // sequence, chunk of the sequence, chunks of the sequence

@@ -24,7 +24,6 @@
 // Statistics and sums are fp32; every output is rounded once; sums have a fixed order.
 #include "norm.h"
 #include "ssm_device.h"
-#include "vec8.h"
 
 namespace gdn {
 
@@ -32,37 +31,26 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// VEC consecutive values, widened.
+// VEC consecutive values: as one load or store of up to 16 bytes (two for 8 fp32), and widened.
 template <typename E, int VEC>
 struct Row {
-  static __device__ __forceinline__ void load(const E* p, float* v) {
-    if constexpr (VEC == 8) {
-      Vec8<E>::load(p, v);
-    } else {
-      typedef E vec __attribute__((ext_vector_type(VEC)));
-      if constexpr (VEC == 1) {
-        v[0] = (float)p[0];
-      } else {
-        const vec r = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = (float)r[i];
-      }
-    }
+  static constexpr int kBytes = VEC * (int)sizeof(E);
+  struct alignas(kBytes < 16 ? kBytes : 16) raw {
+    E e[VEC];
+  };
+  static __device__ __forceinline__ raw load_raw(const E* p) {
+    return *reinterpret_cast<const raw*>(p);
   }
-  static __device__ __forceinline__ void store(E* p, const float* v) {
-    if constexpr (VEC == 8) {
-      Vec8<E>::store(p, v);
-    } else {
-      typedef E vec __attribute__((ext_vector_type(VEC)));
-      if constexpr (VEC == 1) {
-        p[0] = (E)v[0];
-      } else {
-        vec r;
+  static __device__ __forceinline__ void wide(const raw& r, float* v) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) r[i] = (E)v[i];
-        *reinterpret_cast<vec*>(p) = r;
-      }
-    }
+    for (int i = 0; i < VEC; ++i) v[i] = (float)r.e[i];
+  }
+  static __device__ __forceinline__ void load(const E* p, float* v) { wide(load_raw(p), v); }
+  static __device__ __forceinline__ void store(E* p, const float* v) {
+    raw r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.e[i] = (E)v[i];
+    *reinterpret_cast<raw*>(p) = r;
   }
 };
 
@@ -80,6 +68,44 @@ __device__ __forceinline__ float norm_out(float u, float gate, bool gated, bool 
 }
 __device__ __forceinline__ float norm_du(float u, float gate, float dy, bool gated, bool silu) {
   return dy * (gated ? act_f32(gate, silu) : act_slope(u, silu));
+}
+
+// VEC per-channel parameters from channel c on (wide: 16-byte aligned there), or `other` of each.
+template <int VEC>
+__device__ __forceinline__ void load_params(const float* p, int c, bool wide, float other,
+                                            float* v) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = other;
+  } else if (wide && VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i + 3 < VEC; i += 4) {
+      const f32x4 r = *reinterpret_cast<const f32x4*>(p + c + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = r[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = p[c + i];
+  }
+}
+
+// The statistics (stride values a group) of channels c .. c + VEC - 1 of a sample: read again only
+// where a new group begins.
+template <int VEC>
+__device__ __forceinline__ void load_stats(const float* p, int stride, int c, int cpg, float* v) {
+  int g = c / cpg, at = c - g * cpg;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    if (i == 0 || at == 0)
+      v[i] = p[g * stride];
+    else
+      v[i] = v[i ? i - 1 : 0];
+    if (++at == cpg) {
+      at = 0;
+      ++g;
+    }
+  }
 }
 
 // Sum over the lps lanes (a power of two, or the whole workgroup) that share a segment.
@@ -100,8 +126,8 @@ __device__ __forceinline__ float seg_sum(float v, int lps, float* lds) {
 struct RowPlan {
   int lps;   // lanes a segment: a power of two to 64, or 256
   int gp;    // groups a workgroup (a power of two)
-  int rpb;   // rows a workgroup
   int gblk;  // workgroups a row
+  int wgs;   // workgroups that share out the rows
 };
 
 template <typename E, int VEC, int K>
@@ -119,25 +145,39 @@ __global__ __launch_bounds__(kThreads) void k_norm_rows(NormProblem p, RowPlan q
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int v = l + q.lps * k;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int c = g * p.cpg + v * VEC + i;
-      w[k][i] = ok && v < nv && p.weight ? p.weight[c] : 1.f;
-      b[k][i] = ok && v < nv && p.bias ? p.bias[c] : 0.f;
+    if (ok && v < nv) {
+      load_params<VEC>(p.weight, g * p.cpg + v * VEC, p.wide, 1.f, w[k]);
+      load_params<VEC>(p.bias, g * p.cpg + v * VEC, p.wide, 0.f, b[k]);
     }
   }
   const float inv = 1.f / (float)p.cpg;
-  const int r0 = blockIdx.x * q.rpb;
-  for (int j = 0; j < q.rpb; j += rw) {
-    const int r = r0 + j + seg / q.gp;
-    const bool live = ok && r < p.N && j + seg / q.gp < q.rpb;
+  typedef Row<E, VEC> R;
+  typename R::raw rx[K], rg[K];
+  const int step = gridDim.x * rw;  // rows taken at once by all workgroups, one after another
+  auto fetch = [&](int r) {
     const long at = (long)r * p.C + (long)g * p.cpg;
-    float v[K][VEC], s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int iv = l + q.lps * k;
+      if (ok && r < p.N && iv < nv) {
+        rx[k] = R::load_raw(x + at + iv * VEC);
+        if (gate) rg[k] = R::load_raw(gate + at + iv * VEC);
+      }
+    }
+  };
+  const int first = blockIdx.x * rw + seg / q.gp;
+  fetch(first);
+  for (int r0 = blockIdx.x * rw; r0 < p.N; r0 += step) {
+    const int r = r0 + seg / q.gp;
+    const bool live = ok && r < p.N;
+    const long at = (long)r * p.C + (long)g * p.cpg;
+    float v[K][VEC], gt[K][VEC], s = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int iv = l + q.lps * k;
       if (live && iv < nv) {
-        Row<E, VEC>::load(x + at + iv * VEC, v[k]);
+        R::wide(rx[k], v[k]);
+        if (gate) R::wide(rg[k], gt[k]);
       } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[k][i] = 0.f;
@@ -145,6 +185,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_rows(NormProblem p, RowPlan q
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s += v[k][i];
     }
+    fetch(r + step);
     const float mean = seg_sum(s, q.lps, lds) * inv;
     float m2 = 0.f;
 #pragma unroll
@@ -162,11 +203,10 @@ __global__ __launch_bounds__(kThreads) void k_norm_rows(NormProblem p, RowPlan q
     for (int k = 0; k < K; ++k) {
       const int iv = l + q.lps * k;
       if (iv >= nv) continue;
-      float gt[VEC], out[VEC];
-      if (gate) Row<E, VEC>::load(gate + at + iv * VEC, gt);
+      float out[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        out[i] = norm_out(fmaf(v[k][i] * rstd, w[k][i], b[k][i]), gate ? gt[i] : 0.f,
+        out[i] = norm_out(fmaf(v[k][i] * rstd, w[k][i], b[k][i]), gate ? gt[k][i] : 0.f,
                           gate != nullptr, p.silu);
       Row<E, VEC>::store(y + at + iv * VEC, out);
     }
@@ -189,17 +229,23 @@ __global__ __launch_bounds__(kThreads) void k_norm_rows_bwd(NormProblem p, RowPl
   const E* dy = static_cast<const E*>(p.dy);
   const bool ok = g < p.G;
   const bool gated = gate != nullptr;
-  float dw[K][VEC], db[K][VEC];
+  // the parameters stay in registers where they leave enough of them
+  constexpr bool KEEP = K * VEC <= 16;
+  float dw[K][VEC], db[K][VEC], wk[KEEP ? K : 1][VEC], bk[KEEP ? K : 1][VEC];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) dw[k][i] = db[k][i] = 0.f;
+    const int v = l + q.lps * k;
+    if (KEEP && ok && v < nv) {
+      load_params<VEC>(p.weight, g * p.cpg + v * VEC, p.wide, 1.f, wk[KEEP ? k : 0]);
+      load_params<VEC>(p.bias, g * p.cpg + v * VEC, p.wide, 0.f, bk[KEEP ? k : 0]);
+    }
   }
   const float inv = 1.f / (float)p.cpg;
-  const int r0 = blockIdx.x * q.rpb;
-  for (int j = 0; j < q.rpb; j += rw) {
-    const int r = r0 + j + seg / q.gp;
-    const bool live = ok && r < p.N && j + seg / q.gp < q.rpb;
+  for (int r0 = blockIdx.x * rw; r0 < p.N; r0 += gridDim.x * rw) {
+    const int r = r0 + seg / q.gp;
+    const bool live = ok && r < p.N;
     const long at = (long)r * p.C + (long)g * p.cpg;
     const float mean = live ? p.mean[(long)r * p.G + g] : 0.f;
     const float rstd = live ? p.rstd[(long)r * p.G + g] : 0.f;
@@ -212,12 +258,15 @@ __global__ __launch_bounds__(kThreads) void k_norm_rows_bwd(NormProblem p, RowPl
         Row<E, VEC>::load(x + at + iv * VEC, xv);
         Row<E, VEC>::load(dy + at + iv * VEC, dv);
         if (gated) Row<E, VEC>::load(gate + at + iv * VEC, gt);
+        if constexpr (!KEEP) {
+          load_params<VEC>(p.weight, g * p.cpg + iv * VEC, p.wide, 1.f, wk[0]);
+          load_params<VEC>(p.bias, g * p.cpg + iv * VEC, p.wide, 0.f, bk[0]);
+        }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const int c = g * p.cpg + iv * VEC + i;
-          const float w = p.weight ? p.weight[c] : 1.f, b = p.bias ? p.bias[c] : 0.f;
+          const float w = wk[KEEP ? k : 0][i];
           hat[k][i] = (xv[i] - mean) * rstd;
-          const float u = fmaf(hat[k][i], w, b);
+          const float u = fmaf(hat[k][i], w, bk[KEEP ? k : 0][i]);
           const float gv = gated ? gt[i] : 0.f;
           const float du = norm_du(u, gv, dv[i], gated, p.silu);
           if (gated) dg[i] = dv[i] * u * act_slope(gv, p.silu);
@@ -260,10 +309,12 @@ __global__ __launch_bounds__(kThreads) void k_norm_rows_bwd(NormProblem p, RowPl
 
 // --- maps -------------------------------------------------------------------------------------
 
+// A sample's positions go to its `slabs` workgroups in turn, ty at a time, so that the workgroups
+// running at once read neighbouring rows (pieces far apart fall on the same memory channels).
 struct MapPlan {
-  int tx, ty;         // threads over channel vectors and over positions (tx ty = 256)
-  int cblk;           // workgroups a row
-  int slabs, length;  // pieces of the positions, and their length
+  int tx, ty;  // threads over channel vectors and over positions (tx ty = 256)
+  int cblk;    // workgroups a row
+  int slabs;   // workgroups that share a sample's positions
 };
 
 struct Stat {
@@ -284,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_stats(NormProblem p, MapPlan 
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx;
   const int n = blockIdx.x / q.slabs, slab = blockIdx.x - n * q.slabs;
   const int c0 = (blockIdx.y * q.tx + tx) * VEC;
-  const int p0 = slab * q.length, p1 = min(p0 + q.length, p.P);
+  const int p0 = slab * q.ty + ty, step = q.slabs * q.ty;
   const bool ok = c0 < p.C;
   const E* x = static_cast<const E*>(p.x) + (long)n * p.P * p.C + c0;
   float mean[VEC], m2[VEC];
@@ -293,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_stats(NormProblem p, MapPlan 
   float cnt = 0.f;
   if (ok) {
 #pragma unroll 4
-    for (int pos = p0 + ty; pos < p1; pos += q.ty) {
+    for (int pos = p0; pos < p.P; pos += step) {
       float v[VEC];
       Row<E, VEC>::load(x + (long)pos * p.C, v);
       cnt += 1.f;
@@ -339,7 +390,10 @@ __global__ __launch_bounds__(kThreads) void k_norm_join(NormProblem p, MapPlan q
   const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
   const float* ws = p.ws + (long)n * q.slabs * 2 * p.C + (long)g * p.cpg;
   const int items = q.slabs * p.cpg;
-  auto count = [&](int slab) { return (float)(min((slab + 1) * q.length, p.P) - slab * q.length); };
+  auto count = [&](int slab) {  // positions of a slab
+    const int all = q.slabs * q.ty, rest = p.P % all - slab * q.ty;
+    return (float)(p.P / all * q.ty + min(max(rest, 0), q.ty));
+  };
   float s = 0.f;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     const int slab = i / p.cpg, c = i - slab * p.cpg;
@@ -368,23 +422,21 @@ __global__ __launch_bounds__(kThreads) void k_norm_apply(NormProblem p, MapPlan 
   const int n = blockIdx.x / q.slabs, slab = blockIdx.x - n * q.slabs;
   const int c0 = (blockIdx.y * q.tx + tx) * VEC;
   if (c0 >= p.C) return;
-  const int p0 = slab * q.length, p1 = min(p0 + q.length, p.P);
+  const int p0 = slab * q.ty + ty, step = q.slabs * q.ty;
   const long at = (long)n * p.P * p.C + c0;
   const E* x = static_cast<const E*>(p.x) + at;
   const E* gate = static_cast<const E*>(p.gate) + at;
   E* y = static_cast<E*>(p.y) + at;
   const bool gated = p.gate != nullptr;
-  float mu[VEC], sc[VEC], b[VEC];
+  float mu[VEC], sc[VEC], b[VEC], w[VEC];
+  load_stats<VEC>(mean + (long)n * p.G, 1, c0, p.cpg, mu);
+  load_stats<VEC>(rstd + (long)n * p.G, 1, c0, p.cpg, sc);
+  load_params<VEC>(p.weight, c0, p.wide, 1.f, w);
+  load_params<VEC>(p.bias, c0, p.wide, 0.f, b);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const int c = c0 + i;
-    const long k = (long)n * p.G + c / p.cpg;
-    mu[i] = mean[k];
-    sc[i] = rstd[k] * (p.weight ? p.weight[c] : 1.f);
-    b[i] = p.bias ? p.bias[c] : 0.f;
-  }
+  for (int i = 0; i < VEC; ++i) sc[i] *= w[i];
 #pragma unroll 4
-  for (int pos = p0 + ty; pos < p1; pos += q.ty) {
+  for (int pos = p0; pos < p.P; pos += step) {
     float v[VEC], gt[VEC];
     Row<E, VEC>::load(x + (long)pos * p.C, v);
     if (gated) Row<E, VEC>::load(gate + (long)pos * p.C, gt);
@@ -402,7 +454,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_sums(NormProblem p, MapPl
   const int tx = threadIdx.x % q.tx, ty = threadIdx.x / q.tx;
   const int n = blockIdx.x / q.slabs, slab = blockIdx.x - n * q.slabs;
   const int c0 = (blockIdx.y * q.tx + tx) * VEC;
-  const int p0 = slab * q.length, p1 = min(p0 + q.length, p.P);
+  const int p0 = slab * q.ty + ty, step = q.slabs * q.ty;
   const bool ok = c0 < p.C;
   const long at = (long)n * p.P * p.C + c0;
   const E* x = static_cast<const E*>(p.x) + at;
@@ -414,17 +466,12 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_sums(NormProblem p, MapPl
   for (int i = 0; i < VEC; ++i) a[i] = ah[i] = 0.f;
   if (ok) {
     float mu[VEC], rs[VEC], w[VEC], b[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int c = c0 + i;
-      const long k = (long)n * p.G + c / p.cpg;
-      mu[i] = p.mean[k];
-      rs[i] = p.rstd[k];
-      w[i] = p.weight ? p.weight[c] : 1.f;
-      b[i] = p.bias ? p.bias[c] : 0.f;
-    }
+    load_stats<VEC>(p.mean + (long)n * p.G, 1, c0, p.cpg, mu);
+    load_stats<VEC>(p.rstd + (long)n * p.G, 1, c0, p.cpg, rs);
+    load_params<VEC>(p.weight, c0, p.wide, 1.f, w);
+    load_params<VEC>(p.bias, c0, p.wide, 0.f, b);
 #pragma unroll 2
-    for (int pos = p0 + ty; pos < p1; pos += q.ty) {
+    for (int pos = p0; pos < p.P; pos += step) {
       float v[VEC], d[VEC], gt[VEC];
       Row<E, VEC>::load(x + (long)pos * p.C, v);
       Row<E, VEC>::load(dy + (long)pos * p.C, d);
@@ -489,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_apply(NormProblem p, MapP
   const int n = blockIdx.x / q.slabs, slab = blockIdx.x - n * q.slabs;
   const int c0 = (blockIdx.y * q.tx + tx) * VEC;
   if (c0 >= p.C) return;
-  const int p0 = slab * q.length, p1 = min(p0 + q.length, p.P);
+  const int p0 = slab * q.ty + ty, step = q.slabs * q.ty;
   const long at = (long)n * p.P * p.C + c0;
   const E* x = static_cast<const E*>(p.x) + at;
   const E* dy = static_cast<const E*>(p.dy) + at;
@@ -498,19 +545,14 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_apply(NormProblem p, MapP
   E* dgate = static_cast<E*>(p.dgate) + at;
   const bool gated = p.gate != nullptr;
   float mu[VEC], rs[VEC], w[VEC], b[VEC], s1[VEC], s2[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const int c = c0 + i;
-    const long k = (long)n * p.G + c / p.cpg;
-    mu[i] = p.mean[k];
-    rs[i] = p.rstd[k];
-    w[i] = p.weight ? p.weight[c] : 1.f;
-    b[i] = p.bias ? p.bias[c] : 0.f;
-    s1[i] = sums[2 * k];
-    s2[i] = sums[2 * k + 1];
-  }
+  load_stats<VEC>(p.mean + (long)n * p.G, 1, c0, p.cpg, mu);
+  load_stats<VEC>(p.rstd + (long)n * p.G, 1, c0, p.cpg, rs);
+  load_stats<VEC>(sums + 2L * n * p.G, 2, c0, p.cpg, s1);
+  load_stats<VEC>(sums + 2L * n * p.G + 1, 2, c0, p.cpg, s2);
+  load_params<VEC>(p.weight, c0, p.wide, 1.f, w);
+  load_params<VEC>(p.bias, c0, p.wide, 0.f, b);
 #pragma unroll 2
-  for (int pos = p0 + ty; pos < p1; pos += q.ty) {
+  for (int pos = p0; pos < p.P; pos += step) {
     float v[VEC], d[VEC], gt[VEC];
     Row<E, VEC>::load(x + (long)pos * p.C, v);
     Row<E, VEC>::load(dy + (long)pos * p.C, d);
@@ -601,7 +643,10 @@ int pow2_at_least(int n) {
 }
 
 constexpr int kRowVecs = 4;       // vectors of a segment a lane holds, at most
-constexpr int kWantGroups = 2048; // workgroups that keep 256 CUs busy with streaming work
+constexpr int kWantGroups = 2048;  // workgroups of a map's pass
+// workgroups that share out rows: four a CU, which all run at once (16384 gated rows of 4096 channels
+// take 81 us; 107 with 512, 93 with 2048, 83 with 8192)
+constexpr int kRowGroups = 1024;
 
 // Rows: P = 1 and a group that fits the lanes' registers.
 bool row_plan(const NormProblem& p, int vec, RowPlan* q, int* k) {
@@ -616,10 +661,9 @@ bool row_plan(const NormProblem& p, int vec, RowPlan* q, int* k) {
   q->gp = g < segs ? g : segs;
   q->gblk = (p.G + q->gp - 1) / q->gp;
   const int rw = segs / q->gp;
-  long rpb = (long)p.N * q->gblk / kWantGroups;
-  if (rpb < 1) rpb = 1;
-  if (rpb > 64) rpb = 64;
-  q->rpb = (int)((rpb + rw - 1) / rw * rw);
+  long wgs = (p.N + rw - 1L) / rw;
+  const long most = (kRowGroups + q->gblk - 1) / q->gblk;
+  q->wgs = (int)(wgs < most ? wgs : most);
   return true;
 }
 
@@ -630,14 +674,10 @@ MapPlan map_plan(const NormProblem& p, int vec) {
   if (q.tx > kThreads) q.tx = kThreads;
   q.ty = kThreads / q.tx;
   q.cblk = (nv + q.tx - 1) / q.tx;
-  // pieces short enough to fill the GPU, but at least 16 positions a thread
-  const long all = (long)p.N * p.P * q.cblk;
-  long len = (all + kWantGroups - 1) / kWantGroups;
-  const long least = 16L * q.ty;
-  if (len < least) len = least;
-  if (len > p.P) len = p.P;
-  q.length = (int)len;
-  q.slabs = (p.P + q.length - 1) / q.length;
+  // enough workgroups to fill the GPU, but at least 16 positions a thread
+  const long most = (p.P + 16L * q.ty - 1) / (16L * q.ty);
+  const long want = (kWantGroups + (long)p.N * q.cblk - 1) / ((long)p.N * q.cblk);
+  q.slabs = (int)(want < most ? want : most);
   return q;
 }
 
@@ -651,7 +691,7 @@ hipError_t fwd_vec(const NormProblem& p, hipStream_t st) {
   RowPlan r;
   int k;
   if (row_plan(p, VEC, &r, &k)) {
-    const dim3 grid((p.N + r.rpb - 1) / r.rpb, r.gblk);
+    const dim3 grid(r.wgs, r.gblk);
     if (k == 1) k_norm_rows<E, VEC, 1><<<grid, kThreads, 0, st>>>(p, r);
     else if (k == 2) k_norm_rows<E, VEC, 2><<<grid, kThreads, 0, st>>>(p, r);
     else k_norm_rows<E, VEC, 4><<<grid, kThreads, 0, st>>>(p, r);
@@ -677,7 +717,7 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t st) {
   RowPlan r;
   int k;
   if (row_plan(p, VEC, &r, &k)) {
-    const dim3 grid((p.N + r.rpb - 1) / r.rpb, r.gblk);
+    const dim3 grid(r.wgs, r.gblk);
     if (k == 1) k_norm_rows_bwd<E, VEC, 1><<<grid, kThreads, 0, st>>>(p, r);
     else if (k == 2) k_norm_rows_bwd<E, VEC, 2><<<grid, kThreads, 0, st>>>(p, r);
     else k_norm_rows_bwd<E, VEC, 4><<<grid, kThreads, 0, st>>>(p, r);
@@ -699,7 +739,9 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t st) {
 }
 
 template <bool BWD, typename E>
-hipError_t launch_e(const NormProblem& p, hipStream_t st) {
+hipError_t launch_e(const NormProblem& given, hipStream_t st) {
+  NormProblem p = given;
+  p.wide = (reinterpret_cast<uintptr_t>(p.weight) | reinterpret_cast<uintptr_t>(p.bias)) % 16 == 0;
   // in a row a segment's vectors must not cross into the next group
   const int vec = vector_of(p, p.P == 1 ? p.cpg : p.C);
   if constexpr (BWD) {
@@ -726,7 +768,7 @@ size_t norm_workspace(const NormProblem& p, bool backward) {
     int k;
     long need = 0;
     if (row_plan(p, vec, &r, &k)) {
-      if (backward) need = (p.N + r.rpb - 1L) / r.rpb * (kThreads / r.lps / r.gp) * 2 * p.C;
+      if (backward) need = (long)r.wgs * (kThreads / r.lps / r.gp) * 2 * p.C;
     } else if (backward || !group_shape(p)) {
       need = (long)p.N * map_plan(p, vec).slabs * 2 * p.C + 2L * p.N * p.G;
     }

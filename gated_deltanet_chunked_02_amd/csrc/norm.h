@@ -10,6 +10,7 @@ namespace gdn {
 struct NormProblem {
   int N, P, C, G, cpg;  // samples, positions a sample, channels, groups, channels a group
   bool f32, silu;
+  bool wide;            // weight and bias are 16-byte aligned (set by the launchers)
   float eps;
   const void* x;
   const float* weight;  // [C] or null (ones)

@@ -401,6 +401,9 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
     for (int tile = tiles - 1; tile >= 0; --tile) {
       const int m = min(BT, ch.len - tile * BT);
       const float* row = rows + tile * BT * 2 * NS;
+      Rows4 r0, r1;  // asked for before the tile's preparation, which hides their latency
+      r0.load(row, 0);
+      if (m > 4) r1.load(row, 4);
       Raw<E, GATED> own[TPW];
       float sig[TPW];  // sigmoid(z)
 #pragma unroll
@@ -435,9 +438,6 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
       auto body = [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
         float hs[BT][NS], as[BT][NS];
-        Rows4 r0, r1;
-        r0.load(row, 0);
-        if (FULL || m > 4) r1.load(row, 4);
 #pragma unroll
         for (int t = 0; t < BT; ++t) {
           if (FULL || t < m) {
@@ -466,15 +466,14 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
                 const float b = t < 4 ? r0.b(t & 3, k) : r1.b(t & 3, k);
                 const float c = t < 4 ? r0.c(t & 3, k) : r1.c(t & 3, k);
                 const float g = fmaf(e, c, carry[k]);
-                const float ah = as[t][k] * (t ? hs[t ? t - 1 : 0][k] : start[k]);
-                const float q = g * ah;
+                carry[k] = as[t][k] * g;
+                const float q = carry[k] * (t ? hs[t ? t - 1 : 0][k] : start[k]);
                 dA[k] = fmaf(v, q, dA[k]);
                 q1 = k ? fmaf(q, A2[k], q1) : q * A2[k];
                 u = k ? fmaf(g, b, u) : g * b;
                 if (GATED) yy = k ? fmaf(hs[t][k], c, yy) : hs[t][k] * c;
                 pb[k] = g * dx;
                 pc[k] = e * hs[t][k];
-                carry[k] = as[t][k] * g;
               }
               part[0][w][t][lane] = u;
               part[1][w][t][lane] = q1;

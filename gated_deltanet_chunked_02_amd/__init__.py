@@ -186,13 +186,23 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
+def _current_stream(device=None):
+    """The raw current stream of a device (of the current one by default).  The Stream object's
+    own lookup takes about ten times as long, which a single-token call would notice."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return raw(torch.cuda.current_device() if device is None else device.index)
+
+
 def gdn_chunk_fwd(desc: GdnDesc, q, k, v, g, beta, h0, cu_seqlens, scale, o, ht,
                   stream=None) -> int:
     """Raw call: tensors (or integer device addresses / None) are passed as pointers.
     Returns the status code (0 = ok) without raising."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
+        stream = _current_stream()
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     return int(load().gdn_chunk_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
@@ -206,7 +216,7 @@ def gdn_chunk_fwd_noalloc(desc: GdnDesc, q, k, v, g, beta, h0, cu_seqlens, scale
     scratch is the workspace (desc.workspace is ignored).  Returns the status code."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
+        stream = _current_stream()
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     return int(load().gdn_chunk_fwd_noalloc(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v),
@@ -219,7 +229,7 @@ def gdn_fused_sigmoid_gating_delta_rule(desc: GdnDesc, q, k, v, a, b, A_log, dt_
     """Raw call of the decode operator with in-kernel gates; returns the status code."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
+        stream = _current_stream()
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     return int(load().gdn_fused_sigmoid_gating_delta_rule(
@@ -240,7 +250,7 @@ def gdn_chunk_bwd(desc: GdnDesc, q, k, v, g, beta, h0, cu_seqlens, scale, do, dh
     """Raw call of the backward pass; returns the status code (0 = ok) without raising."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
+        stream = _current_stream()
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     return int(load().gdn_chunk_bwd(
@@ -283,9 +293,9 @@ def _check_devices(named, ref):
     _need(ref.type == "cuda", ValueError,
           "the tensors must be device tensors (got %s)" % ref)
     for name, t in named.items():
-        if t is not None:
-            _need(t.device == ref, ValueError,
-                  "%s must be on %s like the other tensors (got %s)" % (name, ref, t.device))
+        if t is not None and t.device != ref:
+            raise ValueError("%s must be on %s like the other tensors (got %s)"
+                             % (name, ref, t.device))
 
 
 def _validate_gdn(q, k, v, g, beta, initial_state, cu_seqlens, workspace, devices=True):
@@ -539,7 +549,7 @@ def gdn_causal_conv1d_fwd(desc: GdnConvDesc, x, weight, bias, conv_state, cache_
     """Raw call (tensors, integer device addresses or None); returns the status code."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
+        stream = _current_stream()
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     return int(load().gdn_causal_conv1d_fwd(

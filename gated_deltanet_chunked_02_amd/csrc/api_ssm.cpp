@@ -105,6 +105,14 @@ void plan_fwd(gdn::ScanProblem* p, bool packed) {
                     : p->N * (int)(p->T > p->Lc ? ((long long)p->T + p->Lc - 1) / p->Lc : 1);
 }
 
+// A launch has fewer than 2^32 threads; so have the passes over B and C rows, over the chunks'
+// channel blocks and over the states.
+bool grids_ok(const gdn::ScanProblem& p) {
+  const long long most = 1LL << 32;
+  return (long long)p.Ttot * p.G * 2 * p.Sp < most - 256 &&
+         (long long)p.slots * p.G * p.nblk * 64 * p.nw < most && (long long)p.N * p.S * 256 < most;
+}
+
 struct ScanLayout {
   size_t bc, hst, dsum, total;
 };
@@ -238,6 +246,10 @@ size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* sta
   if (status) *status = s;
   if (s != GDN_OK) return 0;
   plan_fwd(&p, packed);
+  if (!grids_ok(p)) {
+    if (status) *status = GDN_ERR_UNSUPPORTED;
+    return 0;
+  }
   size_t need = scan_layout(p).total;
   if (!packed && d->B == 1) {  // one sequence may also come as a packed batch of one
     gdn::ScanProblem q;
@@ -266,6 +278,7 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
     return GDN_ERR_INVALID_ARG;
   if (p.N == 0) return GDN_OK;
   plan_fwd(&p, cu_seqlens != nullptr);
+  if (!grids_ok(p)) return GDN_ERR_UNSUPPORTED;
   const ScanLayout L = scan_layout(p);
   if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
                       !aligned(d->workspace, kAlign)))
@@ -299,6 +312,10 @@ size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_desc* d, gdn_status*
   const bool one = !packed && d->B == 1;
   if (one) p.N = 1;
   plan_bwd(&p, packed || one);
+  if (!grids_ok(p)) {
+    if (status) *status = GDN_ERR_UNSUPPORTED;
+    return 0;
+  }
   return bwd_layout(p).total;
 }
 
@@ -324,6 +341,7 @@ gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const v
                         (const void*)dD, (const void*)ddt_bias, (const void*)dh0})
     if (!aligned(q, 4)) return GDN_ERR_INVALID_ARG;
   plan_bwd(&p, cu_seqlens != nullptr);
+  if (!grids_ok(p)) return GDN_ERR_UNSUPPORTED;
   const BwdLayout L = bwd_layout(p);
   if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
                       !aligned(d->workspace, kAlign)))

@@ -50,7 +50,12 @@ struct Row {
     raw r;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) r.e[i] = (E)v[i];
-    *reinterpret_cast<raw*>(p) = r;
+    // past the caches where a store is 16 bytes: a map's second pass finds more of x there, and a
+    // large output would not stay (16384 gated rows of 4096 channels 84 to 79 us)
+    if constexpr (kBytes == 16)
+      __builtin_nontemporal_store(__builtin_bit_cast(f32x4, r), reinterpret_cast<f32x4*>(p));
+    else
+      *reinterpret_cast<raw*>(p) = r;
   }
 };
 

@@ -21,8 +21,8 @@ import ctypes
 import torch
 from torch import Tensor
 
-from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _need, _validate_conv,
-               load)
+from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _current_stream,
+               _need, _validate_conv, load)
 
 _CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -76,14 +76,8 @@ def declare(lib):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-
-
-def _current(device):
-    """The raw current stream of a device (a tenth of the time the Stream object takes)."""
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device.index)
 
 
 def _addresses(tensors):
@@ -161,13 +155,7 @@ def _rows(t, lead):
 
 
 def _on(device, **named):
-    """Every tensor given on ``device``, a CUDA (HIP) device (see _check_devices)."""
-    if device.type == "cuda":
-        for t in named.values():
-            if t is not None and t.device != device:
-                break
-        else:
-            return
+    """Every tensor given on ``device``, a CUDA (HIP) device."""
     _check_devices(named, device)
 
 
@@ -302,7 +290,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
         return y, ht
     ws = _workspace(desc, gdn_selective_scan_workspace_size(desc), workspace, dev)  # noqa: F841
     st = gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, y, ht,
-                                _current(dev))
+                                _current_stream(dev))
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_fwd")
     return y, ht
@@ -332,7 +320,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_soft
     need = gdn_selective_scan_bwd_workspace_size(desc)
     ws = _workspace(desc, need, workspace, dev)  # noqa: F841
     st = gdn_selective_scan_bwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, dy, dht, dx, ddt, dA,
-                                dB, dC, dD, dz, dbias, dh0, _current(dev))
+                                dB, dC, dD, dz, dbias, dh0, _current_stream(dev))
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_bwd")
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
@@ -371,7 +359,7 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     desc.B, desc.T, desc.N, desc.dt_softplus = n, 1, n, int(bool(dt_softplus))
     desc.state_lines = state.shape[0]
     st = gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, read, write, y,
-                                    _current(dev))
+                                    _current_stream(dev))
     if st != 0:
         raise GdnError(st, "gdn_selective_state_update")
     return y
@@ -435,7 +423,7 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
         ws = torch.empty(need, device=dev, dtype=torch.uint8)
     st = gdn_causal_conv1d_bwd(desc, x, weight, bias, first, cu, dy, lines["dfinal_state"], dx,
                                dweight, dbias, dinit, ws, 0 if ws is None else ws.numel(),
-                               _current(dev))
+                               _current_stream(dev))
     if st != 0:
         raise GdnError(st, "gdn_causal_conv1d_bwd")
     return dx, dweight, dbias, dinit
@@ -505,7 +493,7 @@ def group_norm(x, num_groups, weight=None, bias=None, eps=1e-5, activation=None,
     mean = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
     rstd = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc), workspace, dev)  # noqa: F841
-    st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, _current(dev))
+    st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, _current_stream(dev))
     if st != 0:
         raise GdnError(st, "gdn_group_norm_fwd")
     return y, mean, rstd
@@ -531,7 +519,7 @@ def group_norm_bwd(dy, x, num_groups, mean, rstd, weight=None, bias=None, activa
     dx, dweight, dbias, dgate = map(new, (x, weight, bias, gate))
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc, True), workspace, dev)  # noqa: F841
     st = gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight, dbias,
-                            dgate, _current(dev))
+                            dgate, _current_stream(dev))
     if st != 0:
         raise GdnError(st, "gdn_group_norm_bwd")
     return dx, dweight, dbias, dgate

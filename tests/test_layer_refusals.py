@@ -42,6 +42,8 @@ SCAN_BAD = [
     (dict(N=3), 1), (dict(x_stride=127), 1), (dict(dt_stride=-1), 1), (dict(z_stride=64), 1),
     (dict(b_stride=31), 1), (dict(c_stride=31), 1), (dict(dstate=257), 2),
     (dict(B=1 << 16, T=1 << 16, N=0), 2), (dict(channels=1 << 21), 2),
+    # a row so long that a tile of them passes 2 GiB; more B and C values than a launch has threads
+    (dict(x_stride=1 << 24), 2), (dict(B=1 << 15, N=0, T=1 << 12, groups=8, dstate=16), 2),
 ]
 
 

@@ -646,8 +646,9 @@ template <typename E>
 hipError_t launch_e(const ScanProblem& p, const ScanBwd& b, const BwdArgs& a, hipStream_t st) {
   if (p.nw == 1) return launch_cfg<1, false, E>(p, b, a, st);
   if (p.nw == 2) return launch_cfg<2, false, E>(p, b, a, st);
-  if (p.S <= 16) return launch_cfg<4, false, E>(p, b, a, st);
-  return launch_cfg<4, true, E>(p, b, a, st);
+  if (p.nw == 4) return launch_cfg<4, false, E>(p, b, a, st);
+  if (p.S <= 32) return launch_cfg<8, false, E>(p, b, a, st);
+  return launch_cfg<8, true, E>(p, b, a, st);
 }
 
 }  // namespace

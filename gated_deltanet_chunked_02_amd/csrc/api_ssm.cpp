@@ -212,8 +212,11 @@ gdn_status check_norm(const gdn_norm_desc* d, gdn::NormProblem* p) {
     return GDN_ERR_INVALID_ARG;
   if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
   if (d->activation != GDN_ACT_NONE && d->activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
-  // grids of a workgroup for each (sample, group) and for each (sample, piece of a map)
-  if ((long long)d->samples * d->groups > (1 << 23) || d->channels > (1 << 20))
+  // a workgroup of 1024 threads for each (sample, group), except for rows whose groups fit the
+  // lanes' registers at any alignment
+  const bool rows = d->positions == 1 && d->channels / d->groups <= 1024;
+  if ((rows ? d->samples > (1 << 30) : (long long)d->samples * d->groups > (1 << 21)) ||
+      d->channels > (1 << 20))
     return GDN_ERR_UNSUPPORTED;
   memset(p, 0, sizeof(*p));
   p->N = d->samples;

@@ -510,27 +510,46 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_sums(NormProblem p, MapPl
   }
 }
 
-// sum dhat / M and sum (dhat xhat) / M of each (sample, group): sums [N, G, 2].
-__global__ __launch_bounds__(kThreads) void k_norm_bwd_join(NormProblem p, MapPlan q,
-                                                            float* sums) {
-  __shared__ float lds[4];
+// The first N G workgroups: sum dhat / M and sum (dhat xhat) / M of each (sample, group), to sums
+// [N, G, 2]; the others: dw and db from the same partial sums, 64 channels each.
+__global__ __launch_bounds__(kColumnThreads) void k_norm_bwd_join(NormProblem p, MapPlan q,
+                                                                  float* sums) {
+  const int joins = p.N * p.G;
+  if ((int)blockIdx.x >= joins) {
+    const int cols = (p.C + 63) / 64;
+    const int row = (blockIdx.x - joins) / cols;
+    float* to = row == 0 ? p.dweight : p.dbias;
+    if (!to) return;
+    const int c = (blockIdx.x - joins - row * cols) * 64 + lane_id();
+    const float r = column_sum(p.ws + (long)row * p.C, 2L * p.C, (long)p.N * q.slabs, c, p.C);
+    if (threadIdx.x < 64 && c < p.C) to[c] = r;
+    return;
+  }
+  __shared__ float lds[2][kColumnThreads / 64];
   const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
   const float* ws = p.ws + (long)n * q.slabs * 2 * p.C + (long)g * p.cpg;
   const int items = q.slabs * p.cpg;
   float s1 = 0.f, s2 = 0.f;
-  for (int i = threadIdx.x; i < items; i += kThreads) {
+  for (int i = threadIdx.x; i < items; i += kColumnThreads) {
     const int slab = i / p.cpg, c = i - slab * p.cpg;
     const float* o = ws + (long)slab * 2 * p.C + c;
     const float w = p.weight ? p.weight[g * p.cpg + c] : 1.f;
     s2 = fmaf(w, o[0], s2);
     s1 = fmaf(w, o[p.C], s1);
   }
-  const float inv = 1.f / ((float)p.P * (float)p.cpg);
-  s1 = block_sum(s1, lds);
-  s2 = block_sum(s2, lds);
-  if (threadIdx.x == 0) {
-    sums[2 * blockIdx.x] = s1 * inv;
-    sums[2 * blockIdx.x + 1] = s2 * inv;
+  for (int o = 32; o > 0; o >>= 1) {
+    s1 += __shfl_xor(s1, o);
+    s2 += __shfl_xor(s2, o);
+  }
+  if (lane_id() == 0) {
+    lds[0][wave_id()] = s1;
+    lds[1][wave_id()] = s2;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float s = 0.f;
+    for (int k = 0; k < kColumnThreads / 64; ++k) s += lds[threadIdx.x][k];
+    sums[2 * blockIdx.x + threadIdx.x] = s / ((float)p.P * (float)p.cpg);
   }
 }
 
@@ -735,11 +754,8 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t st) {
   const dim3 grid(p.N * q.slabs, q.cblk);
   float* sums = p.ws + (long)p.N * q.slabs * 2 * p.C;
   k_norm_bwd_sums<E, VEC><<<grid, kThreads, 0, st>>>(p, q);
-  k_norm_bwd_join<<<p.N * p.G, kThreads, 0, st>>>(p, q, sums);
+  k_norm_bwd_join<<<p.N * p.G + (p.C + 63) / 64 * 2, kColumnThreads, 0, st>>>(p, q, sums);
   k_norm_bwd_apply<E, VEC><<<grid, kThreads, 0, st>>>(p, q, sums);
-  if (p.dweight || p.dbias)
-    k_norm_params<<<dim3((p.C + 63) / 64, 2), kColumnThreads, 0, st>>>(p.ws, p.dweight, p.dbias,
-                                                                 (long)p.N * q.slabs, p.C);
   return hipGetLastError();
 }
 

@@ -18,7 +18,7 @@
 //     tiles from the last to the first: the tile's states and decays again, kept in registers,
 //     then its tokens backwards;
 //   * sums over channels (dB, dC) and over time (dA, dD, dt_bias) leave partial sums per channel
-//     block and per chunk, which two small kernels add in a fixed order (no atomics).
+//     block and per chunk, which a small kernel adds in a fixed order (no atomics).
 // The sums over the 64 lanes of a wave are the awkward part: dB and dC need one for each (token,
 // state).  A transposing butterfly merges two registers into one at every step (lanes keep the
 // half of the pair that their lane bit names), so 64 sums cost 63 merges, and end one to a lane.
@@ -581,11 +581,26 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
   }
 }
 
-// dB and dC: the channel blocks' partial sums, in order.
+// The partial sums added up.  The first `sums` workgroups take the chunk slots' rows
+// [slots][rows][C]: 64 channels each of a row of dA (transposed to [C, S]), dD or d(dt_bias); the
+// others take dB and dC, a value a thread, over the channel blocks in order.
 template <typename E>
-__global__ __launch_bounds__(256) void k_scan_bwd_bc(const float* bcp, E* dB, E* dC, int Ttot,
-                                                     int G, int S, int Sp, int nblk) {
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(kColumnThreads) void k_scan_bwd_sums(
+    const float* dAp, const float* dvp, const float* bcp, float* dA, float* dD, float* dbias, E* dB,
+    E* dC, int slots, int C, int Ttot, int G, int S, int Sp, int nblk, int sums) {
+  if ((int)blockIdx.x < sums) {
+    const int cols = (C + 63) / 64;
+    const int s = blockIdx.x / cols;  // S rows of dA, then dD, d(dt_bias)
+    const bool vec = s >= S;
+    float* to = !vec ? dA : s == S ? dD : dbias;
+    if (!to) return;
+    const int c = (blockIdx.x - s * cols) * 64 + lane_id();
+    const float r = vec ? column_sum(dvp + (long)(s - S) * C, 2L * C, slots, c, C)
+                        : column_sum(dAp + (long)s * C, (long)S * C, slots, c, C);
+    if (threadIdx.x < 64 && c < C) to[vec ? c : (long)c * S + s] = r;
+    return;
+  }
+  const long i = (long)(blockIdx.x - sums) * kColumnThreads + threadIdx.x;
   const int row = 2 * Sp;
   const long plane = (long)Ttot * G * row;
   if (i >= plane) return;
@@ -593,23 +608,9 @@ __global__ __launch_bounds__(256) void k_scan_bwd_bc(const float* bcp, E* dB, E*
   const int s = k < Sp ? k : k - Sp;
   if (s >= S) return;
   float v = 0.f;
+#pragma unroll 4
   for (int b = 0; b < nblk; ++b) v += bcp[b * plane + i];
   (k < Sp ? dB : dC)[(i / row) * S + s] = (E)v;
-}
-
-// Sums over the chunk slots of rows [slots][rows][C]: dA (transposed to [C, S]), dD and
-// d(dt_bias).
-__global__ __launch_bounds__(kColumnThreads) void k_scan_bwd_params(
-    const float* dAp, const float* dvp, float* dA, float* dD, float* dbias, int slots, int C,
-    int S) {
-  const int s = blockIdx.y;  // S rows of dA, then dD, d(dt_bias)
-  const bool vec = s >= S;
-  float* to = !vec ? dA : s == S ? dD : dbias;
-  if (!to) return;
-  const int c = blockIdx.x * 64 + lane_id();
-  const float r = vec ? column_sum(dvp + (long)(s - S) * C, 2L * C, slots, c, C)
-                      : column_sum(dAp + (long)s * C, (long)S * C, slots, c, C);
-  if (threadIdx.x < 64 && c < C) to[vec ? c : (long)c * S + s] = r;
 }
 
 template <int NW, bool MULTI, typename E>
@@ -617,11 +618,15 @@ hipError_t launch_cfg(const ScanProblem& p, const ScanBwd& b, const BwdArgs& a, 
   // workgroups in a row (and so on XCDs in turn) are a chunk's channel blocks: chunks of unlike
   // lengths then load the XCDs alike
   const unsigned grid = (unsigned)p.slots * a.nb;
-  if (p.slots == 0) {  // no sequences: the parameters' gradients are zero
-    k_scan_bwd_params<<<dim3((p.C + 63) / 64, p.S + 2), kColumnThreads, 0, st>>>(
-        b.dAp, b.dvp, b.dA, b.dD, b.dbias, 0, p.C, p.S);
+  const int sums = (p.C + 63) / 64 * (p.S + 2);
+  auto add_up = [&](long values) {
+    k_scan_bwd_sums<E><<<(unsigned)(sums + (values + kColumnThreads - 1) / kColumnThreads),
+                         kColumnThreads, 0, st>>>(b.dAp, b.dvp, b.bcp, b.dA, b.dD, b.dbias,
+                                                  (E*)b.dB, (E*)b.dC, p.slots, p.C, p.Ttot, p.G,
+                                                  p.S, p.Sp, p.nblk, sums);
     return hipGetLastError();
-  }
+  };
+  if (p.slots == 0) return add_up(0);  // no sequences: the parameters' gradients are zero
   if (a.split) {
     if (a.z)
       k_scan_bwd_state<NW, true, E><<<grid, 64 * NW, 0, st>>>(a);
@@ -633,13 +638,7 @@ hipError_t launch_cfg(const ScanProblem& p, const ScanBwd& b, const BwdArgs& a, 
     k_scan_bwd<NW, MULTI, true, E><<<grid, 64 * NW, 0, st>>>(a);
   else
     k_scan_bwd<NW, MULTI, false, E><<<grid, 64 * NW, 0, st>>>(a);
-  const long n = (long)p.Ttot * p.G * 2 * p.Sp;
-  if (n > 0)
-    k_scan_bwd_bc<E><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
-        b.bcp, (E*)b.dB, (E*)b.dC, p.Ttot, p.G, p.S, p.Sp, p.nblk);
-  k_scan_bwd_params<<<dim3((p.C + 63) / 64, p.S + 2), kColumnThreads, 0, st>>>(
-      b.dAp, b.dvp, b.dA, b.dD, b.dbias, p.slots, p.C, p.S);
-  return hipGetLastError();
+  return add_up((long)p.Ttot * p.G * 2 * p.Sp);
 }
 
 template <typename E>

@@ -122,7 +122,8 @@ def test_conv_gradient_pointers_and_workspace():
 @pytest.mark.parametrize("kw,status", [
     (dict(samples=-1), 1), (dict(positions=-1), 1), (dict(channels=0), 1), (dict(groups=0), 1),
     (dict(groups=5), 1), (dict(dtype=2), 1), (dict(activation=2), 1), (dict(eps=-1.0), 1),
-    (dict(eps=float("nan")), 1), (dict(samples=1 << 22, positions=1), 2)])
+    (dict(eps=float("nan")), 1), (dict(samples=1 << 22), 2),
+    (dict(samples=1 << 22, positions=1, channels=1032, groups=1), 2)])
 def test_norm_descriptors(kw, status):
     d = norm_desc(**kw)
     assert size("gdn_group_norm_workspace_size", d, 1) == (status, 0)
@@ -146,7 +147,8 @@ def test_norm_pointers_and_workspace():
     for i in (0, 4, 5, 6, 7, 10):
         assert gdn.gdn_group_norm_bwd(d, *good[:i], None, *good[i + 1:], 0) == 1, i
     assert gdn.gdn_group_norm_bwd(norm_desc(workspace=A, workspace_bytes=need - 1), *good, 0) == 3
-    # a token's rows need none forward
+    # a token's rows need none forward, however many
+    assert size("gdn_group_norm_workspace_size", norm_desc(samples=1 << 24, positions=1), 0) == (0, 0)
     assert size("gdn_group_norm_workspace_size", norm_desc(positions=1), 0) == (0, 0)
 
 

@@ -203,6 +203,11 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
   // one read is waiting for all of them.  So a step's reads of both kinds are issued together, a
   // step ahead (the first step's and the shares' right after the barrier, ahead of the next tile's
   // preparation), and waited for once.
+  //
+  // Waves in different stages take turns better with priorities than by age, which lets the older
+  // workgroup of a CU run away from the younger.  With 2 states a lane the next tile's preparation
+  // goes first and a wave's claim falls as its tile is done (8 x 2048 tokens of 4096 channels 324
+  // to 268 us); with more, the tokens go first (1 x 8192 tokens 264 to 256 us, 272 the other way).
   const int full = ch.len / TT;
   if (tiles > 0) prepare(0);
   for (int tile = 0; tile < full; ++tile) {
@@ -224,6 +229,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
         zl[i] = zv[i];
       }
     }
+    if (NS == 2) __builtin_amdgcn_s_setprio(3); else __builtin_amdgcn_s_setprio(1);
     prepare(tile + 1);  // past the last tile: never used
     if (OUT) finish(tile - 1, px, pz);
 #pragma unroll
@@ -231,6 +237,10 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
       if (step + 1 < TT / N)
         buf[(step + 1) & 1].load(row + (step + 1) * 32, sd[p] + (step + 1) * N, lane);
       __builtin_amdgcn_sched_barrier(0);
+      if (NS == 2 && 2 * step >= TT / N)
+        __builtin_amdgcn_s_setprio(1);
+      else
+        __builtin_amdgcn_s_setprio(2);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const Step<NS>& q = buf[step & 1];
@@ -238,6 +248,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
   }
   if (full < tiles) {  // the chunk's last tokens
     const int p = full & 1;

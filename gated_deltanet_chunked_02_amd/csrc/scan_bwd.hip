@@ -401,6 +401,9 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
     for (int tile = tiles - 1; tile >= 0; --tile) {
       const int m = min(BT, ch.len - tile * BT);
       const float* row = rows + tile * BT * 2 * NS;
+      // a wave's claim on the vector units falls as its tile is done (see k_scan): 1880 to 1850 us
+      // the 8 x 2048-token step
+      __builtin_amdgcn_s_setprio(3);
       Rows4 r0, r1;  // asked for before the tile's preparation, which hides their latency
       r0.load(row, 0);
       if (m > 4) r1.load(row, 4);
@@ -450,6 +453,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
             }
           }
         }
+        __builtin_amdgcn_s_setprio(1);
         float m1[2], m0[2];
         m1[0] = m1[1] = m0[0] = m0[1] = 0.f;
 #pragma unroll
@@ -496,10 +500,12 @@ __global__ __launch_bounds__(64 * NW) void k_scan_bwd(BwdArgs a) {
           }
         }
       };
+      __builtin_amdgcn_s_setprio(2);
       if (m == BT)
         body(std::true_type());
       else
         body(std::false_type());
+      __builtin_amdgcn_s_setprio(3);
       {
         const int t = ((lane >> 5) & 1) | (lane & 2) | ((lane & 1) << 2);
         const int k = ((lane >> 1) & 2) | ((lane >> 4) & 1), kind = (lane >> 3) & 1;

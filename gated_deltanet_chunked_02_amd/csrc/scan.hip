@@ -232,15 +232,15 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
     if (NS == 2) __builtin_amdgcn_s_setprio(3); else __builtin_amdgcn_s_setprio(1);
     prepare(tile + 1);  // past the last tile: never used
     if (OUT) finish(tile - 1, px, pz);
+    if (NS != 2) __builtin_amdgcn_s_setprio(2);
 #pragma unroll
     for (int step = 0; step < TT / N; ++step) {
       if (step + 1 < TT / N)
         buf[(step + 1) & 1].load(row + (step + 1) * 32, sd[p] + (step + 1) * N, lane);
       __builtin_amdgcn_sched_barrier(0);
-      if (NS == 2 && 2 * step >= TT / N)
-        __builtin_amdgcn_s_setprio(1);
-      else
-        __builtin_amdgcn_s_setprio(2);
+      if (NS == 2) {
+        if (2 * step < TT / N) __builtin_amdgcn_s_setprio(2); else __builtin_amdgcn_s_setprio(1);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const Step<NS>& q = buf[step & 1];

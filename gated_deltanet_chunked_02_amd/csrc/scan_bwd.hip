@@ -22,6 +22,11 @@
 // The sums over the 64 lanes of a wave are the awkward part: dB and dC need one for each (token,
 // state).  A transposing butterfly merges two registers into one at every step (lanes keep the
 // half of the pair that their lane bit names), so 64 sums cost 63 merges, and end one to a lane.
+//
+// Measured on 8 x 2048 tokens of 4096 channels, 16 states, bf16, gated: 1.54 ms in all, of which the
+// chunks' states 342 us (the vector units busy throughout), their composition 58 us (the states'
+// bytes), the gradients 1.18 ms (79 % busy: 202 registers leave two waves a SIMD; a cap at 168 for
+// three spills) and the partial sums 40 us.
 #include <type_traits>
 
 #include "ssm_device.h"
@@ -83,8 +88,9 @@ __device__ __forceinline__ Lane lane_channel(int block, int per, int nblk) {
 // DPP addition of p0 for all lanes and one of p1 that writes only the banks with the bit make a
 // merge in two instructions (a selection before an addition takes three).  Bit 2 adds the mirrored
 // lane of its eight, which pairs the same halves.  A DPP operand must not have been written by the
-// two instructions before: hence the s_nop.
-#define GDN_MERGE4(CTRL, BANKS)                                                        \
+// two instructions before: hence the s_nop.  The lane swaps of the merges after bit 2 have the same
+// rule, and the compiler does not see what these instructions write: hence TAIL.
+#define GDN_MERGE4(CTRL, BANKS, TAIL)                                                  \
   asm("s_nop 1\n\t"                                                                    \
       "v_add_f32_dpp %0, %4, %4 " CTRL " row_mask:0xf bank_mask:0xf\n\t"               \
       "v_add_f32_dpp %1, %5, %5 " CTRL " row_mask:0xf bank_mask:0xf\n\t"               \
@@ -93,15 +99,15 @@ __device__ __forceinline__ Lane lane_channel(int block, int per, int nblk) {
       "v_add_f32_dpp %0, %8, %8 " CTRL " row_mask:0xf bank_mask:" BANKS "\n\t"         \
       "v_add_f32_dpp %1, %9, %9 " CTRL " row_mask:0xf bank_mask:" BANKS "\n\t"         \
       "v_add_f32_dpp %2, %10, %10 " CTRL " row_mask:0xf bank_mask:" BANKS "\n\t"       \
-      "v_add_f32_dpp %3, %11, %11 " CTRL " row_mask:0xf bank_mask:" BANKS              \
+      "v_add_f32_dpp %3, %11, %11 " CTRL " row_mask:0xf bank_mask:" BANKS TAIL         \
       : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])                             \
       : "v"(p0[0]), "v"(p0[1]), "v"(p0[2]), "v"(p0[3]), "v"(p1[0]), "v"(p1[1]),        \
         "v"(p1[2]), "v"(p1[3]))
 __device__ __forceinline__ void merge4_bit3(const float* p0, const float* p1, float* r) {
-  GDN_MERGE4("row_ror:8", "0xc");
+  GDN_MERGE4("row_ror:8", "0xc", "");
 }
 __device__ __forceinline__ void merge4_bit2(const float* p0, const float* p1, float* r) {
-  GDN_MERGE4("row_half_mirror", "0xa");
+  GDN_MERGE4("row_half_mirror", "0xa", "\n\ts_nop 1");
 }
 #undef GDN_MERGE4
 

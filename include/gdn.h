@@ -205,7 +205,9 @@ gdn_status gdn_causal_conv1d_fwd(const gdn_conv_desc* d, const void* x, const fl
  *   A          [channels, dstate]       f32 (negative in the intended use)
  *   D, dt_bias [channels]               f32
  *   h0, ht     [N, channels, dstate]    f32; cu_seqlens [N + 1] int32 as for gdn_chunk_fwd
- * Any channels, groups dividing it, dstate 1 .. 256.  Pointers are device pointers aligned to
+ * Any channels, groups dividing it, dstate 1 .. 256.  GDN_ERR_UNSUPPORTED beyond 2^30 tokens,
+ * 65536 sequences, 2^20 channels, launches of 2^32 threads, or with rows so long that 256 of them
+ * pass 2 GiB.  Pointers are device pointers aligned to
  * their element; errors are returned before any launch; nothing is synchronised or allocated.
  * x, dt, A, Bm, Cm, y are required unless B*T = 0 (A always).  h0 and ht may be the same
  * buffer.  Few or long sequences are split into chunks that run in parallel, so results depend
@@ -296,7 +298,9 @@ gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const fl
  * x, gate, y [samples, positions, channels] dtype (bf16 or f32), contiguous; weight, bias
  * [channels] f32 or NULL (ones, zeros); mean, rstd [samples, groups] f32, written unless NULL (the
  * backward needs them).  Statistics are fp32 sums about the mean.  Any channels, groups dividing
- * it; pointers aligned to their element (vectors are used where 16 bytes fit). */
+ * it, up to 2^20 (GDN_ERR_UNSUPPORTED beyond, and beyond 2^21 (sample, group) pairs unless positions
+ * is 1 and a group has at most 1024 channels); pointers aligned to their element (vectors are used
+ * where 16 bytes fit). */
 typedef struct gdn_norm_desc {
   int32_t samples, positions, channels, groups;
   int32_t dtype;       /* gdn_dtype of x, gate, y, dy, dx, dgate */

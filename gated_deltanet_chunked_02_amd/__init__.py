@@ -16,6 +16,8 @@ gdn_fused_sigmoid_gating_delta_rule):
 The short convolution before it (low level gdn_causal_conv1d_fwd):
     y = causal_conv1d(x, weight, bias=None, conv_state=None, cache_indices=None,
                       has_initial_state=None, cu_seqlens=None, activation=None)
+The selective state-space layer (module ssm): selective_scan, selective_scan_bwd,
+selective_state_update, causal_conv1d_bwd, group_norm, group_norm_bwd.
 """
 from __future__ import annotations
 

@@ -69,11 +69,13 @@ gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) 
 // How the forward runs: states a lane and waves a workgroup (ns nw >= dstate), and the chunk
 // length.  Measured with 16 states (workgroups: sequences times 64-channel blocks):
 //   * from one workgroup a CU on, whole sequences are quicker than chunks, which cost a second
-//     pass: 8 x 2048 tokens of 4096 channels take 339 us whole and 483 us in chunks of 256; 2
-//     states a lane then give the waves that 4 would not (339 against 365 us).  A packed batch
+//     pass: 8 x 2048 tokens of 4096 channels take 268 us whole (before its waves' priorities 339,
+//     where chunks of 256 took 483); 2 states a lane then give the waves that 4 would not (268
+//     against 281 us).  A packed batch
 //     is split at twice its mean length, so that one long sequence does not run alone;
 //   * below that the sequences are split into chunks that fill the GPU, at least 128 tokens
-//     long: 1 x 8192 tokens take 735 us whole, 272 us in chunks of 256 (281 at 512, 291 at 128).
+//     long: 1 x 8192 tokens take 257 us in chunks of 256 (272 before the priorities, where 512
+//     took 281, 128 took 291 and the whole sequence 735).
 constexpr int kUnits = 256;        // CUs
 constexpr int kFillWaves = 8192;   // waves wanted of a split batch
 constexpr int kMinChunk = 128;

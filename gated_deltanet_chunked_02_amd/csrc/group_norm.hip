@@ -22,6 +22,10 @@
 //   * a workgroup for each (sample, group), for maps so small that three launches would cost
 //     more than reading them in short pieces.
 // Statistics and sums are fp32; every output is rounded once; sums have a fixed order.
+//
+// 16384 gated rows of 4096 channels in 32 groups, bf16 (403 MB) take 74 us, 5.4 TB/s, an addition
+// of the same tensors 70; 8 maps of 4096 positions and 512 channels take 33 us forward and 48 us
+// backward, in which every pass of 33 to 100 MB has about 5 us of start and end.
 #include "norm.h"
 #include "ssm_device.h"
 
@@ -668,8 +672,8 @@ int pow2_at_least(int n) {
 
 constexpr int kRowVecs = 4;       // vectors of a segment a lane holds, at most
 constexpr int kWantGroups = 2048;  // workgroups of a map's pass
-// workgroups that share out rows: four a CU, which all run at once (16384 gated rows of 4096 channels
-// take 81 us; 107 with 512, 93 with 2048, 83 with 8192)
+// workgroups that share out rows: four a CU, which all run at once (16384 gated rows of 4096 channels,
+// in one run: 81 us; 107 with 512, 93 with 2048, 83 with 8192; 74 since y is stored past the caches)
 constexpr int kRowGroups = 1024;
 
 // Rows: P = 1 and a group that fits the lanes' registers.

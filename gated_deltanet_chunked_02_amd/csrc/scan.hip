@@ -18,6 +18,12 @@
 //     into chunks: a first pass finds each chunk's own end state from a zero start and its sum
 //     of steps, a small kernel composes the chunks' start states in order (the decay of a
 //     chunk is exp(A * sum of steps)), and the output pass starts from them.
+//
+// Measured with 4096 channels, 16 states, bf16, gated (bytes alone at a copy's 5.1 TB/s in
+// brackets): 8 x 2048 tokens 268 us (71), the vector units busy in 90 % of the cycles (127 M vector
+// instructions, 80 of 121 a token and channel in the recurrence itself); 12454 packed tokens in
+// eight sequences 251 us (80); one sequence of 8192 tokens, in 32 chunks, 257 us (52), of which
+// 113 us is the first pass.
 #include "ssm_device.h"
 
 namespace gdn {

@@ -7,7 +7,9 @@
 // when S is a multiple of 4 and the pool and A are aligned to that), so a wave's loads of the pool
 // and of A are contiguous; y is summed over the LPC lanes.  A workgroup keeps to its channels for
 // `seqs` sequences, so A is loaded once for them, and every sequence's loads are issued before the
-// one before it computes.
+// one before it computes.  256 sequences of 4096 channels and 16 states (143 MB) take 26 us when the
+// last pool is still in the last-level cache and 34 us from HBM (4.2 TB/s; a copy takes 28); one
+// sequence takes 3.6 us.
 #include "ssm_device.h"
 
 namespace gdn {

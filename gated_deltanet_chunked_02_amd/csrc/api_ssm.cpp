@@ -67,33 +67,37 @@ gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) 
 }
 
 // How the forward runs: states a lane and waves a workgroup (ns nw >= dstate), and the chunk
-// length.  Measured with 16 states (workgroups: sequences times 64-channel blocks):
-//   * from one workgroup a CU on, whole sequences are quicker than chunks, which cost a second
-//     pass: 8 x 2048 tokens of 4096 channels take 268 us whole (before its waves' priorities 339,
-//     where chunks of 256 took 483); 2 states a lane then give the waves that 4 would not (268
-//     against 281 us).  A packed batch
-//     is split at twice its mean length, so that one long sequence does not run alone;
-//   * below that the sequences are split into chunks that fill the GPU, at least 128 tokens
-//     long: 1 x 8192 tokens take 257 us in chunks of 256 (272 before the priorities, where 512
-//     took 281, 128 took 291 and the whole sequence 735).
-constexpr int kUnits = 256;        // CUs
-constexpr int kFillWaves = 8192;   // waves wanted of a split batch
-constexpr int kMinChunk = 128;
+// length.  Few states a lane give many waves: with 16 states, 2 a lane take 268 us for 8 x 2048
+// tokens of 4096 channels and 18.3 us for 129 tokens of 1000, 4 a lane 281 and 24.1 us.
+//   * where the (sequence, 64-channel block) pairs are more than a third of the workgroups that run
+//     at once, whole sequences are quicker than chunks, which cost a second pass: 3 x 2048 tokens of
+//     4096 channels take 191 us whole and 243 us in two chunks each, 4 x 2048 of 2560 channels as
+//     long whole and 171 us in three each.  A packed batch is split at twice its mean length, so that
+//     one long sequence does not run alone;
+//   * below that the sequences are split into as many chunks as run at once, which LDS bounds
+//     (k_scan: 16 KB and 8 KB a wave of a CU's 160 KB): 1 x 8192 tokens of 4096 channels take 247 us
+//     in 8 chunks, 257 us in 32, 325 us in 10 (a second round), and about 700 us whole;
+//   * a chunk has at least 32 tokens, which pay for the two more launches: 400 tokens of 1000 channels
+//     take 18.9 us in chunks of 32, 21.7 us of 16, 22.8 us of 64 and 38.5 us of 128.  Splitting saves
+//     7 us of 25 on 200 tokens; on 129 it saves 1 us, less than a host needs for the launches.
+constexpr int kUnits = 256;  // CUs
+constexpr int kMinChunk = 32;
+constexpr int kMinSplit = 192;
 
 void plan_fwd(gdn::ScanProblem* p, bool packed) {
   const long long blocks = (long long)p->G * p->nblk;
-  const bool whole = p->N * blocks >= kUnits;
-  p->ns = p->S <= 8 || (whole && p->S <= 16) ? 2 : p->S <= 32 ? 4 : p->S <= 128 ? 8 : 16;
-  p->nw = p->ns == 2 ? 2 : p->ns == 16 ? 16 : 4;
+  p->ns = p->S <= 16 ? 2 : p->S <= 32 ? 4 : p->S <= 128 ? 8 : 16;
+  p->nw = p->ns == 2 ? 2 : p->ns == 16 ? 16 : 8;
   while (p->nw * p->ns < p->S) p->nw *= 2;
   p->Sp = p->ns * p->nw;
   p->Lc = gdn::kScanNoSplit;
   if (p->N > 0 && p->Ttot > 0) {
     const long long longest = packed ? p->Ttot : p->T;
     long long L = longest;
-    if (!whole) {
-      const long long chunks = (kFillWaves + blocks * p->nw - 1) / (blocks * p->nw);
-      L = (p->Ttot + chunks - 1) / chunks;
+    const long long fill = kUnits * (160 / (16 + 8 * p->nw)) / blocks;
+    if (fill >= 3 * p->N) {
+      const long long each = packed ? fill : fill / p->N;
+      L = (longest + each - 1) / each;
     } else if (packed) {
       L = 2LL * ((p->Ttot + p->N - 1) / p->N);
     }
@@ -101,7 +105,7 @@ void plan_fwd(gdn::ScanProblem* p, bool packed) {
     if (L < kMinChunk) L = kMinChunk;
     // a chunk's rows are reached with 31-bit offsets
     if (L > p->reach) L = p->reach;
-    if (2 * L <= longest || longest > p->reach) p->Lc = (int)L;
+    if ((2 * L <= longest && longest >= kMinSplit) || longest > p->reach) p->Lc = (int)L;
   }
   p->slots = packed ? p->Ttot / p->Lc + p->N
                     : p->N * (int)(p->T > p->Lc ? ((long long)p->T + p->Lc - 1) / p->Lc : 1);
@@ -137,12 +141,21 @@ ScanLayout scan_layout(const gdn::ScanProblem& p) {
 // with blocks of 16 the sums carried from block to block leave LDS for one workgroup of four
 // waves a CU, and 4 x 2048 tokens of 4096 channels and 64 states took 4950 us).  A packed batch has
 // more slots than sequences unless it is empty, so it is composed even when no sequence is long.
+// Chunks are halved, down to 16 tokens, while they give fewer waves than SIMDs: forward and
+// backward of 257 tokens of 2 x 768 channels take 53.8 us (64-token chunks: 71), of 1000 tokens of
+// 1024 channels 74 us in chunks of 32 (64: 81, 16: 83), of 1000 tokens of 2048 channels 101 us in
+// chunks of 64 (32: 108).
+constexpr int kBwdMin = 16;
+constexpr int kBwdFill = 1024;
+
 void plan_bwd(gdn::ScanProblem* p, bool packed) {
   p->ns = 4;
   p->nw = p->S <= 4 ? 1 : p->S <= 8 ? 2 : p->S <= 16 ? 4 : 8;
   const int block = p->ns * p->nw;
   p->Sp = (p->S + block - 1) / block * block;
   p->Lc = gdn::kBwdChunk;
+  while (p->Lc > kBwdMin && (long long)(p->Ttot / p->Lc) * p->G * p->nblk * p->nw < kBwdFill)
+    p->Lc /= 2;
   p->slots = p->N == 0 ? 0
              : packed  ? p->Ttot / p->Lc + p->N
                        : p->N * (p->T > p->Lc ? (p->T + p->Lc - 1) / p->Lc : 1);

@@ -16,14 +16,13 @@
 //     channel) and sum y there; few states a lane keep the registers low and many waves live;
 //   * when the (sequence, channel block) pairs are too few to fill the GPU, sequences are split
 //     into chunks: a first pass finds each chunk's own end state from a zero start and its sum
-//     of steps, a small kernel composes the chunks' start states in order (the decay of a
-//     chunk is exp(A * sum of steps)), and the output pass starts from them.
+//     of steps, the chunks' start states are composed in order (the decay of a chunk is
+//     exp(A * sum of steps)), and the output pass starts from them.
 //
 // Measured with 4096 channels, 16 states, bf16, gated (bytes alone at a copy's 5.1 TB/s in
 // brackets): 8 x 2048 tokens 268 us (71), the vector units busy in 90 % of the cycles (127 M vector
 // instructions, 80 of 121 a token and channel in the recurrence itself); 12454 packed tokens in
-// eight sequences 251 us (80); one sequence of 8192 tokens, in 32 chunks, 257 us (52), of which
-// 113 us is the first pass.
+// eight sequences 246 us (80); one sequence of 8192 tokens, in 8 chunks, 246 us (52).
 #include "ssm_device.h"
 
 namespace gdn {
@@ -51,6 +50,14 @@ struct ScanArgs {
   int nb;  // channel blocks in all (G nblk)
   int softplus, split;
 };
+
+// Chunks' start states: none (whole sequences), composed by k_scan_combine, or by each workgroup of
+// the output pass from the chunks before its own.  The last saves a launch and is quicker with 2
+// states a lane for up to 8 chunks a sequence (12454 packed tokens in eight sequences 254 to 246 us,
+// 300 tokens of 4096 channels 26.9 to 24.2 us); 13 chunks of 1000 channels take 20.6 us so and 19.0
+// composed, and 64 states in 16 chunks 85 and 72 us.
+constexpr int kComposed = 1, kOwn = 2;
+constexpr int kOwnChunks = 8;
 
 // B and C of every token and group as padded fp32 rows [G][Sp / ns][Ttot][2][ns], so that the
 // scan reads them through the scalar cache whatever their type, alignment, strides and number: a
@@ -156,10 +163,23 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
     A2[k] = s < a.S ? a.A[(long)l.c * a.S + s] * kLog2e : 0.f;
     h[k] = 0.f;
     if (OUT && s < a.S) {
-      if (a.split)
+      if (a.split == kComposed)
         h[k] = a.hst[((long)slot * a.S + s) * a.C + l.c];
       else if (a.h0)
         h[k] = a.h0[((long)ch.n * a.C + l.c) * a.S + s];
+    }
+  }
+  if (OUT && NS == 2 && a.split == kOwn) {  // over the chunks before this one
+    const float* ds = a.dsum + (long)(slot - ch.i) * a.C + l.c;
+    const float* hst = a.hst + ((long)(slot - ch.i) * a.S + s0) * a.C + l.c;
+#pragma unroll 4
+    for (int j = 0; j < ch.i; ++j) {
+      const float d = ds[(long)j * a.C];
+#pragma unroll
+      for (int k = 0; k < NS; ++k)
+        if (s0 + k < a.S)
+          h[k] = fmaf(__builtin_amdgcn_exp2f(d * A2[k]), h[k],
+                      hst[((long)j * a.S + k) * a.C]);
     }
   }
 
@@ -211,9 +231,8 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
   // preparation), and waited for once.
   //
   // Waves in different stages take turns better with priorities than by age, which lets the older
-  // workgroup of a CU run away from the younger.  With 2 states a lane the next tile's preparation
-  // goes first and a wave's claim falls as its tile is done (8 x 2048 tokens of 4096 channels 324
-  // to 268 us); with more, the tokens go first (1 x 8192 tokens 264 to 256 us, 272 the other way).
+  // workgroup of a CU run away from the younger: the next tile's preparation goes first and a wave's
+  // claim falls as its tile is done (8 x 2048 tokens of 4096 channels 324 to 268 us).
   const int full = ch.len / TT;
   if (tiles > 0) prepare(0);
   for (int tile = 0; tile < full; ++tile) {
@@ -235,18 +254,15 @@ __global__ __launch_bounds__(64 * NW) void k_scan(ScanArgs a) {
         zl[i] = zv[i];
       }
     }
-    if (NS == 2) __builtin_amdgcn_s_setprio(3); else __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_s_setprio(3);
     prepare(tile + 1);  // past the last tile: never used
     if (OUT) finish(tile - 1, px, pz);
-    if (NS != 2) __builtin_amdgcn_s_setprio(2);
 #pragma unroll
     for (int step = 0; step < TT / N; ++step) {
       if (step + 1 < TT / N)
         buf[(step + 1) & 1].load(row + (step + 1) * 32, sd[p] + (step + 1) * N, lane);
       __builtin_amdgcn_sched_barrier(0);
-      if (NS == 2) {
-        if (2 * step < TT / N) __builtin_amdgcn_s_setprio(2); else __builtin_amdgcn_s_setprio(1);
-      }
+      if (2 * step < TT / N) __builtin_amdgcn_s_setprio(2); else __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const Step<NS>& q = buf[step & 1];
@@ -333,7 +349,8 @@ hipError_t launch_cfg(const ScanProblem& p, const ScanArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)p.slots * a.nb;
   if (a.split) {
     k_scan<NS, NW, false, false, E><<<grid, 64 * NW, 0, st>>>(a);
-    k_scan_combine<<<dim3(p.N * p.S, (p.C + 255) / 256), 256, 0, st>>>(a);
+    if (a.split == kComposed)
+      k_scan_combine<<<dim3(p.N * p.S, (p.C + 255) / 256), 256, 0, st>>>(a);
   }
   if (a.z)
     k_scan<NS, NW, true, true, E><<<grid, 64 * NW, 0, st>>>(a);
@@ -348,7 +365,6 @@ hipError_t launch_e(const ScanProblem& p, const ScanArgs& a, hipStream_t st) {
     case 202: return launch_cfg<2, 2, E>(p, a, st);
     case 204: return launch_cfg<2, 4, E>(p, a, st);
     case 208: return launch_cfg<2, 8, E>(p, a, st);
-    case 404: return launch_cfg<4, 4, E>(p, a, st);
     case 408: return launch_cfg<4, 8, E>(p, a, st);
     case 808: return launch_cfg<8, 8, E>(p, a, st);
     case 816: return launch_cfg<8, 16, E>(p, a, st);
@@ -399,7 +415,8 @@ hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t st) {
   a.nb = p.G * p.nblk;
   a.Sp = p.Sp;
   a.softplus = p.softplus;
-  a.split = p.Lc != kScanNoSplit;
+  const long chunks = ((p.cu ? p.Ttot : p.T) + p.Lc - 1L) / p.Lc;
+  a.split = p.Lc == kScanNoSplit ? 0 : p.ns == 2 && chunks <= kOwnChunks ? kOwn : kComposed;
   return p.f32 ? launch_e<float>(p, a, st) : launch_e<bf16>(p, a, st);
 }
 

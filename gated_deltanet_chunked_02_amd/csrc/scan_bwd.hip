@@ -8,7 +8,7 @@
 //
 // The mapping is the forward's: a lane is a channel, B and C come through the scalar cache, the
 // states of 64 channels are split over the waves of a workgroup.  Nothing of the forward is kept:
-// every sequence is split into chunks of kBwdChunk tokens, and
+// every sequence is split into chunks of up to kBwdChunk tokens, and
 //   * k_scan_bwd_state finds, for every chunk from zero boundaries, its end state and the gradient
 //     a g that it hands to the chunk before it (both in one pass over its tokens: the gradient's
 //     factors are the running products of a), and its sum of steps;
@@ -36,7 +36,7 @@ namespace gdn {
 namespace {
 
 constexpr int BT = 8;                  // tokens of a tile
-constexpr int KT = kBwdChunk / BT;     // tiles of a chunk
+constexpr int KT = kBwdChunk / BT;     // tiles of a chunk, at most
 constexpr int NS = 4;                  // states a lane
 
 struct BwdArgs {

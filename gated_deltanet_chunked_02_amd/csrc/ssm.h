@@ -48,7 +48,7 @@ hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t st);
 // B and C as padded fp32 rows (p.bc).
 hipError_t launch_scan_pack(const ScanProblem& p, hipStream_t st);
 
-// Backward: the same problem at chunks of kBwdChunk tokens, nw waves of 4 states (blocks of 32
+// Backward: the same problem at chunks of up to kBwdChunk tokens, nw waves of 4 states (blocks of 32
 // states one after another when there are more), plus the gradients.
 constexpr int kBwdChunk = 64;
 struct ScanBwd {

@@ -154,6 +154,13 @@ def _rows(t, lead):
     return (t, row) if row >= width else (t.contiguous(), 0)
 
 
+def _new(t):
+    """A new contiguous tensor of t's shape, dtype and device, or None.  t is contiguous or has
+    evenly spaced rows (see _rows), whose order an empty_like keeps; it takes a third of the time of
+    an empty with the three given."""
+    return None if t is None else torch.empty_like(t)
+
+
 def _on(device, **named):
     """Every tensor given on ``device``, a CUDA (HIP) device."""
     _check_devices(named, device)
@@ -282,10 +289,10 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
     _on(dev, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, initial_state=h0,
         cu_seqlens=cu, workspace=workspace)
     desc.B, desc.T, desc.N, desc.dt_softplus = x.shape[0], x.shape[1], N, int(bool(dt_softplus))
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    y = _new(x)
     ht = None
     if output_final_state:
-        ht = torch.empty((N, desc.channels, desc.dstate), device=dev, dtype=torch.float32)
+        ht = A.new_empty((N, desc.channels, desc.dstate)) if h0 is None else _new(h0)
     if x.shape[0] == 0:
         return y, ht
     ws = _workspace(desc, gdn_selective_scan_workspace_size(desc), workspace, dev)  # noqa: F841
@@ -313,8 +320,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_soft
         dht=dht, cu_seqlens=cu, workspace=workspace)
     dy = dy.contiguous()
     desc.B, desc.T, desc.N, desc.dt_softplus = x.shape[0], x.shape[1], N, int(bool(dt_softplus))
-    new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)  # noqa: E731
-    dx, ddt, dA, dB, dC, dD, dz, dbias, dh0 = map(new, (x, dt, A, B, C, D, z, dt_bias, h0))
+    dx, ddt, dA, dB, dC, dD, dz, dbias, dh0 = map(_new, (x, dt, A, B, C, D, z, dt_bias, h0))
     if x.shape[0] == 0:
         return dx, ddt, dA.zero_(), dB, dC, _zero(dD), dz, _zero(dbias), dh0
     need = gdn_selective_scan_bwd_workspace_size(desc)
@@ -353,7 +359,7 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     dev = x.device
     _on(dev, state=state, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
         cache_indices=read, out_indices=write)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    y = _new(x)
     if n == 0:
         return y
     desc.B, desc.T, desc.N, desc.dt_softplus = n, 1, n, int(bool(dt_softplus))
@@ -410,11 +416,8 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
     desc = GdnConvDesc(B=B, T=T, N=N, channels=C, width=W, dtype=_code(x),
                        activation=ACTIVATIONS[activation], state_lines=0)
     dev = x.device
-    dx = torch.empty(x.shape, device=dev, dtype=x.dtype)
-    dweight = torch.empty(weight.shape, device=dev, dtype=torch.float32)
-    dbias = None if bias is None else torch.empty(C, device=dev, dtype=torch.float32)
     first = lines["initial_state"]
-    dinit = None if first is None else torch.empty(first.shape, device=dev, dtype=x.dtype)
+    dx, dweight, dbias, dinit = _new(x), _new(weight), _new(bias), _new(first)
     if B == 0:
         return dx, dweight.zero_(), _zero(dbias), dinit
     need = gdn_causal_conv1d_bwd_workspace_size(desc)
@@ -454,25 +457,29 @@ def gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight,
 
 
 def _norm_operands(x, num_groups, weight, bias, eps, activation, gate):
-    _need(isinstance(x, torch.Tensor), TypeError, "x must be a torch tensor")
-    code = _code(x)
-    _need(code is not None, TypeError, "x must be bf16 or fp32, got %s" % x.dtype)
-    _need(x.dim() >= 2 and x.shape[-1] > 0, ValueError,
-          "x must be [samples, channels] or [samples, ..., channels]")
-    _need(activation in ACTIVATIONS, ValueError, "activation must be None, 'none' or 'silu'")
-    C = x.shape[-1]
-    _need(isinstance(num_groups, int) and num_groups > 0 and C % num_groups == 0, ValueError,
-          "num_groups must divide the %d channels, got %r" % (C, num_groups))
-    _need(eps >= 0, ValueError, "eps must not be negative")
+    if not isinstance(x, Tensor):
+        raise TypeError("x must be a torch tensor")
+    code, shape = _CODES.get(x.dtype), x.shape
+    if code is None:
+        raise TypeError("x must be bf16 or fp32, got %s" % x.dtype)
+    if len(shape) < 2 or shape[-1] == 0:
+        raise ValueError("x must be [samples, channels] or [samples, ..., channels]")
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be None, 'none' or 'silu'")
+    C = shape[-1]
+    if not isinstance(num_groups, int) or num_groups <= 0 or C % num_groups:
+        raise ValueError("num_groups must divide the %d channels, got %r" % (C, num_groups))
+    if not eps >= 0:
+        raise ValueError("eps must not be negative")
     weight, bias = _f32("weight", weight, (C,)), _f32("bias", bias, (C,))
     _like("gate", gate, x)
     if gate is not None:
         gate = gate.contiguous()
     positions = 1
-    for n in x.shape[1:-1]:
+    for n in shape[1:-1]:
         positions *= n
-    desc = GdnNormDesc(samples=x.shape[0], positions=positions, channels=C, groups=num_groups,
-                       dtype=code, activation=ACTIVATIONS[activation], eps=eps)
+    desc = GdnNormDesc(shape[0], positions, C, num_groups, code, ACTIVATIONS[activation], eps, None,
+                       0)
     return desc, x.contiguous(), weight, bias, gate
 
 
@@ -489,9 +496,9 @@ def group_norm(x, num_groups, weight=None, bias=None, eps=1e-5, activation=None,
                                                  gate)
     dev = x.device
     _on(dev, x=x, weight=weight, bias=bias, gate=gate, workspace=workspace)
-    y = torch.empty(x.shape, device=dev, dtype=x.dtype)
-    mean = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
-    rstd = torch.empty((x.shape[0], num_groups), device=dev, dtype=torch.float32)
+    y = _new(x)
+    mean = x.new_empty((x.shape[0], num_groups), dtype=torch.float32)
+    rstd = _new(mean)
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc), workspace, dev)  # noqa: F841
     st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, _current_stream(dev))
     if st != 0:
@@ -515,8 +522,7 @@ def group_norm_bwd(dy, x, num_groups, mean, rstd, weight=None, bias=None, activa
     _on(dev, x=x, dy=dy, mean=mean, rstd=rstd, weight=weight, bias=bias, gate=gate,
         workspace=workspace)
     dy = dy.contiguous()
-    new = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)  # noqa: E731
-    dx, dweight, dbias, dgate = map(new, (x, weight, bias, gate))
+    dx, dweight, dbias, dgate = map(_new, (x, weight, bias, gate))
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc, True), workspace, dev)  # noqa: F841
     st = gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight, dbias,
                             dgate, _current_stream(dev))

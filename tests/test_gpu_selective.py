@@ -123,6 +123,35 @@ def test_packed_matches_oracle(lens, dtype):
             assert torch.equal(ht[n].cpu(), p["h0"][n])
 
 
+@pytest.mark.parametrize("B,T,C,G,S,dtype", [
+    (1, 31, 64, 1, 16, "f32"), (1, 32, 64, 1, 16, "bf16"), (1, 63, 64, 1, 16, "f32"),
+    (1, 64, 64, 1, 16, "bf16"), (1, 65, 65, 1, 16, "f32"), (2, 97, 64, 1, 8, "f32"),
+    (2, 100, 130, 130, 16, "f32"),   # blocks enough for whole sequences
+    (1, 90, 200, 200, 4, "bf16"),
+    (1, 70, 190, 95, 256, "f32"),
+    (1, 400, 50, 50, 16, "f32"),     # chunks of 48 tokens
+    (3, 200, 40, 40, 64, "f32"),
+])
+def test_chunk_lengths(B, T, C, G, S, dtype):
+    """Lengths about a chunk's, whole sequences and longer chunks (a group has its own channel
+    blocks, so many groups of few channels make many workgroups)."""
+    p = make(B, T, C, G, S, dtype, seed=B + T + C + S)
+    y_ref, ht_ref = oracle_fwd(p)
+    y, ht = run_fwd(p)
+    check("y", y, y_ref, TOL[dtype])
+    check("ht", ht, ht_ref, TOL_F32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_packed_of_many_blocks_matches_oracle(dtype):
+    """Sequences split at twice their mean length."""
+    p = make(C=104, G=104, S=16, dtype=dtype, lens=[3, 500, 0, 129, 1, 63], seed=2)
+    y_ref, ht_ref = oracle_fwd(p)
+    y, ht = run_fwd(p)
+    check("y", y, y_ref, TOL[dtype])
+    check("ht", ht, ht_ref, TOL_F32)
+
+
 def test_without_softplus_bias_or_skip():
     p = make(2, 50, 64, 1, 16, D=False, bias=False, seed=9)
     p["dt"] = torch.rand(p["dt"].shape, generator=torch.Generator().manual_seed(1)) * 0.1

@@ -73,6 +73,28 @@ def test_gradients_match_oracle(B, T, C, G, S, dtype, z, h0, dht):
     check_all(p, run_bwd(p, dht=dht), oracle_bwd(p, dht=dht), dtype)
 
 
+@pytest.mark.parametrize("B,T,C,G,S,dtype", [
+    (1, 16, 64, 1, 16, "f32"), (1, 17, 64, 1, 16, "bf16"), (1, 31, 64, 1, 4, "f32"),
+    (1, 130, 128, 64, 16, "f32"),    # chunks of 32 tokens
+    (1, 330, 128, 64, 16, "f32"),    # of 64
+    (2, 129, 128, 64, 16, "bf16"),
+    (1, 650, 128, 64, 8, "bf16"),
+    (1, 140, 128, 64, 40, "f32"),    # and two blocks of states
+    (1, 1100, 128, 64, 2, "f32"),
+])
+def test_chunk_lengths(B, T, C, G, S, dtype):
+    """Chunks of every length that the number of workgroups chooses (a group has its own channel
+    blocks, so many groups of few channels make many workgroups)."""
+    p = make(B, T, C, G, S, dtype, seed=B + T + C + S)
+    check_all(p, run_bwd(p), oracle_bwd(p), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_packed_gradients_of_many_blocks_match_oracle(dtype):
+    p = make(C=128, G=64, S=16, dtype=dtype, lens=[3, 200, 0, 129, 1, 63], seed=2)
+    check_all(p, run_bwd(p), oracle_bwd(p), dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("lens", [[1], [5, 0, 1, 64, 65, 2], [0, 0, 7], [3, 300, 0, 129, 1, 63],
                                   [1] * 70, [0, 0]])

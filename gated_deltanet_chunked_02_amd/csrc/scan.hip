@@ -55,7 +55,8 @@ struct ScanArgs {
 // the output pass from the chunks before its own.  The last saves a launch and is quicker with 2
 // states a lane for up to 8 chunks a sequence (12454 packed tokens in eight sequences 254 to 246 us,
 // 300 tokens of 4096 channels 26.9 to 24.2 us); 13 chunks of 1000 channels take 20.6 us so and 19.0
-// composed, and 64 states in 16 chunks 85 and 72 us.
+// composed, and 64 states in 16 chunks 85 and 72 us.  It reads h0 in every chunk's workgroup while the
+// last chunk's writes ht, so a call with one buffer for both is composed instead (the same bits).
 constexpr int kComposed = 1, kOwn = 2;
 constexpr int kOwnChunks = 8;
 
@@ -416,7 +417,10 @@ hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t st) {
   a.Sp = p.Sp;
   a.softplus = p.softplus;
   const long chunks = ((p.cu ? p.Ttot : p.T) + p.Lc - 1L) / p.Lc;
-  a.split = p.Lc == kScanNoSplit ? 0 : p.ns == 2 && chunks <= kOwnChunks ? kOwn : kComposed;
+  const bool in_place = p.h0 && p.h0 == p.ht;
+  a.split = p.Lc == kScanNoSplit                              ? 0
+            : p.ns == 2 && chunks <= kOwnChunks && !in_place ? kOwn
+                                                              : kComposed;
   return p.f32 ? launch_e<float>(p, a, st) : launch_e<bf16>(p, a, st);
 }
 

@@ -1,0 +1,76 @@
+"""The selective scan's ways of running a batch (whole sequences, chunks whose start states a launch
+of its own composes, chunks that compose their own), each against the fp64 oracle and each with the
+states carried in place.
+
+Every case names the chunk slots it is meant for, which the workspace's size gives away (see
+``slots_of``): 0 for whole sequences, else sequence by sequence its chunks (and one more a sequence of
+a packed batch or of a batch of one, which may come as either, at most).  Tolerances, relative L2.  fp32: a state is a sum over its tokens, each rounded
+twice, and over chunks whose decay's exponent is rounded once; rounding errors of unlike sign over the
+at most 600 tokens here add up to about sqrt(1200) x 2^-24 = 2e-6 of it: 1e-5.  bf16 outputs: one
+rounding to 8 significant bits more, 2^-8 + 1e-5.
+"""
+import pytest
+import torch
+
+from test_gpu_selective import TOL, TOL_F32, check, dev, make, oracle_fwd, run_fwd
+
+pytestmark = pytest.mark.gpu
+
+
+def desc_of(p):
+    import gated_deltanet_chunked_02_amd as gdn
+    B, T, C = p["x"].shape
+    N = B if p["cu"] is None else p["cu"].numel() - 1
+    return gdn.GdnScanDesc(B=B, T=T, N=N, channels=C, groups=p["B"].shape[2],
+                           dstate=p["A"].shape[1], dtype=int(p["x"].dtype == torch.bfloat16),
+                           dt_softplus=1)
+
+
+def slots_of(d):
+    """Chunk slots the forward plans: what its workspace holds beside the B and C rows."""
+    import gated_deltanet_chunked_02_amd as gdn
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    rest = gdn.gdn_selective_scan_workspace_size(d)
+    padded = next(n for n in (4, 8, 16, 32, 64, 128, 256) if n >= d.dstate)
+    rest -= up(d.B * d.T * d.groups * 2 * padded * 4)
+    slots = 0
+    while up(slots * d.dstate * d.channels * 4) + up(slots * d.channels * 4) < rest:
+        slots += 1
+    return slots
+
+
+def run_in_place(p, ht=None):
+    """The raw call on one buffer for the initial and the final states (or on ``ht``)."""
+    import gated_deltanet_chunked_02_amd as gdn
+    q = dev(p)
+    d = desc_of(p)
+    ws = torch.empty(gdn.gdn_selective_scan_workspace_size(d), dtype=torch.uint8, device="cuda")
+    d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
+    y = torch.empty_like(q["x"])
+    ht = q["h0"] if ht is None else ht
+    st = gdn.gdn_selective_scan_fwd(d, q["x"], q["dt"], q["A"], q["B"], q["C"], q["D"], q["z"],
+                                    q["dt_bias"], q["h0"], q["cu"], y, ht)
+    torch.cuda.synchronize()
+    assert st == 0
+    return y, ht
+
+
+@pytest.mark.parametrize("B,T,C,G,S,lens,slots", [
+    (2, 60, 64, 1, 16, None, 0),      # whole sequences
+    (1, 225, 64, 1, 16, None, 8),     # 8 chunks that compose their own start, the last of one token
+    (1, 225, 64, 1, 4, None, 8),
+    (2, 400, 50, 50, 16, None, 10),
+    (1, 0, 64, 1, 16, [97, 1, 127], 10),
+    (1, 500, 64, 1, 16, None, 16),    # chunks composed by a launch of their own
+    (1, 225, 64, 1, 64, None, 8),
+])
+def test_states_in_place(B, T, C, G, S, lens, slots):
+    """h0 and ht in one buffer: the same bits as in two."""
+    p = make(B, T, C, G, S, "f32", lens=lens, seed=B + T + S)
+    assert slots_of(desc_of(p)) == slots
+    y2, ht2 = run_in_place(p, torch.empty_like(p["h0"], device="cuda"))
+    y1, ht1 = run_in_place(p)
+    assert torch.equal(y1, y2) and torch.equal(ht1, ht2)
+    y_ref, ht_ref = oracle_fwd(p)
+    check("y", y1, y_ref, TOL_F32)
+    check("ht", ht1, ht_ref, TOL_F32)

@@ -227,6 +227,8 @@ gdn_status check_norm(const gdn_norm_desc* d, gdn::NormProblem* p) {
     return GDN_ERR_INVALID_ARG;
   if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
   if (d->activation != GDN_ACT_NONE && d->activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
+  // the kernels step over positions in 32 bits, by less than 2^20 at a time
+  if (d->positions > (1 << 30)) return GDN_ERR_UNSUPPORTED;
   // a workgroup of 1024 threads for each (sample, group), except for rows whose groups fit the
   // lanes' registers at any alignment
   const bool rows = d->positions == 1 && d->channels / d->groups <= 1024;

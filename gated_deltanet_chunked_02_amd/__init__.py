@@ -59,6 +59,12 @@ class GdnError(RuntimeError):
                                         gdn_status_string(status) if _lib else "?"))
 
 
+def _fits(*sizes):
+    """Refuses sizes that the descriptors' 32-bit fields cannot hold (ctypes would wrap them)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise GdnError(2, "a size of %d" % max(sizes))
+
+
 class GdnDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("H", ctypes.c_int32), ("Hg", ctypes.c_int32), ("Dk", ctypes.c_int32),
@@ -276,6 +282,7 @@ def make_desc(q, v, beta, cu_seqlens=None, chunk_size=128, variant="auto", stop_
     H, Dv = v.shape[2], v.shape[3]
     if N is None:
         N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _fits(B, T, N, H, Hg, Dk, Dv)
     return GdnDesc(B=B, T=T, N=N, H=H, Hg=Hg, Dk=Dk, Dv=Dv, chunk=chunk_size,
                    qkv_dtype=_dtype_code(q), beta_dtype=_dtype_code(beta),
                    variant=VARIANTS[variant] if isinstance(variant, str) else int(variant),
@@ -574,9 +581,10 @@ def causal_conv1d(x, weight, bias=None, conv_state=None, cache_indices=None,
     i32 = lambda t: None if t is None else t.to(torch.int32).contiguous()
     cu, idx, init = i32(cu_seqlens), i32(cache_indices), i32(has_initial_state)
     N = B if cu is None else cu.numel() - 1
+    lines = 0 if conv_state is None else conv_state.shape[0]
+    _fits(B, T, N, C, lines)
     desc = GdnConvDesc(B=B, T=T, N=N, channels=C, width=weight.shape[1], dtype=_dtype_code(x),
-                       activation=ACTIVATIONS[activation],
-                       state_lines=0 if conv_state is None else conv_state.shape[0])
+                       activation=ACTIVATIONS[activation], state_lines=lines)
     y = torch.empty_like(x)
     st = gdn_causal_conv1d_fwd(desc, x, weight, bias, conv_state, idx, init, cu, y)
     if st != 0:

@@ -22,7 +22,7 @@ import torch
 from torch import Tensor
 
 from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _current_stream,
-               _need, _validate_conv, load)
+               _fits, _need, _validate_conv, load)
 
 _CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -231,6 +231,7 @@ def _operands(x, dt, A, B, C, D, z, dt_bias, lead):
     G = rows[lead]
     if G == 0 or ch % G:
         raise ValueError("the channels (%d) must be a multiple of the groups (%d)" % (ch, G))
+    _fits(*rows, *shape)
     D, dt_bias = _f32("D", D, (ch,)), _f32("dt_bias", dt_bias, (ch,))
     x, sx = _rows(x, lead)
     dt, sdt = _rows(dt, lead)
@@ -254,6 +255,7 @@ def _sequences(x, cu_seqlens):
     _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1, ValueError,
           "cu_seqlens must be 1-D [N + 1]")
     _need(x.shape[0] == 1, ValueError, "a packed batch (cu_seqlens) needs B == 1")
+    _fits(cu_seqlens.numel())
     return cu_seqlens.to(torch.int32).contiguous(), cu_seqlens.numel() - 1
 
 
@@ -356,6 +358,7 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
                                                                         out_indices, n)
     _need(read is not None or state.shape[0] >= n, ValueError,
           "state has fewer lines (%d) than there are sequences (%d)" % (state.shape[0], n))
+    _fits(state.shape[0])
     dev = x.device
     _on(dev, state=state, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
         cache_indices=read, out_indices=write)
@@ -400,6 +403,7 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
     B, T, C = x.shape
     W = weight.shape[1]
     cu, N = _sequences(x, cu_seqlens)
+    _fits(B, T, N, C)
     _need(dy is not None, TypeError, "dy is required")
     _like("dy", dy, x)
     lines = dict(initial_state=initial_state, dfinal_state=dfinal_state)
@@ -471,13 +475,14 @@ def _norm_operands(x, num_groups, weight, bias, eps, activation, gate):
         raise ValueError("num_groups must divide the %d channels, got %r" % (C, num_groups))
     if not eps >= 0:
         raise ValueError("eps must not be negative")
+    positions = 1
+    for n in shape[1:-1]:
+        positions *= n
+    _fits(shape[0], positions, C)
     weight, bias = _f32("weight", weight, (C,)), _f32("bias", bias, (C,))
     _like("gate", gate, x)
     if gate is not None:
         gate = gate.contiguous()
-    positions = 1
-    for n in shape[1:-1]:
-        positions *= n
     desc = GdnNormDesc(shape[0], positions, C, num_groups, code, ACTIVATIONS[activation], eps, None,
                        0)
     return desc, x.contiguous(), weight, bias, gate

@@ -204,6 +204,17 @@ def _current_stream(device=None):
     return raw(torch.cuda.current_device() if device is None else device.index)
 
 
+def _launch(device, call, *args):
+    """call(*args, stream) on the current stream of the tensors' device, that device made the current
+    one around it: the library launches on the current device, and a device's default stream does not
+    say which it belongs to."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return call(*args, _current_stream(device))
+    with torch.cuda.device(device):
+        return call(*args, _current_stream(device))
+
+
 def gdn_chunk_fwd(desc: GdnDesc, q, k, v, g, beta, h0, cu_seqlens, scale, o, ht,
                   stream=None) -> int:
     """Raw call: tensors (or integer device addresses / None) are passed as pointers.
@@ -431,7 +442,8 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
             workspace = torch.empty(ws_bytes, device=q.device, dtype=torch.uint8)
         desc.workspace = workspace.data_ptr()
         desc.workspace_bytes = workspace.numel()
-    st = gdn_chunk_fwd(desc, q, k, v, g, beta, initial_state, cu_seqlens, scale, o, ht)
+    st = _launch(q.device, gdn_chunk_fwd, desc, q, k, v, g, beta, initial_state, cu_seqlens, scale,
+                 o, ht)
     if st != 0:
         raise GdnError(st, "gdn_chunk_fwd")
     return o, ht
@@ -492,8 +504,8 @@ def chunk_gated_delta_rule_bwd(q, k, v, g, beta, do, dht=None, scale=None,
         workspace = torch.empty(max(ws_bytes, 1), device=q.device, dtype=torch.uint8)
     desc.workspace = workspace.data_ptr()
     desc.workspace_bytes = workspace.numel()
-    st = gdn_chunk_bwd(desc, q, k, v, g, beta, initial_state, cu_seqlens, scale, do, dht, dq,
-                       dk, dv, dg, dbeta, dh0)
+    st = _launch(q.device, gdn_chunk_bwd, desc, q, k, v, g, beta, initial_state, cu_seqlens, scale,
+                 do, dht, dq, dk, dv, dg, dbeta, dh0)
     if st != 0:
         raise GdnError(st, "gdn_chunk_bwd")
     return dq, dk, dv, dg, dbeta, dh0
@@ -546,8 +558,8 @@ def fused_sigmoid_gating_delta_rule(q, k, v, a, b, A_log, dt_bias=None, scale=No
     elif output_final_state:
         ht = torch.empty((desc.N, desc.H, desc.Dk, desc.Dv), device=q.device,
                          dtype=torch.float32)
-    st = gdn_fused_sigmoid_gating_delta_rule(desc, q, k, v, a, b, A_log, dt_bias,
-                                             initial_state, cu_seqlens, scale, o, ht)
+    st = _launch(q.device, gdn_fused_sigmoid_gating_delta_rule, desc, q, k, v, a, b, A_log, dt_bias,
+                 initial_state, cu_seqlens, scale, o, ht)
     if st != 0:
         raise GdnError(st, "gdn_fused_sigmoid_gating_delta_rule")
     return o, ht
@@ -586,7 +598,7 @@ def causal_conv1d(x, weight, bias=None, conv_state=None, cache_indices=None,
     desc = GdnConvDesc(B=B, T=T, N=N, channels=C, width=weight.shape[1], dtype=_dtype_code(x),
                        activation=ACTIVATIONS[activation], state_lines=lines)
     y = torch.empty_like(x)
-    st = gdn_causal_conv1d_fwd(desc, x, weight, bias, conv_state, idx, init, cu, y)
+    st = _launch(x.device, gdn_causal_conv1d_fwd, desc, x, weight, bias, conv_state, idx, init, cu, y)
     if st != 0:
         raise GdnError(st, "gdn_causal_conv1d_fwd")
     return y

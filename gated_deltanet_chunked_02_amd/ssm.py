@@ -22,7 +22,7 @@ import torch
 from torch import Tensor
 
 from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _current_stream,
-               _fits, _need, _validate_conv, load)
+               _fits, _launch, _need, _validate_conv, load)
 
 _CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -298,8 +298,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
     if x.shape[0] == 0:
         return y, ht
     ws = _workspace(desc, gdn_selective_scan_workspace_size(desc), workspace, dev)  # noqa: F841
-    st = gdn_selective_scan_fwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, y, ht,
-                                _current_stream(dev))
+    st = _launch(dev, gdn_selective_scan_fwd, desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, y, ht)
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_fwd")
     return y, ht
@@ -327,8 +326,8 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_soft
         return dx, ddt, dA.zero_(), dB, dC, _zero(dD), dz, _zero(dbias), dh0
     need = gdn_selective_scan_bwd_workspace_size(desc)
     ws = _workspace(desc, need, workspace, dev)  # noqa: F841
-    st = gdn_selective_scan_bwd(desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, dy, dht, dx, ddt, dA,
-                                dB, dC, dD, dz, dbias, dh0, _current_stream(dev))
+    st = _launch(dev, gdn_selective_scan_bwd, desc, x, dt, A, B, C, D, z, dt_bias, h0, cu, dy, dht,
+                 dx, ddt, dA, dB, dC, dD, dz, dbias, dh0)
     if st != 0:
         raise GdnError(st, "gdn_selective_scan_bwd")
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
@@ -367,8 +366,8 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
         return y
     desc.B, desc.T, desc.N, desc.dt_softplus = n, 1, n, int(bool(dt_softplus))
     desc.state_lines = state.shape[0]
-    st = gdn_selective_state_update(desc, state, x, dt, A, B, C, D, z, dt_bias, read, write, y,
-                                    _current_stream(dev))
+    st = _launch(dev, gdn_selective_state_update, desc, state, x, dt, A, B, C, D, z, dt_bias, read,
+                 write, y)
     if st != 0:
         raise GdnError(st, "gdn_selective_state_update")
     return y
@@ -428,9 +427,9 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
     ws = _workspace(desc, 0, workspace, dev)
     if need and (ws is None or ws.numel() < need):
         ws = torch.empty(need, device=dev, dtype=torch.uint8)
-    st = gdn_causal_conv1d_bwd(desc, x, weight, bias, first, cu, dy, lines["dfinal_state"], dx,
-                               dweight, dbias, dinit, ws, 0 if ws is None else ws.numel(),
-                               _current_stream(dev))
+    st = _launch(dev, gdn_causal_conv1d_bwd, desc, x, weight, bias, first, cu, dy,
+                 lines["dfinal_state"], dx, dweight, dbias, dinit, ws,
+                 0 if ws is None else ws.numel())
     if st != 0:
         raise GdnError(st, "gdn_causal_conv1d_bwd")
     return dx, dweight, dbias, dinit
@@ -505,7 +504,7 @@ def group_norm(x, num_groups, weight=None, bias=None, eps=1e-5, activation=None,
     mean = x.new_empty((x.shape[0], num_groups), dtype=torch.float32)
     rstd = _new(mean)
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc), workspace, dev)  # noqa: F841
-    st = gdn_group_norm_fwd(desc, x, weight, bias, gate, y, mean, rstd, _current_stream(dev))
+    st = _launch(dev, gdn_group_norm_fwd, desc, x, weight, bias, gate, y, mean, rstd)
     if st != 0:
         raise GdnError(st, "gdn_group_norm_fwd")
     return y, mean, rstd
@@ -529,8 +528,8 @@ def group_norm_bwd(dy, x, num_groups, mean, rstd, weight=None, bias=None, activa
     dy = dy.contiguous()
     dx, dweight, dbias, dgate = map(_new, (x, weight, bias, gate))
     ws = _workspace(desc, gdn_group_norm_workspace_size(desc, True), workspace, dev)  # noqa: F841
-    st = gdn_group_norm_bwd(desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight, dbias,
-                            dgate, _current_stream(dev))
+    st = _launch(dev, gdn_group_norm_bwd, desc, x, weight, bias, gate, mean, rstd, dy, dx, dweight,
+                 dbias, dgate)
     if st != 0:
         raise GdnError(st, "gdn_group_norm_bwd")
     return dx, dweight, dbias, dgate

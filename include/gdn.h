@@ -32,7 +32,8 @@
  * workspace.  The library keeps no pointer after a call returns, allocates nothing, and
  * has no mutable global state; calls are reentrant.  All work is enqueued on `stream`
  * (NULL = the default stream) and nothing is synchronised: errors found on the host are
- * returned before any launch; a launch failure returns GDN_ERR_HIP.  cu_seqlens is read
+ * returned before any launch; a launch failure returns GDN_ERR_HIP.  The buffers' device is the
+ * calling thread's current one (work on its default stream goes there).  cu_seqlens is read
  * only on the device: values outside [0, B*T] are clamped (a sequence never reads or
  * writes outside the token range), but non-monotone values give unspecified results.
  *

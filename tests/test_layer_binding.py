@@ -84,3 +84,31 @@ def test_sizes_past_32_bits_are_refused(recorder, call):
     with pytest.raises(gdn.GdnError) as e:
         call()
     assert e.value.status == 2 and not recorder.calls
+
+
+def _gdn_args(T=2, D=64):
+    return (meta(1, T, 1, D), meta(1, T, 1, D), meta(1, T, 1, D))
+
+
+@pytest.mark.parametrize("name,call", [
+    ("gdn_selective_scan_fwd", lambda: gdn.selective_scan(*scan_args(1, 5))),
+    ("gdn_selective_scan_bwd", lambda: gdn.selective_scan_bwd(*scan_args(1, 5), meta(1, 5, 8))),
+    ("gdn_selective_state_update", lambda: gdn.selective_state_update(*step_args(2, 3))),
+    ("gdn_causal_conv1d_fwd", lambda: gdn.causal_conv1d(meta(1, 5, 8), meta(8, 4))),
+    ("gdn_causal_conv1d_bwd", lambda: gdn.causal_conv1d_bwd(meta(1, 5, 8), meta(8, 4),
+                                                            meta(1, 5, 8))),
+    ("gdn_group_norm_fwd", lambda: gdn.group_norm(meta(3, 8), 2)),
+    ("gdn_group_norm_bwd", lambda: gdn.group_norm_bwd(meta(3, 8), meta(3, 8), 2, meta(3, 2),
+                                                      meta(3, 2))),
+    ("gdn_chunk_fwd", lambda: gdn.chunk_gated_delta_rule(*_gdn_args(), meta(1, 2, 1),
+                                                         meta(1, 2, 1))),
+    ("gdn_chunk_bwd", lambda: gdn.chunk_gated_delta_rule_bwd(*_gdn_args(), meta(1, 2, 1),
+                                                             meta(1, 2, 1), meta(1, 2, 1, 64))),
+    ("gdn_fused_sigmoid_gating_delta_rule", lambda: gdn.fused_sigmoid_gating_delta_rule(
+        *_gdn_args(), meta(1, 2, 1), meta(1, 2, 1), meta(1))),
+])
+def test_launches_with_the_tensors_device_current(recorder, name, call):
+    """Device 0 is current; the tensors are on another one, whose default stream is 0 as well."""
+    call()
+    assert [(c[0], c[3]) for c in recorder.calls] == [(name, torch.device("meta"))]
+    assert recorder.device == 0

@@ -56,13 +56,22 @@ gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) 
   if ((long long)p->G * p->nblk > 65535) return GDN_ERR_UNSUPPORTED;
   p->f32 = d->dtype == GDN_F32;
   p->softplus = d->dt_softplus != 0;
-  // tokens whose rows lie within 2 GiB of the first one's, for every tensor
+  return GDN_OK;
+}
+
+// Prompts reach a chunk's rows from its first token by 31-bit offsets (the single-token form has a
+// 64-bit offset for each row): fills the tokens whose rows lie within 2 GiB of the first one's, for
+// every tensor.  Sequences longer than that are split, into chunks of no fewer than 4 * 64 tokens.
+gdn_status check_reach(bool packed, gdn::ScanProblem* p) {
+  const int longest = packed ? p->Ttot : p->T;
   int64_t row = p->C;
   for (int64_t v : {p->sx, p->sdt, p->sz})
     if (v > row) row = v;
-  const int64_t reach = (((int64_t)1 << 31) - 1) / (row * (p->f32 ? 4 : 2)) - 1;
-  if (reach < 4 * kLongestTile) return GDN_ERR_UNSUPPORTED;
-  p->reach = (int)(reach > (1 << 30) ? 1 << 30 : reach / kLongestTile * kLongestTile);
+  int64_t reach = (((int64_t)1 << 31) - 1) / (row * (p->f32 ? 4 : 2)) - 1;
+  if (reach < 1) reach = 1;  // a token's own row, whatever comes after it
+  if (reach < longest && reach < 4 * kLongestTile) return GDN_ERR_UNSUPPORTED;
+  if (reach > (1 << 30)) reach = 1 << 30;
+  p->reach = (int)(reach < longest ? reach / kLongestTile * kLongestTile : reach);
   return GDN_OK;
 }
 
@@ -264,7 +273,8 @@ extern "C" {
 size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* status) {
   gdn::ScanProblem p;
   const bool packed = looks_packed(d);
-  const gdn_status s = check_scan(d, packed, &p);
+  gdn_status s = check_scan(d, packed, &p);
+  if (s == GDN_OK) s = check_reach(packed, &p);
   if (status) *status = s;
   if (s != GDN_OK) return 0;
   plan_fwd(&p, packed);
@@ -274,8 +284,7 @@ size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* sta
   }
   size_t need = scan_layout(p).total;
   if (!packed && d->B == 1) {  // one sequence may also come as a packed batch of one
-    gdn::ScanProblem q;
-    check_scan(d, false, &q);
+    gdn::ScanProblem q = p;
     q.N = 1;
     plan_fwd(&q, true);
     const size_t alt = scan_layout(q).total;
@@ -290,7 +299,8 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
                                   const float* h0, const int32_t* cu_seqlens, void* y, float* ht,
                                   hipStream_t stream) {
   gdn::ScanProblem p;
-  const gdn_status s = check_scan(d, cu_seqlens != nullptr, &p);
+  gdn_status s = check_scan(d, cu_seqlens != nullptr, &p);
+  if (s == GDN_OK) s = check_reach(cu_seqlens != nullptr, &p);
   if (s != GDN_OK) return s;
   if (!A || (p.Ttot > 0 && (!x || !dt || !Bm || !Cm || !y))) return GDN_ERR_INVALID_ARG;
   const size_t e = p.f32 ? 4 : 2;
@@ -327,7 +337,8 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
 size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_desc* d, gdn_status* status) {
   gdn::ScanProblem p;
   const bool packed = looks_packed(d);
-  const gdn_status s = check_scan(d, packed, &p);
+  gdn_status s = check_scan(d, packed, &p);
+  if (s == GDN_OK) s = check_reach(packed, &p);
   if (status) *status = s;
   if (s != GDN_OK) return 0;
   // one dense sequence may also come as a packed batch of one, which never has fewer slots
@@ -349,7 +360,8 @@ gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const v
                                   void* dC, float* dD, void* dz, float* ddt_bias, float* dh0,
                                   hipStream_t stream) {
   gdn::ScanProblem p;
-  const gdn_status s = check_scan(d, cu_seqlens != nullptr, &p);
+  gdn_status s = check_scan(d, cu_seqlens != nullptr, &p);
+  if (s == GDN_OK) s = check_reach(cu_seqlens != nullptr, &p);
   if (s != GDN_OK) return s;
   if (!A || !dA) return GDN_ERR_INVALID_ARG;
   if (p.Ttot > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dB || !dC || (z && !dz)))

@@ -207,9 +207,10 @@ gdn_status gdn_causal_conv1d_fwd(const gdn_conv_desc* d, const void* x, const fl
  *   D, dt_bias [channels]               f32
  *   h0, ht     [N, channels, dstate]    f32; cu_seqlens [N + 1] int32 as for gdn_chunk_fwd
  * Any channels, groups dividing it, dstate 1 .. 256.  GDN_ERR_UNSUPPORTED beyond 2^30 tokens,
- * 65536 sequences, 2^20 channels, launches of 2^32 threads, or with rows so long that 256 of them
- * pass 2 GiB.  Pointers are device pointers aligned to
- * their element; errors are returned before any launch; nothing is synchronised or allocated.
+ * 65536 sequences, 2^20 channels, launches of 2^32 threads, or where the rows of a sequence (of all
+ * tokens of a packed batch) and one more, or of 257 tokens if it is longer, pass 2 GiB.  Pointers are
+ * device pointers aligned to their element; errors are returned before any launch; nothing is
+ * synchronised or allocated.
  * x, dt, A, Bm, Cm, y are required unless B*T = 0 (A always).  h0 and ht may be the same
  * buffer.  Few or long sequences are split into chunks that run in parallel, so results depend
  * on the descriptor in their last bits, never on scheduling. */
@@ -263,8 +264,8 @@ gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const v
  * in a pool: sequence b reads line cache_indices[b] (b when NULL) of state [state_lines,
  * channels, dstate] and writes line out_indices[b] (the line it read when NULL).  A line read
  * from outside the pool is a zero start, one written outside it is dropped.  A line that one
- * sequence writes and another reads or writes in the same call has unspecified contents.  No
- * workspace. */
+ * sequence writes and another reads or writes in the same call has unspecified contents.  Rows may
+ * be any number of bytes apart.  No workspace. */
 gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, const void* x,
                                       const void* dt, const float* A, const void* Bm,
                                       const void* Cm, const float* D, const void* z,

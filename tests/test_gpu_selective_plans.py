@@ -74,3 +74,43 @@ def test_states_in_place(B, T, C, G, S, lens, slots):
     y_ref, ht_ref = oracle_fwd(p)
     check("y", y1, y_ref, TOL_F32)
     check("ht", ht1, ht_ref, TOL_F32)
+
+
+def test_rows_far_apart():
+    """One token of a long batch, 8 MB from row to row, and a prompt whose rows are 256 MB apart: the
+    same bits as from rows one after another."""
+    import gated_deltanet_chunked_02_amd as gdn
+    p = make(4, 1, 4096, 1, 16, "bf16", seed=3)
+    q = dev(p)
+    wide = torch.zeros(4, 1024, 4096, dtype=torch.bfloat16, device="cuda")
+    at = wide[:, 700:701]
+    at.copy_(q["x"])
+    kw = dict(D=q["D"], z=q["z"], dt_bias=q["dt_bias"], dt_softplus=True)
+    one = lambda t: t[:, 0]  # noqa: E731
+    kw1 = dict(kw, z=one(q["z"]))
+    rest = (q["dt"], q["A"], q["B"], q["C"])
+    rest1 = tuple(t if t is q["A"] else one(t) for t in rest)
+    a, b = q["h0"].clone(), q["h0"].clone()
+    assert torch.equal(gdn.selective_state_update(a, one(at), *rest1, **kw1),
+                       gdn.selective_state_update(b, one(q["x"]), *rest1, **kw1))
+    assert torch.equal(a, b)
+    for got, want in zip(gdn.selective_scan(at, *rest, initial_state=q["h0"], **kw),
+                         gdn.selective_scan(q["x"], *rest, initial_state=q["h0"], **kw)):
+        assert torch.equal(got, want)
+    for got, want in zip(gdn.selective_scan_bwd(at, *rest, q["dy"], dht=q["dht"], **kw),
+                         gdn.selective_scan_bwd(q["x"], *rest, q["dy"], dht=q["dht"], **kw)):
+        assert got is None and want is None or torch.equal(got, want)
+    del wide
+    p = make(1, 3, 64, 1, 16, "f32", seed=4)
+    q = dev(p)
+    far = torch.zeros(1, 3, 1 << 26, device="cuda")[..., 5:69]
+    far.copy_(q["x"])
+    rest = (q["dt"], q["A"], q["B"], q["C"])
+    kw = dict(D=q["D"], z=q["z"], dt_bias=q["dt_bias"], dt_softplus=True, initial_state=q["h0"])
+    y, ht = gdn.selective_scan(far, *rest, **kw)
+    y_ref, ht_ref = oracle_fwd(p)
+    check("y", y, y_ref, TOL_F32)
+    check("ht", ht, ht_ref, TOL_F32)
+    for got, want in zip(gdn.selective_scan_bwd(far, *rest, q["dy"], **kw),
+                         gdn.selective_scan_bwd(q["x"], *rest, q["dy"], **kw)):
+        assert torch.equal(got, want)

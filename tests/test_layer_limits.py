@@ -17,3 +17,22 @@ def test_norm_positions(positions, status):
     if status:
         assert gdn.gdn_group_norm_fwd(d, *[A] * 7, 0) == status
         assert gdn.gdn_group_norm_bwd(d, *[A] * 11, 0) == status
+
+
+def test_rows_far_apart():
+    """Token t of a [4, 1024, 4096] tensor, and a prompt of one token there: 8 MB from row to row.
+    A prompt of three tokens may be 256 MB a row, not 512."""
+    far = dict(B=4, N=4, T=1, channels=4096, groups=1)
+    for strides in (dict(x_stride=1 << 22), dict(dt_stride=1 << 22, z_stride=1 << 40)):
+        d = scan_desc(**far, **strides)
+        assert gdn.gdn_selective_state_update(d, A, None, *[A] * 7, None, None, A, 0) == 1
+        for name in ("gdn_selective_scan_workspace_size", "gdn_selective_scan_bwd_workspace_size"):
+            assert size(name, d)[0] == 0
+    for log, status in ((27, 0), (28, 2)):  # bf16 elements
+        d = scan_desc(B=1, N=1, T=3, channels=64, groups=1, x_stride=1 << log)
+        for name in ("gdn_selective_scan_workspace_size", "gdn_selective_scan_bwd_workspace_size"):
+            assert size(name, d)[0] == status
+    # and of any length where 257 rows lie within 2 GiB
+    for log, status in ((21, 0), (22, 2)):
+        d = scan_desc(B=1, N=1, T=100000, channels=64, groups=1, x_stride=1 << log)
+        assert size("gdn_selective_scan_workspace_size", d)[0] == status

@@ -121,11 +121,13 @@ void plan_fwd(gdn::ScanProblem* p, bool packed) {
 }
 
 // A launch has fewer than 2^32 threads; so have the passes over B and C rows, over the chunks'
-// channel blocks and over the states.
-bool grids_ok(const gdn::ScanProblem& p) {
-  const long long most = 1LL << 32;
-  return (long long)p.Ttot * p.G * 2 * p.Sp < most - 256 &&
-         (long long)p.slots * p.G * p.nblk * 64 * p.nw < most && (long long)p.N * p.S * 256 < most;
+// channel blocks and over the states, and the gradient's sums (launch_scan_bwd), in workgroups of
+// 1024 threads.
+bool grids_ok(const gdn::ScanProblem& p, bool backward) {
+  const long long most = 1LL << 32, rows = (long long)p.Ttot * p.G * 2 * p.Sp;
+  const long long sums = backward ? (p.C + 63LL) / 64 * (p.S + 2) + (rows + 1023) / 1024 : 0;
+  return rows < most - 256 && (long long)p.slots * p.G * p.nblk * 64 * p.nw < most &&
+         (long long)p.N * p.S * 256 < most && sums * 1024 < most;
 }
 
 struct ScanLayout {
@@ -278,7 +280,7 @@ size_t gdn_selective_scan_workspace_size(const gdn_scan_desc* d, gdn_status* sta
   if (status) *status = s;
   if (s != GDN_OK) return 0;
   plan_fwd(&p, packed);
-  if (!grids_ok(p)) {
+  if (!grids_ok(p, false)) {
     if (status) *status = GDN_ERR_UNSUPPORTED;
     return 0;
   }
@@ -310,7 +312,7 @@ gdn_status gdn_selective_scan_fwd(const gdn_scan_desc* d, const void* x, const v
     return GDN_ERR_INVALID_ARG;
   if (p.N == 0) return GDN_OK;
   plan_fwd(&p, cu_seqlens != nullptr);
-  if (!grids_ok(p)) return GDN_ERR_UNSUPPORTED;
+  if (!grids_ok(p, false)) return GDN_ERR_UNSUPPORTED;
   const ScanLayout L = scan_layout(p);
   if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
                       !aligned(d->workspace, kAlign)))
@@ -345,7 +347,7 @@ size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_desc* d, gdn_status*
   const bool one = !packed && d->B == 1;
   if (one) p.N = 1;
   plan_bwd(&p, packed || one);
-  if (!grids_ok(p)) {
+  if (!grids_ok(p, true)) {
     if (status) *status = GDN_ERR_UNSUPPORTED;
     return 0;
   }
@@ -375,7 +377,7 @@ gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const v
                         (const void*)dD, (const void*)ddt_bias, (const void*)dh0})
     if (!aligned(q, 4)) return GDN_ERR_INVALID_ARG;
   plan_bwd(&p, cu_seqlens != nullptr);
-  if (!grids_ok(p)) return GDN_ERR_UNSUPPORTED;
+  if (!grids_ok(p, true)) return GDN_ERR_UNSUPPORTED;
   const BwdLayout L = bwd_layout(p);
   if (L.total > 0 && (!d->workspace || d->workspace_bytes < L.total ||
                       !aligned(d->workspace, kAlign)))

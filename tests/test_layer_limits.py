@@ -36,3 +36,20 @@ def test_rows_far_apart():
     for log, status in ((21, 0), (22, 2)):
         d = scan_desc(B=1, N=1, T=100000, channels=64, groups=1, x_stride=1 << log)
         assert size("gdn_selective_scan_workspace_size", d)[0] == status
+
+
+@pytest.mark.parametrize("kw,forward,backward", [
+    # 16384 x 258 workgroups of 1024 threads for the sums of dA, dD and d(dt_bias)
+    (dict(B=1, N=1, T=4, channels=1 << 20, groups=1, dstate=256), 0, 2),
+    (dict(B=1, N=1, T=4, channels=1 << 20, groups=1, dstate=240), 0, 0),
+    # 2^32 - 2^22 values of B and C, and the channels' 2 x 18 workgroups with them
+    (dict(B=1, N=1, T=(1 << 27) - (1 << 17), channels=128, groups=1, dstate=16), 0, 0),
+    (dict(B=1, N=1, T=(1 << 27) - 32, channels=128, groups=1, dstate=16), 0, 2),
+])
+def test_gradient_sums_fit_a_launch(kw, forward, backward):
+    d = scan_desc(**kw)
+    assert size("gdn_selective_scan_workspace_size", d)[0] == forward
+    assert size("gdn_selective_scan_bwd_workspace_size", d)[0] == backward
+    if backward:
+        d.workspace, d.workspace_bytes = A, 1 << 62
+        assert gdn.gdn_selective_scan_bwd(d, *[A] * 9, None, *[A] * 11, 0) == backward

@@ -53,7 +53,6 @@ gdn_status check_scan(const gdn_scan_desc* d, bool packed, gdn::ScanProblem* p) 
   p->S = d->dstate;
   p->per = p->C / p->G;
   p->nblk = (p->per + gdn::kScanLanes - 1) / gdn::kScanLanes;
-  if ((long long)p->G * p->nblk > 65535) return GDN_ERR_UNSUPPORTED;
   p->f32 = d->dtype == GDN_F32;
   p->softplus = d->dt_softplus != 0;
   return GDN_OK;

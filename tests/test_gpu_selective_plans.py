@@ -114,3 +114,23 @@ def test_rows_far_apart():
     for got, want in zip(gdn.selective_scan_bwd(far, *rest, q["dy"], **kw),
                          gdn.selective_scan_bwd(q["x"], *rest, q["dy"], **kw)):
         assert torch.equal(got, want)
+
+
+def test_many_groups():
+    """A group for each of 70000 channels: more blocks of channels than 16 bits count."""
+    import gated_deltanet_chunked_02_amd as gdn
+    from test_gpu_selective_bwd import check_all, oracle_bwd, run_bwd
+    p = make(2, 5, 70000, 70000, 1, "f32", seed=8)
+    y_ref, ht_ref = oracle_fwd(p)
+    y, ht = run_fwd(p)
+    check("y", y, y_ref, TOL_F32)
+    check("ht", ht, ht_ref, TOL_F32)
+    check_all(p, run_bwd(p), oracle_bwd(p), "f32")
+    p = make(2, 1, 70000, 70000, 1, "f32", seed=9)
+    q = dev(p)
+    one = [q[k] if k == "A" else q[k][:, 0] for k in ("x", "dt", "A", "B", "C")]
+    y = gdn.selective_state_update(q["h0"], *one, D=q["D"], z=q["z"][:, 0], dt_bias=q["dt_bias"],
+                                   dt_softplus=True)
+    y_ref, ht_ref = oracle_fwd(p)
+    check("y", y, y_ref[:, 0], TOL_F32)
+    check("state", q["h0"], ht_ref, TOL_F32)

@@ -53,3 +53,12 @@ def test_gradient_sums_fit_a_launch(kw, forward, backward):
     if backward:
         d.workspace, d.workspace_bytes = A, 1 << 62
         assert gdn.gdn_selective_scan_bwd(d, *[A] * 9, None, *[A] * 11, 0) == backward
+
+
+def test_any_number_of_groups():
+    """65536 and more blocks of channels, as one channel a group makes of 70000."""
+    d = scan_desc(B=2, N=2, T=5, channels=70000, groups=70000, dstate=1)
+    for name in ("gdn_selective_scan_workspace_size", "gdn_selective_scan_bwd_workspace_size"):
+        assert size(name, d)[0] == 0
+    d.T = 1
+    assert gdn.gdn_selective_state_update(d, A, None, *[A] * 7, None, None, A, 0) == 1

@@ -217,6 +217,8 @@ gdn_status check_conv_bwd(const gdn_conv_desc* d, bool packed, gdn::ConvBwdProbl
   const long long Ttot = (long long)d->B * d->T;
   if (Ttot > (1LL << 30) || (long long)d->channels * 8 > (1LL << 30) || d->N > (1 << 24))
     return GDN_ERR_UNSUPPORTED;
+  // the grid's y axis counts blocks of 1024 channels, in 16 bits
+  if ((d->channels + 1023LL) / 1024 > 65535) return GDN_ERR_UNSUPPORTED;
   memset(p, 0, sizeof(*p));
   p->T = d->T;
   p->Ttot = (int)Ttot;

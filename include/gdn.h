@@ -280,7 +280,7 @@ gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, cons
  *   dweight  [C, W], dbias [C]   f32 sums over all tokens (NULL: not written)
  *   dinitial [N, W - 1, C]  dtype, the gradient of initial (NULL: not written)
  * d->state_lines is ignored; shapes, checks and the rest as for the forward (x, dy, dx, initial,
- * dfinal and dinitial 16-byte aligned).  Sums are made in a fixed order.  The workspace (256-byte
+ * dfinal and dinitial 16-byte aligned; at most 65535 * 1024 channels).  Sums are made in a fixed order.  The workspace (256-byte
  * aligned, gdn_causal_conv1d_bwd_workspace_size bytes) is required when B*T > 0. */
 size_t gdn_causal_conv1d_bwd_workspace_size(const gdn_conv_desc* d, gdn_status* status);
 

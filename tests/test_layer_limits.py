@@ -62,3 +62,12 @@ def test_any_number_of_groups():
         assert size(name, d)[0] == 0
     d.T = 1
     assert gdn.gdn_selective_state_update(d, A, None, *[A] * 7, None, None, A, 0) == 1
+
+
+@pytest.mark.parametrize("channels,status", [(65535 * 1024, 0), (65535 * 1024 + 8, 2), (1 << 27, 2)])
+def test_conv_gradient_channels(channels, status):
+    """Blocks of 1024 channels are a grid's y axis."""
+    d = conv_desc(B=1, N=1, T=1, channels=channels)
+    assert size("gdn_causal_conv1d_bwd_workspace_size", d)[0] == status
+    if status:
+        assert gdn.gdn_causal_conv1d_bwd(d, *[A] * 4, None, *[A] * 7, 1 << 62, 0) == status

@@ -524,12 +524,17 @@ gdn_status gdn_group_norm_fwd(const gdn_norm_desc* d, const void* x, const float
   gdn::NormProblem p;
   gdn_status s = check_norm(d, &p);
   if (s != GDN_OK) return s;
-  if (p.N == 0 || p.P == 0) return GDN_OK;
-  if (!x || !y) return GDN_ERR_INVALID_ARG;
+  if (p.N == 0) return GDN_OK;
+  if (p.P > 0 && (!x || !y)) return GDN_ERR_INVALID_ARG;
   const size_t e = p.f32 ? 4 : 2;
   if (!aligned(x, e) || !aligned(gate, e) || !aligned(y, e) || !aligned(weight, 4) ||
       !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
     return GDN_ERR_INVALID_ARG;
+  if (p.P == 0) {
+    p.mean = mean;
+    p.rstd = rstd;
+    return gdn::launch_norm_no_stats(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+  }
   s = norm_space(d, false, &p);
   if (s != GDN_OK) return s;
   p.x = x;

@@ -647,6 +647,14 @@ __global__ __launch_bounds__(kThreads) void k_norm_group(NormProblem p) {
   }
 }
 
+// The mean and deviation of no values.
+__global__ __launch_bounds__(kThreads) void k_norm_no_stats(float* mean, float* rstd, int n) {
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  if (mean) mean[i] = __builtin_nanf("");
+  if (rstd) rstd[i] = __builtin_nanf("");
+}
+
 // --- plans ------------------------------------------------------------------------------------
 
 bool all_aligned(const NormProblem& p, size_t bytes) {
@@ -804,6 +812,13 @@ size_t norm_workspace(const NormProblem& p, bool backward) {
 
 hipError_t launch_norm_fwd(const NormProblem& p, hipStream_t st) {
   return p.f32 ? launch_e<false, float>(p, st) : launch_e<false, bf16>(p, st);
+}
+
+hipError_t launch_norm_no_stats(const NormProblem& p, hipStream_t st) {
+  if (!p.mean && !p.rstd) return hipSuccess;
+  const int n = p.N * p.G;  // at most 2^21 where the positions are not 1
+  k_norm_no_stats<<<(n + kThreads - 1) / kThreads, kThreads, 0, st>>>(p.mean, p.rstd, n);
+  return hipGetLastError();
 }
 
 hipError_t launch_norm_no_params(const NormProblem& p, hipStream_t st) {

@@ -31,6 +31,8 @@ struct NormProblem {
 size_t norm_workspace(const NormProblem& p, bool backward);
 hipError_t launch_norm_fwd(const NormProblem& p, hipStream_t st);
 hipError_t launch_norm_bwd(const NormProblem& p, hipStream_t st);
+// The statistics of no positions: NaN.
+hipError_t launch_norm_no_stats(const NormProblem& p, hipStream_t st);
 // The parameters' gradients of no data: zeros.
 hipError_t launch_norm_no_params(const NormProblem& p, hipStream_t st);
 

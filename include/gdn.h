@@ -299,10 +299,10 @@ gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const fl
  *
  * x, gate, y [samples, positions, channels] dtype (bf16 or f32), contiguous; weight, bias
  * [channels] f32 or NULL (ones, zeros); mean, rstd [samples, groups] f32, written unless NULL (the
- * backward needs them).  Statistics are fp32 sums about the mean.  Any channels, groups dividing
- * it, up to 2^20 (GDN_ERR_UNSUPPORTED beyond, beyond 2^30 positions, and beyond 2^21 (sample, group)
- * pairs unless positions is 1 and a group has at most 1024 channels); pointers aligned to their
- * element (vectors are used where 16 bytes fit). */
+ * backward needs them; NaN where there are no positions).  Statistics are fp32 sums about the mean.
+ * Any channels, groups dividing it, up to 2^20 (GDN_ERR_UNSUPPORTED beyond, beyond 2^30 positions,
+ * and beyond 2^21 (sample, group) pairs unless positions is 1 and a group has at most 1024
+ * channels); pointers aligned to their element (vectors are used where 16 bytes fit). */
 typedef struct gdn_norm_desc {
   int32_t samples, positions, channels, groups;
   int32_t dtype;       /* gdn_dtype of x, gate, y, dy, dx, dgate */

@@ -183,6 +183,8 @@ def _indices(name, t, n):
         raise TypeError("%s must be an int32 or int64 tensor" % name)
     if t.shape != (n,):
         raise ValueError("%s must be [%d]" % (name, n))
+    if t.dtype == torch.int64:
+        t = t.clamp(-1, 0x7FFFFFFF)  # outside the pool either way, where a cast would wrap into it
     return t.to(torch.int32).contiguous()
 
 

@@ -112,3 +112,12 @@ def test_launches_with_the_tensors_device_current(recorder, name, call):
     call()
     assert [(c[0], c[3]) for c in recorder.calls] == [(name, torch.device("meta"))]
     assert recorder.device == 0
+
+
+def test_64_bit_lines_outside_the_pool_stay_outside():
+    from gated_deltanet_chunked_02_amd.ssm import _indices
+    given = torch.tensor([0, 5, -1, -7, 2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 32, 2 ** 31 - 1])
+    got = _indices("cache_indices", given, 9)
+    assert got.dtype == torch.int32 and got[:2].tolist() == [0, 5]
+    assert all(i < 0 or i == 2 ** 31 - 1 for i in got[2:].tolist())
+    assert _indices("cache_indices", got, 9) is got

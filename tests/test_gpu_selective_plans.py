@@ -76,6 +76,52 @@ def test_states_in_place(B, T, C, G, S, lens, slots):
     check("ht", ht1, ht_ref, TOL_F32)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,C,G,S,h0,slots", [
+    # a dense sequence whose chunks compose their own start states: 2 to 8 of them
+    (1, 225, 64, 1, 16, True, 8), (1, 256, 64, 1, 16, True, 9), (1, 256, 64, 1, 16, False, 9),
+    (1, 225, 64, 1, 4, True, 8), (1, 250, 70, 2, 3, False, 8),
+    (1, 225, 64, 1, 8, True, 8), (1, 193, 130, 1, 7, True, 7),
+    (2, 225, 64, 1, 16, True, 16), (2, 256, 100, 1, 8, True, 16), (2, 400, 50, 50, 16, False, 10),
+    (1, 600, 80, 80, 16, True, 6), (2, 300, 80, 80, 16, True, 6), (1, 400, 170, 170, 9, True, 3),
+    (2, 200, 200, 200, 2, True, 6),
+    # composed by a launch of their own: many chunks, or more states than 16
+    (1, 300, 64, 1, 4, True, 10), (1, 300, 65, 1, 8, False, 10), (1, 577, 64, 1, 16, True, 19),
+    (1, 225, 64, 1, 17, True, 8), (1, 300, 64, 1, 32, True, 10), (2, 225, 70, 1, 32, False, 16),
+    (1, 225, 64, 1, 65, True, 8), (1, 300, 64, 1, 128, True, 10), (2, 193, 40, 2, 128, False, 14),
+    (1, 225, 64, 1, 129, True, 8), (1, 300, 64, 1, 256, False, 10), (2, 225, 30, 1, 256, True, 16),
+])
+def test_dense_chunks(B, T, C, G, S, h0, slots, dtype):
+    p = make(B, T, C, G, S, dtype, h0=h0, seed=B + T + C + S)
+    assert slots_of(desc_of(p)) == slots
+    y_ref, ht_ref = oracle_fwd(p)
+    y, ht = run_fwd(p)
+    check("y", y, y_ref, TOL[dtype])
+    check("ht", ht, ht_ref, TOL_F32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [4, 8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("lens,slots", [([97, 1, 0, 127], 11),        # at most 8 chunks by length
+                                        ([3, 290, 0, 129, 1, 63], 21)])
+def test_packed_chunks(lens, slots, S, dtype):
+    p = make(C=72, G=2, S=S, dtype=dtype, lens=lens, seed=S)
+    assert slots_of(desc_of(p)) == slots
+    y_ref, ht_ref = oracle_fwd(p)
+    y, ht = run_fwd(p)
+    check("y", y, y_ref, TOL[dtype])
+    check("ht", ht, ht_ref, TOL_F32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [1, 4, 8, 32, 33, 256])
+def test_packed_gradients(S, dtype):
+    """Every number of waves, and one state block (up to 32 states) or several."""
+    from test_gpu_selective_bwd import check_all, oracle_bwd, run_bwd
+    p = make(C=72, G=2, S=S, dtype=dtype, lens=[3, 200, 0, 129, 1, 63], seed=S)
+    check_all(p, run_bwd(p), oracle_bwd(p), dtype)
+
+
 def test_rows_far_apart():
     """One token of a long batch, 8 MB from row to row, and a prompt whose rows are 256 MB apart: the
     same bits as from rows one after another."""

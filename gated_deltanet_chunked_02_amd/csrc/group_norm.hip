@@ -17,8 +17,8 @@
 //   * maps (P > 1).  A group's channels are a short piece of every position's row, so a
 //     workgroup takes whole rows: a thread keeps to VEC channels and goes over positions with a
 //     running mean and sum of squares about it for each (joined exactly, never as a difference
-//     of large sums); a small kernel joins the pieces of each (sample, group); a last pass
-//     applies them.
+//     of large sums); a small kernel joins the pieces of each (sample, group), many pieces after
+//     another has folded them; a last pass applies them.
 //   * a workgroup for each (sample, group), for maps so small that three launches would cost
 //     more than reading them in short pieces.
 // Statistics and sums are fp32; every output is rounded once; sums have a fixed order.
@@ -392,17 +392,43 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
   return seg_sum(v, kThreads, lds);
 }
 
-// mean and rstd of each (sample, group) from the channels' pieces: to p.mean and p.rstd.
-__global__ __launch_bounds__(kThreads) void k_norm_join(NormProblem p, MapPlan q, float* mean,
-                                                        float* rstd) {
+// Positions that a sample's slab takes.
+__device__ __forceinline__ float slab_count(const NormProblem& p, const MapPlan& q, int slab) {
+  const int all = q.slabs * q.ty, rest = p.P % all - slab * q.ty;
+  return (float)(p.P / all * q.ty + min(max(rest, 0), q.ty));
+}
+
+// Every channel's statistics over a sample's slabs, in place of the first slab's: a workgroup takes
+// 64 channels, its 16 waves every 16th slab each, and nothing else touches those columns.
+__global__ __launch_bounds__(kColumnThreads) void k_norm_fold(NormProblem p, MapPlan q) {
+  constexpr int WAVES = kColumnThreads / 64;
+  __shared__ Stat lds[WAVES][64];
+  const int cols = (p.C + 63) / 64;
+  const int n = blockIdx.x / cols, c = (blockIdx.x - n * cols) * 64 + lane_id();
+  float* ws = p.ws + (long)n * q.slabs * 2 * p.C + c;
+  Stat s{0.f, 0.f, 0.f};
+  if (c < p.C)
+    for (int slab = wave_id(); slab < q.slabs; slab += WAVES) {
+      const float* o = ws + (long)slab * 2 * p.C;
+      s = join(s, Stat{slab_count(p, q, slab), o[0], o[p.C]});
+    }
+  lds[wave_id()][lane_id()] = s;
+  __syncthreads();
+  if (threadIdx.x >= 64 || c >= p.C) return;
+  for (int k = 1; k < WAVES; ++k) s = join(s, lds[k][lane_id()]);
+  ws[0] = s.mean;
+  ws[p.C] = s.m2;
+}
+
+// mean and rstd of each (sample, group) from the channels' pieces, one for each of the slabs or one
+// in all (folded): to p.mean and p.rstd.
+__global__ __launch_bounds__(kThreads) void k_norm_join(NormProblem p, MapPlan q, bool folded,
+                                                        float* mean, float* rstd) {
   __shared__ float lds[4];
   const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
   const float* ws = p.ws + (long)n * q.slabs * 2 * p.C + (long)g * p.cpg;
-  const int items = q.slabs * p.cpg;
-  auto count = [&](int slab) {  // positions of a slab
-    const int all = q.slabs * q.ty, rest = p.P % all - slab * q.ty;
-    return (float)(p.P / all * q.ty + min(max(rest, 0), q.ty));
-  };
+  const int items = (folded ? 1 : q.slabs) * p.cpg;
+  auto count = [&](int slab) { return folded ? (float)p.P : slab_count(p, q, slab); };
   float s = 0.f;
   for (int i = threadIdx.x; i < items; i += kThreads) {
     const int slab = i / p.cpg, c = i - slab * p.cpg;
@@ -514,10 +540,21 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd_sums(NormProblem p, MapPl
   }
 }
 
+// The sums over a sample's slabs in place of the first slab's, as k_norm_fold: 64 columns of a plane
+// to a workgroup.
+__global__ __launch_bounds__(kColumnThreads) void k_norm_bwd_fold(NormProblem p, MapPlan q) {
+  const int cols = (p.C + 63) / 64;
+  const int row = blockIdx.x / cols, c = (blockIdx.x - row * cols) * 64 + lane_id();
+  float* ws = p.ws + ((long)(row >> 1) * q.slabs * 2 + (row & 1)) * p.C;
+  const float r = column_sum(ws, 2L * p.C, q.slabs, c, p.C);
+  if (threadIdx.x < 64 && c < p.C) ws[c] = r;
+}
+
 // The first N G workgroups: sum dhat / M and sum (dhat xhat) / M of each (sample, group), to sums
-// [N, G, 2]; the others: dw and db from the same partial sums, 64 channels each.
+// [N, G, 2]; the others: dw and db from the same partial sums, 64 channels each.  folded: one piece
+// a sample, else one for each of its slabs.
 __global__ __launch_bounds__(kColumnThreads) void k_norm_bwd_join(NormProblem p, MapPlan q,
-                                                                  float* sums) {
+                                                                  bool folded, float* sums) {
   const int joins = p.N * p.G;
   if ((int)blockIdx.x >= joins) {
     const int cols = (p.C + 63) / 64;
@@ -525,14 +562,16 @@ __global__ __launch_bounds__(kColumnThreads) void k_norm_bwd_join(NormProblem p,
     float* to = row == 0 ? p.dweight : p.dbias;
     if (!to) return;
     const int c = (blockIdx.x - joins - row * cols) * 64 + lane_id();
-    const float r = column_sum(p.ws + (long)row * p.C, 2L * p.C, (long)p.N * q.slabs, c, p.C);
+    const long pieces = folded ? q.slabs : 1;
+    const float r = column_sum(p.ws + (long)row * p.C, 2L * p.C * pieces,
+                               (long)p.N * q.slabs / pieces, c, p.C);
     if (threadIdx.x < 64 && c < p.C) to[c] = r;
     return;
   }
   __shared__ float lds[2][kColumnThreads / 64];
   const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
   const float* ws = p.ws + (long)n * q.slabs * 2 * p.C + (long)g * p.cpg;
-  const int items = q.slabs * p.cpg;
+  const int items = (folded ? 1 : q.slabs) * p.cpg;
   float s1 = 0.f, s2 = 0.f;
   for (int i = threadIdx.x; i < items; i += kColumnThreads) {
     const int slab = i / p.cpg, c = i - slab * p.cpg;
@@ -717,6 +756,17 @@ MapPlan map_plan(const NormProblem& p, int vec) {
   return q;
 }
 
+// A (sample, group)'s pieces, slabs times channels, are joined by one workgroup, which many of them
+// (few samples, wide groups) keep busy long after the passes; more than these are first folded over
+// the slabs by a launch of its own.  8 maps of 4096 x 512, folded and not: forward 2048 pieces 31.1
+// and 32.0 us, 4096 30.7 and 38.8, 32768 32.0 and 120; backward 8192 pieces 44.6 and 45.6, 16384 44.3
+// and 49.1.  A map of 16384 x 4096 in one group takes 121 us forward and 145 backward, 11.6 and 1.82
+// ms with its 4 million pieces joined at once.
+constexpr int kFoldItems = 2048, kBwdFoldItems = 8192;
+bool fold_slabs(const NormProblem& p, const MapPlan& q, int most) {
+  return q.slabs > 1 && (long)q.slabs * p.cpg > most;
+}
+
 // Maps so small that one launch with short reads is quicker than three: at most this many values
 // a (sample, group), or a row too wide for the lanes' registers.
 constexpr long kGroupItems = 4096;
@@ -743,7 +793,9 @@ hipError_t fwd_vec(const NormProblem& p, hipStream_t st) {
   float* mean = p.mean ? p.mean : stats;
   float* rstd = p.rstd ? p.rstd : stats + (long)p.N * p.G;
   k_norm_stats<E, VEC><<<grid, kThreads, 0, st>>>(p, q);
-  k_norm_join<<<p.N * p.G, kThreads, 0, st>>>(p, q, mean, rstd);
+  const bool fold = fold_slabs(p, q, kFoldItems);
+  if (fold) k_norm_fold<<<p.N * ((p.C + 63) / 64), kColumnThreads, 0, st>>>(p, q);
+  k_norm_join<<<p.N * p.G, kThreads, 0, st>>>(p, q, fold, mean, rstd);
   k_norm_apply<E, VEC><<<grid, kThreads, 0, st>>>(p, q, mean, rstd);
   return hipGetLastError();
 }
@@ -766,7 +818,9 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t st) {
   const dim3 grid(p.N * q.slabs, q.cblk);
   float* sums = p.ws + (long)p.N * q.slabs * 2 * p.C;
   k_norm_bwd_sums<E, VEC><<<grid, kThreads, 0, st>>>(p, q);
-  k_norm_bwd_join<<<p.N * p.G + (p.C + 63) / 64 * 2, kColumnThreads, 0, st>>>(p, q, sums);
+  const bool fold = fold_slabs(p, q, kBwdFoldItems);
+  if (fold) k_norm_bwd_fold<<<p.N * 2 * ((p.C + 63) / 64), kColumnThreads, 0, st>>>(p, q);
+  k_norm_bwd_join<<<p.N * p.G + (p.C + 63) / 64 * 2, kColumnThreads, 0, st>>>(p, q, fold, sums);
   k_norm_bwd_apply<E, VEC><<<grid, kThreads, 0, st>>>(p, q, sums);
   return hipGetLastError();
 }

@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from test_gpu_layer import test_norm_matches_oracle as norm_matches_oracle
+
 pytestmark = pytest.mark.gpu
 
 
@@ -19,3 +21,33 @@ def test_statistics_of_no_positions():
     assert dx.shape == x.shape and not dw.any()
     y, mean, _ = gdn.group_norm(torch.zeros(0, 5, 64, device="cuda"), 4)
     assert y.shape == (0, 5, 64) and mean.shape == (0, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,groups,silu,gated,affine", [
+    ((1, 1000, 512), 1, True, False, True),    # 16 slabs of a group of 512 channels
+    ((2, 3000, 520), 1, False, True, True),    # 94
+    ((1, 700, 333), 3, True, True, False),     # odd: single values
+    ((3, 900, 1024), 4, True, False, True),
+    ((1, 33, 4100), 2, True, True, True),      # wide rows, few slabs
+])
+def test_norm_of_wide_groups(shape, groups, dtype, silu, gated, affine):
+    """Groups of so many pieces that these are folded over the slabs first."""
+    norm_matches_oracle(shape, groups, dtype, silu, gated, affine)
+
+
+def test_norm_of_wide_groups_far_from_zero_and_with_one_infinity():
+    import gated_deltanet_chunked_02_amd as gdn
+    from oracle import norm
+    from test_gpu_layer import check, host
+    x = torch.randn(2, 900, 512, generator=torch.Generator().manual_seed(2)) + 4096.0
+    y, mean, rstd = gdn.group_norm(x.cuda(), 2)
+    y_ref, _, rstd_ref = norm.group_norm(host(x), 2)
+    # x - mean loses no more than 4096 x 2^-23 x 2 of the deviation
+    check("y", y, y_ref, 1e-3)
+    check("rstd", rstd, rstd_ref, 1e-3)
+    x[0, 17, 300] = float("inf")  # sample 0, group 1
+    z = gdn.group_norm(x.cuda(), 2)[0]
+    assert z[0, ..., 256:].isnan().any()
+    z[0, ..., 256:], y[0, ..., 256:] = 0, 0
+    assert torch.equal(z, y)

@@ -59,9 +59,12 @@ class GdnError(RuntimeError):
                                         gdn_status_string(status) if _lib else "?"))
 
 
+_MOST = 0x7FFFFFFF
+
+
 def _fits(*sizes):
     """Refuses sizes that the descriptors' 32-bit fields cannot hold (ctypes would wrap them)."""
-    if max(sizes) > 0x7FFFFFFF:
+    if max(sizes) > _MOST:
         raise GdnError(2, "a size of %d" % max(sizes))
 
 
@@ -194,25 +197,40 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
+_raw = None
+
+
+def _runtime():
+    """(the current device's index, a device index's raw current stream), looked up once: the Stream
+    object's own lookup takes about ten times as long as the call, which a single token would notice."""
+    global _raw
+    if _raw is None:
+        import torch
+        _raw = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                getattr(torch._C, "_cuda_getCurrentRawStream",
+                        lambda index: torch.cuda.current_stream(index).cuda_stream))
+    return _raw
+
+
 def _current_stream(device=None):
-    """The raw current stream of a device (of the current one by default).  The Stream object's
-    own lookup takes about ten times as long, which a single-token call would notice."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return raw(torch.cuda.current_device() if device is None else device.index)
+    """The raw current stream of a device (of the current one by default)."""
+    if device is None:
+        import torch
+        return _runtime()[1](torch.cuda.current_device())
+    return _runtime()[1](device.index)
 
 
 def _launch(device, call, *args):
     """call(*args, stream) on the current stream of the tensors' device, that device made the current
     one around it: the library launches on the current device, and a device's default stream does not
     say which it belongs to."""
+    current, stream = _runtime()
+    index = device.index
+    if index == current():
+        return call(*args, stream(index))
     import torch
-    if device.index == torch.cuda.current_device():
-        return call(*args, _current_stream(device))
     with torch.cuda.device(device):
-        return call(*args, _current_stream(device))
+        return call(*args, stream(index))
 
 
 def gdn_chunk_fwd(desc: GdnDesc, q, k, v, g, beta, h0, cu_seqlens, scale, o, ht,

@@ -21,8 +21,8 @@ import ctypes
 import torch
 from torch import Tensor
 
-from . import (ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices, _current_stream,
-               _fits, _launch, _need, _validate_conv, load)
+from . import (_MOST, ACTIVATIONS, BF16, F32, GdnConvDesc, GdnError, _check_devices,
+               _current_stream, _fits, _launch, _need, _validate_conv, load)
 
 _CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -75,6 +75,8 @@ def declare(lib):
 
 
 def _stream(stream):
+    if type(stream) is int:
+        return stream
     if stream is None:
         return _current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
@@ -183,9 +185,9 @@ def _indices(name, t, n):
         raise TypeError("%s must be an int32 or int64 tensor" % name)
     if t.shape != (n,):
         raise ValueError("%s must be [%d]" % (name, n))
-    if t.dtype == torch.int64:
-        t = t.clamp(-1, 0x7FFFFFFF)  # outside the pool either way, where a cast would wrap into it
-    return t.to(torch.int32).contiguous()
+    if t.dtype == torch.int64:  # outside the pool either way, where a bare cast would wrap into it
+        t = t.clamp(-1, _MOST).to(torch.int32)
+    return t.contiguous()
 
 
 def _like(name, t, x):
@@ -233,7 +235,8 @@ def _operands(x, dt, A, B, C, D, z, dt_bias, lead):
     G = rows[lead]
     if G == 0 or ch % G:
         raise ValueError("the channels (%d) must be a multiple of the groups (%d)" % (ch, G))
-    _fits(*rows, *shape)
+    if not 0 < x.numel() <= _MOST or S > _MOST:  # else no axis is longer either
+        _fits(*rows, *shape)
     D, dt_bias = _f32("D", D, (ch,)), _f32("dt_bias", dt_bias, (ch,))
     x, sx = _rows(x, lead)
     dt, sdt = _rows(dt, lead)
@@ -359,7 +362,8 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
                                                                         out_indices, n)
     _need(read is not None or state.shape[0] >= n, ValueError,
           "state has fewer lines (%d) than there are sequences (%d)" % (state.shape[0], n))
-    _fits(state.shape[0])
+    if state.shape[0] > _MOST:
+        _fits(state.shape[0])
     dev = x.device
     _on(dev, state=state, x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias,
         cache_indices=read, out_indices=write)
@@ -479,7 +483,8 @@ def _norm_operands(x, num_groups, weight, bias, eps, activation, gate):
     positions = 1
     for n in shape[1:-1]:
         positions *= n
-    _fits(shape[0], positions, C)
+    if not 0 < x.numel() <= _MOST:  # else no axis is longer either
+        _fits(shape[0], positions, C)
     weight, bias = _f32("weight", weight, (C,)), _f32("bias", bias, (C,))
     _like("gate", gate, x)
     if gate is not None:

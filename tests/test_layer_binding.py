@@ -44,8 +44,7 @@ def recorder(monkeypatch):
     for module in (gdn, gdn.ssm):
         monkeypatch.setattr(module, "load", lambda: rec)
         monkeypatch.setattr(module, "_check_devices", lambda *a: None)
-        monkeypatch.setattr(module, "_current_stream", lambda d=None: 0, raising=False)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(gdn, "_raw", (lambda: 0, lambda index: 0))
     monkeypatch.setattr(torch.cuda, "device", device)
     return rec
 

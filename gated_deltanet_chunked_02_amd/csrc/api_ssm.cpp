@@ -150,7 +150,8 @@ ScanLayout scan_layout(const gdn::ScanProblem& p) {
 // The backward's plan: chunks of kBwdChunk tokens and blocks of up to 32 states (eight waves of 4:
 // with blocks of 16 the sums carried from block to block leave LDS for one workgroup of four
 // waves a CU, and 4 x 2048 tokens of 4096 channels and 64 states took 4950 us).  A packed batch has
-// more slots than sequences unless it is empty, so it is composed even when no sequence is long.
+// more slots than sequences unless it has fewer tokens than a chunk, so it is composed even when no
+// sequence is long.
 // Chunks are halved, down to 16 tokens, while they give fewer waves than SIMDs: forward and
 // backward of 257 tokens of 2 x 768 channels take 53.8 us (64-token chunks: 71), of 1000 tokens of
 // 1024 channels 74 us in chunks of 32 (64: 81, 16: 83), of 1000 tokens of 2048 channels 101 us in

@@ -24,8 +24,9 @@
 // Statistics and sums are fp32; every output is rounded once; sums have a fixed order.
 //
 // 16384 gated rows of 4096 channels in 32 groups, bf16 (403 MB) take 74 us, 5.4 TB/s, an addition
-// of the same tensors 70; 8 maps of 4096 positions and 512 channels take 33 us forward and 48 us
-// backward, in which every pass of 33 to 100 MB has about 5 us of start and end.
+// of the same tensors 70; their gradient (671 MB) 133 to 143 us; in fp32 170 us (805 MB) and 267
+// (1342 MB).  8 maps of 4096 positions and 512 channels take 30 us forward and 46 us backward, in
+// which every pass of 33 to 100 MB has about 5 us of start and end.
 #include "norm.h"
 #include "ssm_device.h"
 
@@ -55,7 +56,9 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) r.e[i] = (E)v[i];
     // past the caches where a store is 16 bytes: a map's second pass finds more of x there, and a
-    // large output would not stay (16384 gated rows of 4096 channels 84 to 79 us)
+    // large output would not stay (16384 gated rows of 4096 channels 84 to 79 us).  The 32 bytes of 8
+    // fp32 values are ordinary stores: past the caches 16384 ungated rows of 4096 take 95 us for 110,
+    // but the gradient of gated ones 280 for 267, and 8 maps of 4096 x 512 47 forward for 44
     if constexpr (kBytes == 16)
       __builtin_nontemporal_store(__builtin_bit_cast(f32x4, r), reinterpret_cast<f32x4*>(p));
     else
@@ -768,7 +771,11 @@ bool fold_slabs(const NormProblem& p, const MapPlan& q, int most) {
 }
 
 // Maps so small that one launch with short reads is quicker than three: at most this many values
-// a (sample, group), or a row too wide for the lanes' registers.
+// a (sample, group), or a row too wide for the lanes' registers.  bf16, one launch and three: 64
+// groups of 630 values 4.7 and 20.7 us, 64 of 2560 10.5 and 21.1, 256 of 4096 (one channel each)
+// 21.6 and 73; 256 of 8192 26.9 and 21.4.  Of many groups the three passes are already quicker near
+// the bound, which does not look at their number: 8192 of 1024 32.9 and 30.9, 1024 of 4096 39.5 and
+// 32.7, 2048 of 4096 35.6 and 23.1; 524288 of 64 take 498 and 553.
 constexpr long kGroupItems = 4096;
 bool group_shape(const NormProblem& p) { return p.P == 1 || (long)p.P * p.cpg <= kGroupItems; }
 

@@ -23,10 +23,11 @@
 // state).  A transposing butterfly merges two registers into one at every step (lanes keep the
 // half of the pair that their lane bit names), so 64 sums cost 63 merges, and end one to a lane.
 //
-// Measured on 8 x 2048 tokens of 4096 channels, 16 states, bf16, gated: 1.54 ms in all, of which the
-// chunks' states 342 us (the vector units busy throughout), their composition 58 us (the states'
-// bytes), the gradients 1.18 ms (79 % busy: 202 registers leave two waves a SIMD; a cap at 168 for
-// three spills) and the partial sums 40 us.
+// Measured on 8 x 2048 tokens of 4096 channels, 16 states, bf16, gated: 1.55 ms a call among others.
+// Profiled, each kernel by itself, 1.59 ms: packing B and C 5 us, the chunks' states 336 us (the
+// vector units busy throughout), their composition 59 us (the states' bytes), the gradients 1.15 ms
+// (79 % busy: 202 registers leave two waves a SIMD; a cap at 168 for three spills), the partial sums
+// 40 us.
 #include <type_traits>
 
 #include "ssm_device.h"

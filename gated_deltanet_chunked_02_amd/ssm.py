@@ -288,7 +288,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=Fal
     x, dt, z: [B, T, channels] (bf16 or fp32; z None: no gate); A [channels, dstate] fp32;
     B, C: [B, T, groups, dstate], shared by channels / groups channels each; D, dt_bias
     [channels] fp32 or None; initial_state [N, channels, dstate] fp32 or None; cu_seqlens
-    [N + 1] for a packed batch (B == 1).  Returns (y in x's dtype, final state fp32 or None)."""
+    [N + 1] for a packed batch (B == 1; y of tokens that no sequence has is not written).  Returns (y
+    in x's dtype, final state fp32 or None)."""
     desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 2)
     cu, N = _sequences(x, cu_seqlens)
     h0 = _f32("initial_state", initial_state, (N, desc.channels, desc.dstate))
@@ -314,7 +315,9 @@ def selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_soft
     """Gradients of selective_scan's inputs on the current stream, given the gradient ``dy`` of y
     (x's shape and dtype) and ``dht`` of the final state (fp32, or None: zero); the forward's
     inputs as there.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinitial_state): dx, ddt,
-    dz, dB, dC in x's dtype, the others in fp32, None where the input is None."""
+    dz, dB, dC in x's dtype, the others in fp32, None where the input is None.  Those of tokens of a
+    packed batch that no sequence has are unspecified.  The workspace is larger than the inputs (see
+    include/gdn.h); one may be given (uint8)."""
     desc, x, dt, A, B, C, D, z, dt_bias = _operands(x, dt, A, B, C, D, z, dt_bias, 2)
     cu, N = _sequences(x, cu_seqlens)
     states = (N, desc.channels, desc.dstate)
@@ -401,6 +404,7 @@ def causal_conv1d_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state
     """Gradients of causal_conv1d's inputs on the current stream, given ``dy`` [B, T, C] and
     ``dfinal_state`` [N, W - 1, C] of the state lines afterwards (None: zero).  initial_state
     [N, W - 1, C]: the inputs before each sequence, its line before the forward (None: zeros).
+    dx of tokens of a packed batch that no sequence has is not written.
     Returns (dx in x's dtype, dweight [C, W] and dbias [C] fp32, dinitial_state in x's dtype);
     dbias and dinitial_state are None where the input is None."""
     _validate_conv(x, weight, bias, None, None, None, cu_seqlens)
@@ -502,7 +506,7 @@ def group_norm(x, num_groups, weight=None, bias=None, eps=1e-5, activation=None,
     (statistics over a sample's positions and a group's channels), bf16 or fp32; weight, bias
     [channels] fp32 or None; gate: x's shape and dtype, or None.  y = act(u) without a gate and
     u act(gate) with one, u the normalised, scaled and shifted x.  Returns (y, mean, rstd), mean
-    and rstd [samples, num_groups] fp32."""
+    and rstd [samples, num_groups] fp32 (NaN where there are no positions)."""
     desc, x, weight, bias, gate = _norm_operands(x, num_groups, weight, bias, eps, activation,
                                                  gate)
     dev = x.device

@@ -211,9 +211,10 @@ gdn_status gdn_causal_conv1d_fwd(const gdn_conv_desc* d, const void* x, const fl
  * tokens of a packed batch) and one more, or of 257 tokens if it is longer, pass 2 GiB.  Pointers are
  * device pointers aligned to their element; errors are returned before any launch; nothing is
  * synchronised or allocated.
- * x, dt, A, Bm, Cm, y are required unless B*T = 0 (A always).  h0 and ht may be the same
- * buffer.  Few or long sequences are split into chunks that run in parallel, so results depend
- * on the descriptor in their last bits, never on scheduling. */
+ * x, dt, A, Bm, Cm, y are required unless B*T = 0 (A always).  h0 and ht may be the same buffer.  y
+ * of tokens of a packed batch that no sequence has is not written.  Few or long sequences are split
+ * into chunks that run in parallel, so results depend on the descriptor in their last bits, never on
+ * scheduling. */
 typedef struct gdn_scan_desc {
   int32_t B, T;         /* dense [B, T, ...]; packed: B = 1, T = total tokens               */
   int32_t N;            /* sequences: B (or 0) for a dense batch, len(cu_seqlens) - 1       */
@@ -251,7 +252,12 @@ size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_desc* d, gdn_status*
  *   dA [channels, dstate], dD, ddt_bias [channels], dh0 [N, channels, dstate]  f32; dD, ddt_bias
  *                      and dh0 may be NULL (not written)
  * Sums are made in a fixed order (no atomics): the same call gives the same bits.  Gradients of
- * tokens of a packed batch that no sequence has are unspecified. */
+ * tokens of a packed batch that no sequence has are unspecified.
+ * The workspace is larger than the inputs: beside B and C as fp32 rows it holds dB's and dC's partial
+ * sums for every block of 64 channels of a group, 8 * B*T * dstate bytes a block (dstate rounded up
+ * to 4, 8, 16 or a multiple of 32), and three sets of states for every chunk of 64 tokens (fewer in
+ * small batches), 12 * channels * dstate bytes a chunk: 350 MB for 8 x 2048 tokens of 4096 channels
+ * and 16 states, 1.36 GB with 64 states, 5.4 GB with 256. */
 gdn_status gdn_selective_scan_bwd(const gdn_scan_desc* d, const void* x, const void* dt,
                                   const float* A, const void* Bm, const void* Cm,
                                   const float* D, const void* z, const float* dt_bias,
@@ -280,8 +286,9 @@ gdn_status gdn_selective_state_update(const gdn_scan_desc* d, float* state, cons
  *   dweight  [C, W], dbias [C]   f32 sums over all tokens (NULL: not written)
  *   dinitial [N, W - 1, C]  dtype, the gradient of initial (NULL: not written)
  * d->state_lines is ignored; shapes, checks and the rest as for the forward (x, dy, dx, initial,
- * dfinal and dinitial 16-byte aligned; at most 65535 * 1024 channels).  Sums are made in a fixed order.  The workspace (256-byte
- * aligned, gdn_causal_conv1d_bwd_workspace_size bytes) is required when B*T > 0. */
+ * dfinal and dinitial 16-byte aligned; at most 65535 * 1024 channels).  Sums are made in a fixed
+ * order.  dx of tokens of a packed batch that no sequence has is not written.  The workspace
+ * (256-byte aligned, gdn_causal_conv1d_bwd_workspace_size bytes) is required when B*T > 0. */
 size_t gdn_causal_conv1d_bwd_workspace_size(const gdn_conv_desc* d, gdn_status* status);
 
 gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const float* weight,

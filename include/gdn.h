@@ -214,7 +214,9 @@ gdn_status gdn_causal_conv1d_fwd(const gdn_conv_desc* d, const void* x, const fl
  * x, dt, A, Bm, Cm, y are required unless B*T = 0 (A always).  h0 and ht may be the same buffer.  y
  * of tokens of a packed batch that no sequence has is not written.  Few or long sequences are split
  * into chunks that run in parallel, so results depend on the descriptor in their last bits, never on
- * scheduling. */
+ * scheduling.  An infinity or a NaN in x, dt, z or dy reaches its own channel of its own sequence and
+ * the gradients that sum over it (dB and dC of its group, the parameters'); what an infinity makes
+ * there is not finite, but may be NaN where the formula has an infinity. */
 typedef struct gdn_scan_desc {
   int32_t B, T;         /* dense [B, T, ...]; packed: B = 1, T = total tokens               */
   int32_t N;            /* sequences: B (or 0) for a dense batch, len(cu_seqlens) - 1       */

@@ -51,3 +51,34 @@ def test_norm_of_wide_groups_far_from_zero_and_with_one_infinity():
     assert z[0, ..., 256:].isnan().any()
     z[0, ..., 256:], y[0, ..., 256:] = 0, 0
     assert torch.equal(z, y)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("S", [1, 5, 16, 40])
+def test_one_bad_input_stays_in_its_channel_and_sequence(S, bad):
+    """In the last channel of a group, whose workgroup has lanes without a channel."""
+    from test_gpu_selective import make, run_fwd
+    from test_gpu_selective_bwd import run_bwd
+    lens, C, G = [50, 40, 260], 70, 2
+    p = make(C=C, G=G, S=S, dtype="f32", lens=lens, seed=S)
+    clean = dict(zip(("y", "ht"), run_fwd(p)), **run_bwd(p))
+    others = [c for c in range(C) if c != 34]
+    for key in ("x", "dt", "z", "dy"):
+        q = dict(p, **{key: p[key].clone()})
+        q[key][0, 60, 34] = bad  # token 10 of sequence 1
+        got = dict(zip(("y", "ht"), run_fwd(q)), **run_bwd(q))
+        for k in ("y", "dx", "ddt", "dz"):  # [1, T, C]
+            assert torch.equal(got[k][..., others], clean[k][..., others]), (key, k)
+            for cut in (slice(0, 50), slice(90, None)):
+                assert torch.equal(got[k][:, cut], clean[k][:, cut]), (key, k)
+        for k in ("dB", "dC"):  # [1, T, G, S]
+            assert torch.equal(got[k][:, :, 1], clean[k][:, :, 1]), (key, k)
+            for cut in (slice(0, 50), slice(90, None)):
+                assert torch.equal(got[k][:, cut], clean[k][:, cut]), (key, k)
+        for k in ("ht", "dh0"):  # [N, C, S]
+            assert torch.equal(got[k][:, others], clean[k][:, others]), (key, k)
+            assert torch.equal(got[k][[0, 2]], clean[k][[0, 2]]), (key, k)
+        for k in ("dA", "dD", "dbias"):
+            assert torch.equal(got[k][others], clean[k][others]), (key, k)
+        if key != "dy":
+            assert not got["y"][0, 60, 34].isfinite()

@@ -18,6 +18,8 @@ The short convolution before it (low level gdn_causal_conv1d_fwd):
                       has_initial_state=None, cu_seqlens=None, activation=None)
 The selective state-space layer (module ssm): selective_scan, selective_scan_bwd,
 selective_state_update, causal_conv1d_bwd, group_norm, group_norm_bwd.
+Linear attention with a decay for each head (module linear): linear_attention,
+linear_attention_bwd, linear_state_update.
 """
 from __future__ import annotations
 
@@ -39,6 +41,9 @@ __all__ = [
     "selective_state_update", "gdn_causal_conv1d_bwd", "gdn_causal_conv1d_bwd_workspace_size",
     "causal_conv1d_bwd", "GdnNormDesc", "gdn_group_norm_fwd", "gdn_group_norm_bwd",
     "gdn_group_norm_workspace_size", "group_norm", "group_norm_bwd",
+    "GdnLinearDesc", "gdn_linear_attn_fwd", "gdn_linear_attn_workspace_size",
+    "gdn_linear_attn_bwd", "gdn_linear_attn_bwd_workspace_size", "gdn_linear_state_update",
+    "linear_attention", "linear_attention_bwd", "linear_state_update",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -131,6 +136,7 @@ def load(path: str = LIB_PATH):
     lib.gdn_causal_conv1d_fwd.argtypes = [ctypes.POINTER(GdnConvDesc), P, P, P, P, P, P, P, P,
                                           P]
     ssm.declare(lib)
+    linear.declare(lib)
     _lib = lib
     return lib
 
@@ -631,3 +637,9 @@ from .ssm import (  # noqa: E402
     gdn_selective_scan_bwd_workspace_size, gdn_selective_scan_fwd,
     gdn_selective_scan_workspace_size, gdn_selective_state_update, group_norm, group_norm_bwd,
     selective_scan, selective_scan_bwd, selective_state_update)
+# linear attention's (they use the state-space layer's helpers)
+from . import linear  # noqa: E402
+from .linear import (  # noqa: E402
+    GdnLinearDesc, gdn_linear_attn_bwd, gdn_linear_attn_bwd_workspace_size, gdn_linear_attn_fwd,
+    gdn_linear_attn_workspace_size, gdn_linear_state_update, linear_attention,
+    linear_attention_bwd, linear_state_update)

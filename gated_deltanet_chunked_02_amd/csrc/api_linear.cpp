@@ -1,0 +1,313 @@
+// C ABI of the linear attention calls (declared in include/gdn.h): host-side validation, workspace
+// layout and dispatch to the launchers.  No allocation, no synchronisation.
+#include <stdint.h>
+#include <string.h>
+
+#include "gdn.h"
+#include "linear.h"
+#include "ssm.h"
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Rows are read 16 bytes at a time and reached from a chunk's first one by 31-bit byte offsets, so
+// they are less than 2^23 elements apart (64 rows of 4 bytes).
+constexpr int64_t kFar = (int64_t)1 << 23;
+
+gdn_status check_row(int64_t given, int64_t row, int e, int64_t* out) {
+  *out = given == 0 ? row : given;
+  if (*out < row || (*out * e) % 16 != 0) return GDN_ERR_INVALID_ARG;
+  return *out < kFar ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+// Descriptor checks shared by the entry points; fills the shape part of the problem.
+gdn_status check_linear(const gdn_linear_desc* d, bool packed, gdn::LinearProblem* p) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->B < 1 || d->T < 0 || d->N < 0 || d->H < 1 || d->Hg < 1 || d->H % d->Hg != 0 ||
+      d->Dk < 1 || d->Dv < 1)
+    return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (d->head_decay != 0 && d->head_decay != 1) return GDN_ERR_INVALID_ARG;
+  if (packed ? d->B != 1 : (d->N != 0 && d->N != d->B)) return GDN_ERR_INVALID_ARG;
+  if (d->Dk % 8 != 0 || d->Dv % 8 != 0 || d->Dk > 256 || d->Dv > 256) return GDN_ERR_UNSUPPORTED;
+  memset(p, 0, sizeof(*p));
+  const long long Ttot = (long long)d->B * d->T;
+  p->N = packed ? d->N : d->B;
+  if (Ttot > (1LL << 30) || p->N > (1 << 16) || (int64_t)d->H * d->Dk >= kFar ||
+      (int64_t)d->H * d->Dv >= kFar)
+    return GDN_ERR_UNSUPPORTED;
+  const int e = d->dtype == GDN_F32 ? 4 : 2;
+  const int64_t kw = (int64_t)d->Hg * d->Dk, vw = (int64_t)d->H * d->Dv;
+  gdn_status s = check_row(d->q_stride, kw, e, &p->sq);
+  if (s == GDN_OK) s = check_row(d->k_stride, kw, e, &p->sk);
+  if (s == GDN_OK) s = check_row(d->v_stride, vw, e, &p->sv);
+  if (s != GDN_OK) return s;
+  p->T = d->T;
+  p->Ttot = (int)Ttot;
+  p->H = d->H;
+  p->Hg = d->Hg;
+  p->Dk = d->Dk;
+  p->Dv = d->Dv;
+  p->f32 = d->dtype == GDN_F32;
+  p->head_decay = d->head_decay != 0;
+  p->scale = d->scale;
+  return GDN_OK;
+}
+
+// Segment length: sequences stay whole where their heads (times the value slabs) make half of the
+// `fill` workgroups that run at once, and are cut into as many segments as fill them elsewhere, of
+// at least kMinSegment tokens; a packed batch is cut at twice its mean length at least, so that one
+// long sequence does not run alone.
+constexpr int kMinSegment = 128;
+
+void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
+  p->Lc = gdn::kScanNoSplit;
+  if (p->N > 0 && p->Ttot > 0) {
+    const long long units = (long long)p->H * slabs, longest = packed ? p->Ttot : p->T;
+    long long L = longest;
+    if (units * p->N * 2 <= fill) {
+      const long long each = packed ? fill / units : fill / (units * p->N);
+      L = (longest + each - 1) / each;
+    } else if (packed) {
+      L = 2LL * ((p->Ttot + p->N - 1) / p->N);
+    }
+    L = (L + gdn::kLinearChunk - 1) / gdn::kLinearChunk * gdn::kLinearChunk;
+    if (L < kMinSegment) L = kMinSegment;
+    if (L < longest) p->Lc = (int)L;
+  }
+  p->slots = p->N == 0 ? 0
+             : packed  ? p->Ttot / p->Lc + p->N
+                       : p->N * (int)(p->T > p->Lc ? ((long long)p->T + p->Lc - 1) / p->Lc : 1);
+}
+
+int slabs_of(const gdn::LinearProblem& p) { return (p.Dv + gdn::kLinearSlab - 1) / gdn::kLinearSlab; }
+
+constexpr int kFwdFill = 512;  // two workgroups a CU
+constexpr int kBwdFill = 256;  // one
+
+void plan_fwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, slabs_of(*p), kFwdFill); }
+void plan_bwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, 1, kBwdFill); }
+
+// A launch has fewer than 2^32 threads: segments' heads and slabs in workgroups of up to 512, the
+// composition's four values a thread, and the shared heads' sums.
+bool grids_ok(const gdn::LinearProblem& p) {
+  const long long most = 1LL << 32, cell = ((long long)p.Dk * p.Dv / 4 + 255) / 256 * 256;
+  return (long long)p.slots * p.H * slabs_of(p) * 512 < most && (long long)p.N * p.H * cell < most &&
+         (long long)p.Ttot * p.Hg * p.Dk / 4 + 256 < most;
+}
+
+struct FwdLayout {
+  size_t states, sums, total;
+};
+
+FwdLayout fwd_layout(const gdn::LinearProblem& p) {
+  FwdLayout L = {};
+  if (p.Lc == gdn::kScanNoSplit) return L;
+  const size_t heads = (size_t)p.slots * p.H;
+  L.sums = align_up(heads * p.Dk * p.Dv * 4);
+  L.total = L.sums + align_up(heads * 4);
+  return L;
+}
+
+struct BwdLayout {
+  size_t states, sums, grads, chunks, part, dgp, total;
+};
+
+BwdLayout bwd_layout(const gdn::LinearProblem& p, bool packed) {
+  BwdLayout L = {};
+  size_t o = 0;
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
+    return at;
+  };
+  const size_t heads = (size_t)p.slots * p.H;
+  const int C = gdn::linear_chunk(p.f32);
+  const size_t chunks = p.Ttot == 0 ? 0
+                        : packed    ? (size_t)p.Ttot / C + p.N
+                                    : (size_t)p.N * (((size_t)p.T + C - 1) / C);
+  const bool split = p.Lc != gdn::kScanNoSplit;
+  L.states = take(split ? heads * p.Dk * p.Dv * 4 : 0);
+  L.sums = take(split ? heads * 4 : 0);
+  L.grads = take(split ? heads * p.Dk * p.Dv * 4 : 0);
+  L.chunks = take(chunks * p.H * gdn::linear_tile(p.Dk) * gdn::linear_tile(p.Dv) * 4);
+  L.part = take(p.H != p.Hg ? (size_t)p.Ttot * p.H * p.Dk * 8 : 0);
+  L.dgp = take(p.head_decay ? heads * 4 : 0);
+  L.total = o;
+  return L;
+}
+
+bool looks_packed(const gdn_linear_desc* d) { return d && d->N != 0 && d->N != d->B; }
+
+gdn_status check_bwd(const gdn_linear_desc* d, bool packed, gdn::LinearProblem* p) {
+  gdn_status s = check_linear(d, packed, p);
+  if (s != GDN_OK) return s;
+  if (d->Dk > 128 || d->Dv > 128) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+bool space_ok(const gdn_linear_desc* d, size_t need) {
+  return need == 0 || (d->workspace && d->workspace_bytes >= need && aligned(d->workspace, kAlign));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_linear_attn_workspace_size(const gdn_linear_desc* d, gdn_status* status) {
+  gdn::LinearProblem p;
+  const bool packed = looks_packed(d);
+  gdn_status s = check_linear(d, packed, &p);
+  size_t need = 0;
+  if (s == GDN_OK) {
+    plan_fwd(&p, packed);
+    if (!grids_ok(p)) s = GDN_ERR_UNSUPPORTED;
+    need = fwd_layout(p).total;
+    if (!packed && d->B == 1) {  // one sequence may also come as a packed batch of one
+      plan_fwd(&p, true);
+      const size_t alt = fwd_layout(p).total;
+      if (alt > need) need = alt;
+    }
+  }
+  if (status) *status = s;
+  return s == GDN_OK ? need : 0;
+}
+
+gdn_status gdn_linear_attn_fwd(const gdn_linear_desc* d, const void* q, const void* k,
+                               const void* v, const float* g, const float* h0,
+                               const int32_t* cu_seqlens, void* o, float* ht,
+                               hipStream_t stream) {
+  gdn::LinearProblem p;
+  const gdn_status s = check_linear(d, cu_seqlens != nullptr, &p);
+  if (s != GDN_OK) return s;
+  if (p.Ttot > 0 && (!q || !k || !v || !g || !o)) return GDN_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, (const void*)o, (const void*)h0, (const void*)ht})
+    if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(g, 4) || !aligned(cu_seqlens, 4)) return GDN_ERR_INVALID_ARG;
+  if (p.N == 0) return GDN_OK;
+  plan_fwd(&p, cu_seqlens != nullptr);
+  if (!grids_ok(p)) return GDN_ERR_UNSUPPORTED;
+  const FwdLayout L = fwd_layout(p);
+  if (!space_ok(d, L.total)) return GDN_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(d->workspace);
+  p.states = reinterpret_cast<float*>(ws + L.states);
+  p.sums = reinterpret_cast<float*>(ws + L.sums);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = g;
+  p.h0 = h0;
+  p.cu = cu_seqlens;
+  p.o = o;
+  p.ht = ht;
+  return gdn::launch_linear_fwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_desc* d, gdn_status* status) {
+  gdn::LinearProblem p;
+  const bool packed = looks_packed(d);
+  gdn_status s = check_bwd(d, packed, &p);
+  size_t need = 0;
+  if (s == GDN_OK) {
+    plan_bwd(&p, packed);
+    if (!grids_ok(p)) s = GDN_ERR_UNSUPPORTED;
+    need = bwd_layout(p, packed).total;
+    if (!packed && d->B == 1) {
+      plan_bwd(&p, true);
+      const size_t alt = bwd_layout(p, true).total;
+      if (alt > need) need = alt;
+    }
+  }
+  if (status) *status = s;
+  return s == GDN_OK ? need : 0;
+}
+
+gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const void* k,
+                               const void* v, const float* g, const float* h0,
+                               const int32_t* cu_seqlens, const void* dout, const float* dht,
+                               void* dq, void* dk, void* dv, float* dg, float* dh0,
+                               hipStream_t stream) {
+  const bool packed = cu_seqlens != nullptr;
+  gdn::LinearProblem p;
+  const gdn_status s = check_bwd(d, packed, &p);
+  if (s != GDN_OK) return s;
+  if (p.Ttot > 0 && (!q || !k || !v || !g || !dout || !dq || !dk || !dv)) return GDN_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, dout, (const void*)h0, (const void*)dht, (const void*)dq,
+                        (const void*)dk, (const void*)dv, (const void*)dh0})
+    if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)g, (const void*)cu_seqlens, (const void*)dg})
+    if (!aligned(x, 4)) return GDN_ERR_INVALID_ARG;
+  plan_bwd(&p, packed);
+  if (!grids_ok(p)) return GDN_ERR_UNSUPPORTED;
+  const BwdLayout L = bwd_layout(p, packed);
+  if (!space_ok(d, L.total)) return GDN_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(d->workspace);
+  auto at = [ws](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  p.states = at(L.states);
+  p.sums = at(L.sums);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = g;
+  p.h0 = h0;
+  p.cu = cu_seqlens;
+  gdn::LinearBwd b;
+  b.dout = dout;
+  b.dht = dht;
+  b.dq = dq;
+  b.dk = dk;
+  b.dv = dv;
+  b.dg = dg;
+  b.dh0 = dh0;
+  b.grads = at(L.grads);
+  b.chunks = at(L.chunks);
+  b.part = at(L.part);
+  b.dgp = at(L.dgp);
+  return gdn::launch_linear_bwd(p, b, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+gdn_status gdn_linear_state_update(const gdn_linear_desc* d, float* state, const void* q,
+                                   const void* k, const void* v, const float* g,
+                                   const int32_t* cache_indices, const int32_t* out_indices,
+                                   void* o, hipStream_t stream) {
+  gdn::LinearProblem p;
+  const gdn_status s = check_linear(d, false, &p);
+  if (s != GDN_OK) return s;
+  if (d->T != 1 || d->state_lines < 1) return GDN_ERR_INVALID_ARG;
+  if (!state || !q || !k || !v || !g || !o) return GDN_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)state, q, k, v, (const void*)o})
+    if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(g, 4) || !aligned(cache_indices, 4) || !aligned(out_indices, 4))
+    return GDN_ERR_INVALID_ARG;
+  // a workgroup of 256 threads for each 32 columns of a head
+  if ((long long)d->B * p.H * ((p.Dv + 31) / 32) >= (1LL << 24)) return GDN_ERR_UNSUPPORTED;
+  gdn::LinearStepProblem x;
+  x.B = d->B;
+  x.H = p.H;
+  x.Hg = p.Hg;
+  x.Dk = p.Dk;
+  x.Dv = p.Dv;
+  x.lines = d->state_lines;
+  x.f32 = p.f32;
+  x.head_decay = p.head_decay;
+  x.scale = p.scale;
+  x.sq = p.sq;
+  x.sk = p.sk;
+  x.sv = p.sv;
+  x.state = state;
+  x.q = q;
+  x.k = k;
+  x.v = v;
+  x.g = g;
+  x.read = cache_indices;
+  x.write = out_indices;
+  x.o = o;
+  return gdn::launch_linear_step(x, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,86 @@
+// Host-side views of the linear attention calls, shared by the C ABI (api_linear.cpp) and the
+// launchers (linear.hip, linear_bwd.hip, linear_step.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdn {
+
+constexpr int kLinearChunk = 64;     // tokens of a chunk in bf16
+constexpr int kLinearChunkF32 = 32;  // in fp32, whose tiles take twice the LDS
+constexpr int kLinearSlab = 128;     // value columns of a workgroup, at most
+
+// Segments are chunks of Lc tokens (a multiple of the tile chunk, or kScanNoSplit for whole
+// sequences) with the slots of ScanProblem (ssm.h); tile chunks have slots of the same form with the
+// chunk length in place of Lc.
+struct LinearProblem {
+  int T, Ttot, N;      // tokens a sequence (dense), all tokens, sequences
+  int H, Hg, Dk, Dv;   // value heads, q/k heads, head sizes
+  int Lc, slots;       // segment length, segment slots
+  int group;           // workgroups in a row that share q and k rows (set by the launchers)
+  bool f32, head_decay;
+  float scale;
+  int64_t sq, sk, sv;  // elements from one token's row to the next
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;      // [H] with head_decay, [B, T, H] without
+  const float* h0;     // [N, H, Dk, Dv] or null
+  const int32_t* cu;   // [N + 1] or null
+  void* o;
+  float* ht;           // [N, H, Dk, Dv] or null
+  float* states;       // workspace: [slots, H, Dk, Dv], each segment's own end state, then its start
+  float* sums;         // workspace: [slots, H], each segment's sum of log2 decays
+};
+
+hipError_t launch_linear_fwd(const LinearProblem& p, hipStream_t st);
+
+// A pass over segments that makes states only: sums of x_t y_t^T.
+struct LinearPass {
+  const void* x;       // k, or q with reverse
+  const void* y;       // v, or dout
+  int64_t sx, sy;
+  bool reverse;        // from the segments' ends back
+  float* own;          // [slots, H, Dk, Dv] every segment's own sum
+  float* chunks;       // instead: every tile chunk's start state (LinearBwd::chunks)
+};
+hipError_t launch_linear_state(const LinearProblem& p, const LinearPass& a, hipStream_t st);
+hipError_t launch_linear_compose(const LinearProblem& p, hipStream_t st);
+
+struct LinearBwd {
+  const void* dout;    // [B, T, H, Dv]
+  const float* dht;    // [N, H, Dk, Dv] or null
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;           // [H] or [B, T, H], or null
+  float* dh0;          // or null
+  float* grads;        // workspace: [slots, H, Dk, Dv], as states but from the ends
+  float* chunks;       // workspace: the state at every tile chunk's start, in the kernels' tile order
+  float* part;         // workspace: [2, Ttot, H, Dk] dq and dk of every value head (shared q/k heads)
+  float* dgp;          // workspace: [slots, H] sums of dg (head_decay)
+};
+// Tile sizes of the backward: 64 or 128 for head sizes up to that.
+inline int linear_tile(int D) { return D <= 64 ? 64 : 128; }
+inline int linear_chunk(bool f32) { return f32 ? kLinearChunkF32 : kLinearChunk; }
+hipError_t launch_linear_bwd(const LinearProblem& p, const LinearBwd& b, hipStream_t st);
+
+struct LinearStepProblem {
+  int B, H, Hg, Dk, Dv, lines;
+  bool f32, head_decay;
+  float scale;
+  int64_t sq, sk, sv;
+  float* state;           // [lines, H, Dk, Dv]
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const int32_t* read;    // [B] or null (line b)
+  const int32_t* write;   // [B] or null (the line read)
+  void* o;
+};
+hipError_t launch_linear_step(const LinearStepProblem& p, hipStream_t st);
+
+}  // namespace gdn

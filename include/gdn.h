@@ -299,6 +299,89 @@ gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const fl
                                  void* dx, float* dweight, float* dbias, void* dinitial,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Linear attention with a decay for each head, the delta rule's recurrence without its correction.
+ * For every sequence n and value head h with q/k head hk = h / (H / Hg), from S = h0[n, h] (zero when
+ * h0 is NULL), for each token t
+ *
+ *     S   <- exp(g) S + k_t v_t^T          (k_t, q_t of head hk, v_t of head h)
+ *     o_t <- scale S^T q_t
+ *
+ * and finally ht[n, h] = S.  g is a log-decay for each head (head_decay = 1) or each token and head.
+ *
+ * Layouts (row-major; a token's row is contiguous, the rows *_stride elements apart over the whole
+ * [B, T] token axis; 0 = rows one after another):
+ *   q, k    [B, T, Hg, Dk]   dtype (bf16 or f32)
+ *   v, o    [B, T, H, Dv]    dtype; o contiguous
+ *   g       [H] or [B, T, H] f32 (at most 0 in the intended use; -inf forgets the state)
+ *   h0, ht  [N, H, Dk, Dv]   f32; cu_seqlens [N + 1] int32 as for gdn_chunk_fwd
+ * Dk and Dv are multiples of 8 up to 256, equal or not; any H, Hg dividing it.  Pointers are device
+ * pointers aligned to 16 bytes (g, cu_seqlens, indices: 4) and rows a multiple of 16 bytes apart.
+ * GDN_ERR_UNSUPPORTED beyond 2^30 tokens, 65536 sequences, rows of 2^23 elements or launches of 2^32
+ * threads.  Errors are returned before any launch; nothing is synchronised or allocated.
+ * q, k, v, g, o are required unless B*T = 0.  h0 and ht may be the same buffer.  o of tokens of a
+ * packed batch that no sequence has is not written.
+ * States and sums are fp32.  In bf16, the scores within a chunk of 64 tokens and the state that meets
+ * q are each rounded once to bf16 on their way to o (relative error of o about 2.4e-3, of which its own
+ * rounding is 1.7e-3); ht is as exact as fp32 sums.  Few or long sequences are split into segments
+ * that run in parallel, so results depend on the descriptor in their last bits, never on scheduling.
+ * An infinity or a NaN in q, k, v or g reaches its own head (its q/k head's value heads) of its own
+ * sequence, from the chunk it is in: the outputs of that chunk's earlier tokens may be NaN too. */
+typedef struct gdn_linear_desc {
+  int32_t B, T;         /* dense [B, T, ...]; packed: B = 1, T = total tokens               */
+  int32_t N;            /* sequences: B (or 0) for a dense batch, len(cu_seqlens) - 1       */
+  int32_t H, Hg;        /* value heads, q/k heads; H % Hg == 0                              */
+  int32_t Dk, Dv;       /* head sizes                                                       */
+  int32_t dtype;        /* gdn_dtype of q, k, v, o (and of dout, dq, dk, dv)                */
+  int32_t head_decay;   /* 1: g [H]; 0: g [B, T, H]                                         */
+  int32_t state_lines;  /* gdn_linear_state_update only: lines of the pool                  */
+  float scale;          /* Dk^-0.5 is the usual choice                                      */
+  int64_t q_stride, k_stride, v_stride;
+  void* workspace;      /* 256-byte aligned, as many bytes as the call's query gives        */
+  size_t workspace_bytes;
+} gdn_linear_desc;
+
+/* Bytes of workspace gdn_linear_attn_fwd needs: 0 where sequences stay whole (dense and packed
+ * alike: N other than 0 or B is a packed batch; B == 1 may be either).  Host-only.  0 and *status set
+ * when refused. */
+size_t gdn_linear_attn_workspace_size(const gdn_linear_desc* d, gdn_status* status);
+
+gdn_status gdn_linear_attn_fwd(const gdn_linear_desc* d, const void* q, const void* k,
+                               const void* v, const float* g, const float* h0,
+                               const int32_t* cu_seqlens, void* o, float* ht, hipStream_t stream);
+
+/* Bytes of workspace gdn_linear_attn_bwd needs.  Host-only. */
+size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_desc* d, gdn_status* status);
+
+/* The gradient of gdn_linear_attn_fwd, from the forward's inputs (nothing of a forward call is kept)
+ * and the gradients of its outputs.
+ *   dout    [B, T, H, Dv]  dtype, contiguous
+ *   dht     [N, H, Dk, Dv] f32, or NULL (zero)
+ *   dq, dk  [B, T, Hg, Dk] dtype, contiguous: summed over the value heads that share them in fp32,
+ *                          rounded once
+ *   dv      [B, T, H, Dv]  dtype, contiguous
+ *   dg      g's shape      f32, or NULL (not wanted)
+ *   dh0     [N, H, Dk, Dv] f32, or NULL (not written); may be dht's buffer
+ * Dk and Dv up to 128 (GDN_ERR_UNSUPPORTED beyond).  Sums have a fixed order (no atomics).  Gradients
+ * of tokens of a packed batch that no sequence has are not written.
+ * The workspace holds the state at every chunk's start in fp32: 4 Dk Dv bytes (sizes rounded up to 64
+ * or 128) a value head and 64 tokens (32 in f32), 1 KB a token and head of 128 x 128; and, where q/k
+ * heads are shared, every value head's dq and dk in fp32, 8 Dk bytes a token and head. */
+gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const void* k,
+                               const void* v, const float* g, const float* h0,
+                               const int32_t* cu_seqlens, const void* dout, const float* dht,
+                               void* dq, void* dk, void* dv, float* dg, float* dh0,
+                               hipStream_t stream);
+
+/* The same recurrence for one token of each of d->B sequences (T is 1, N is 0 or B; g [H] or [B, H]),
+ * the states in a pool: sequence b reads line cache_indices[b] (b when NULL) of state [state_lines, H,
+ * Dk, Dv] and writes line out_indices[b] (the line it read when NULL).  A line read from outside the
+ * pool is a zero start, one written outside it is dropped.  A line that one sequence writes and
+ * another reads or writes in the same call has unspecified contents.  No workspace. */
+gdn_status gdn_linear_state_update(const gdn_linear_desc* d, float* state, const void* q,
+                                   const void* k, const void* v, const float* g,
+                                   const int32_t* cache_indices, const int32_t* out_indices,
+                                   void* o, hipStream_t stream);
+
 /* Group norm of channels-last data with an activation or a gate: the norm of a token's heads after
  * a mixing layer (positions = 1), or of a feature map's channel groups.  For sample n and group g
  * of channels / groups consecutive channels, over the sample's positions and the group's channels,

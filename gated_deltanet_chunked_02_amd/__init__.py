@@ -19,7 +19,8 @@ The short convolution before it (low level gdn_causal_conv1d_fwd):
 The selective state-space layer (module ssm): selective_scan, selective_scan_bwd,
 selective_state_update, causal_conv1d_bwd, group_norm, group_norm_bwd.
 Linear attention with a decay for each head (module linear): linear_attention,
-linear_attention_bwd, linear_state_update.
+linear_attention_bwd, linear_state_update.  The norms before and after a block with its gate and
+residual scale (module block): block_norm, block_norm_bwd.
 """
 from __future__ import annotations
 
@@ -44,6 +45,8 @@ __all__ = [
     "GdnLinearDesc", "gdn_linear_attn_fwd", "gdn_linear_attn_workspace_size",
     "gdn_linear_attn_bwd", "gdn_linear_attn_bwd_workspace_size", "gdn_linear_state_update",
     "linear_attention", "linear_attention_bwd", "linear_state_update",
+    "GdnBlockNormDesc", "gdn_block_norm_fwd", "gdn_block_norm_bwd",
+    "gdn_block_norm_bwd_workspace_size", "block_norm", "block_norm_bwd",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
@@ -137,6 +140,7 @@ def load(path: str = LIB_PATH):
                                           P]
     ssm.declare(lib)
     linear.declare(lib)
+    block.declare(lib)
     _lib = lib
     return lib
 
@@ -643,3 +647,7 @@ from .linear import (  # noqa: E402
     GdnLinearDesc, gdn_linear_attn_bwd, gdn_linear_attn_bwd_workspace_size, gdn_linear_attn_fwd,
     gdn_linear_attn_workspace_size, gdn_linear_state_update, linear_attention,
     linear_attention_bwd, linear_state_update)
+from . import block  # noqa: E402
+from .block import (  # noqa: E402
+    GdnBlockNormDesc, block_norm, block_norm_bwd, gdn_block_norm_bwd,
+    gdn_block_norm_bwd_workspace_size, gdn_block_norm_fwd)

@@ -31,7 +31,8 @@ LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["api.cpp", "stages.hip", "fused.hip", "segment.hip", "recurrent.hip", "conv1d.hip",
            "noalloc.hip", "backward.hip", "api_ssm.cpp", "scan.hip",
            "scan_bwd.hip", "scan_step.hip", "conv1d_bwd.hip", "group_norm.hip", "api_linear.cpp",
-           "linear.hip", "linear_bwd.hip", "linear_step.hip"]
+           "linear.hip", "linear_bwd.hip", "linear_step.hip", "api_block_norm.cpp",
+           "block_norm.hip"]
 ARCH = "gfx950"
 
 

@@ -419,6 +419,56 @@ gdn_status gdn_group_norm_bwd(const gdn_norm_desc* d, const void* x, const float
                               const float* rstd, const void* dy, void* dx, float* dweight,
                               float* dbias, void* dgate, hipStream_t stream);
 
+/* The norms before and after a block with its gate and residual scale, one pass over the rows: what
+ * follows a block's output projection up to the next block's input.  For a row of the residual stream
+ * x, the block's output h and its gate (RMS norms),
+ *
+ *   n = h (E[h^2] + eps)^-1/2 post_weight            (n = h without post_norm)
+ *   z = n act(gate)                                  (z = n without a gate)
+ *   x_out = x + residual_scale scale z               (scale NULL: ones)
+ *   y = x_out (E[x_out^2] + eps)^-1/2 weight         (weight NULL: ones; y NULL: left out)
+ *
+ * x, x_out [rows, channels] residual_dtype; h, gate, y [rows, channels] dtype; h and gate rows
+ * *_stride elements apart (0 = one after another), the others contiguous; post_weight, scale, weight
+ * [channels] f32; post_rstd, rstd [rows] f32, the two norms' factors, written unless NULL (the
+ * backward needs them).  Statistics are fp32 and y comes from x_out before it is rounded.  x_out may be
+ * x's buffer.  h NULL: x_out is x and not written, y its norm; gate, post_weight, scale and post_norm
+ * belong to h, post_weight to post_norm.  dtype bf16 or f32; residual_dtype the same, or f32 with
+ * bf16.  Any channels up to 2^20, rows up to 2^30 (GDN_ERR_UNSUPPORTED beyond); pointers aligned to
+ * their element (vectors are used where rows start on them).  An infinity or a NaN stays in its row. */
+typedef struct gdn_block_norm_desc {
+  int32_t rows, channels;
+  int32_t dtype;           /* gdn_dtype of h, gate, y, dy, dh, dgate */
+  int32_t residual_dtype;  /* gdn_dtype of x, x_out, dx_out, dx      */
+  int32_t post_norm;       /* 0 or 1                                 */
+  int32_t activation;      /* gdn_activation of the gate             */
+  float eps;               /* >= 0                                   */
+  float residual_scale;
+  int64_t h_stride, gate_stride;
+  void* workspace;         /* backward: 256-byte aligned, as many bytes as the query gives */
+  size_t workspace_bytes;
+} gdn_block_norm_desc;
+
+gdn_status gdn_block_norm_fwd(const gdn_block_norm_desc* d, const void* x, const void* h,
+                              const void* gate, const float* post_weight, const float* scale,
+                              const float* weight, void* x_out, void* y, float* post_rstd,
+                              float* rstd, hipStream_t stream);
+
+/* Bytes of workspace gdn_block_norm_bwd needs.  Host-only. */
+size_t gdn_block_norm_bwd_workspace_size(const gdn_block_norm_desc* d, gdn_status* status);
+
+/* Its gradient, from the forward's inputs, its two factors and the gradients dx_out [rows, channels]
+ * residual_dtype (NULL: zero) and dy [rows, channels] dtype (NULL: y was left out) of its outputs, one
+ * of them at least: dx residual_dtype; dh (with h), dgate (with a gate) dtype; contiguous.
+ * dpost_weight, dscale, dweight [channels] f32 sums over the rows in a fixed order (NULL: not
+ * written). */
+gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc* d, const void* x, const void* h,
+                              const void* gate, const float* post_weight, const float* scale,
+                              const float* weight, const float* post_rstd, const float* rstd,
+                              const void* dx_out, const void* dy, void* dx, void* dh, void* dgate,
+                              float* dpost_weight, float* dscale, float* dweight,
+                              hipStream_t stream);
+
 /* Bytes of workspace the variant chosen by d->variant needs (for AUTO, what AUTO picks when
  * given that much).  The fused variant needs none on a dense batch; on a packed batch of
  * 2 .. 65536 sequences it asks for 4 bytes per sequence (256-byte aligned) to run them

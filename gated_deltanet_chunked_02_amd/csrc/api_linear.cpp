@@ -65,6 +65,12 @@ gdn_status check_linear(const gdn_linear_desc* d, bool packed, gdn::LinearProble
 // long sequence does not run alone.
 constexpr int kMinSegment = 128;
 
+int slots_of(const gdn::LinearProblem& p, bool packed) {
+  return p.N == 0 ? 0
+         : packed ? p.Ttot / p.Lc + p.N
+                  : p.N * (int)(p.T > p.Lc ? ((long long)p.T + p.Lc - 1) / p.Lc : 1);
+}
+
 void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
   p->Lc = gdn::kScanNoSplit;
   if (p->N > 0 && p->Ttot > 0) {
@@ -80,9 +86,7 @@ void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
     if (L < kMinSegment) L = kMinSegment;
     if (L < longest) p->Lc = (int)L;
   }
-  p->slots = p->N == 0 ? 0
-             : packed  ? p->Ttot / p->Lc + p->N
-                       : p->N * (int)(p->T > p->Lc ? ((long long)p->T + p->Lc - 1) / p->Lc : 1);
+  p->slots = slots_of(*p, packed);
 }
 
 int slabs_of(const gdn::LinearProblem& p) { return (p.Dv + gdn::kLinearSlab - 1) / gdn::kLinearSlab; }
@@ -91,7 +95,16 @@ constexpr int kFwdFill = 512;  // two workgroups a CU
 constexpr int kBwdFill = 256;  // one
 
 void plan_fwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, slabs_of(*p), kFwdFill); }
-void plan_bwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, 1, kBwdFill); }
+void plan_bwd(gdn::LinearProblem* p, bool packed) {
+  plan(p, packed, 1, kBwdFill);
+  // a segment holds whole spans between the states kept for the gradient, or is one
+  const int span = gdn::kLinearAnchor * gdn::linear_chunk(p->f32);
+  if (p->Lc != gdn::kScanNoSplit && p->Lc > span) {
+    p->Lc = (p->Lc + span - 1) / span * span;
+    if (p->Lc >= (packed ? p->Ttot : p->T)) p->Lc = gdn::kScanNoSplit;
+    p->slots = slots_of(*p, packed);
+  }
+}
 
 // A launch has fewer than 2^32 threads: segments' heads and slabs in workgroups of up to 512, the
 // composition's four values a thread, and the shared heads' sums.
@@ -115,7 +128,8 @@ FwdLayout fwd_layout(const gdn::LinearProblem& p) {
 }
 
 struct BwdLayout {
-  size_t states, sums, grads, chunks, part, dgp, total;
+  size_t states, sums, grads, anchors, a, part, dgp, total;
+  int every;
 };
 
 BwdLayout bwd_layout(const gdn::LinearProblem& p, bool packed) {
@@ -127,15 +141,19 @@ BwdLayout bwd_layout(const gdn::LinearProblem& p, bool packed) {
     return at;
   };
   const size_t heads = (size_t)p.slots * p.H;
+  // the states kept for the gradient: at every 8th chunk's end, or a shorter segment's
   const int C = gdn::linear_chunk(p.f32);
-  const size_t chunks = p.Ttot == 0 ? 0
-                        : packed    ? (size_t)p.Ttot / C + p.N
-                                    : (size_t)p.N * (((size_t)p.T + C - 1) / C);
+  L.every = p.Lc < gdn::kLinearAnchor * C ? p.Lc / C : gdn::kLinearAnchor;
+  const size_t span = (size_t)L.every * C;
+  const size_t anchors = p.Ttot == 0 ? 0
+                         : packed    ? (size_t)p.Ttot / span + p.N
+                                     : (size_t)p.N * (((size_t)p.T + span - 1) / span);
   const bool split = p.Lc != gdn::kScanNoSplit;
   L.states = take(split ? heads * p.Dk * p.Dv * 4 : 0);
   L.sums = take(split ? heads * 4 : 0);
   L.grads = take(split ? heads * p.Dk * p.Dv * 4 : 0);
-  L.chunks = take(chunks * p.H * gdn::linear_tile(p.Dk) * gdn::linear_tile(p.Dv) * 4);
+  L.anchors = take(anchors * p.H * gdn::linear_tile(p.Dk) * gdn::linear_tile(p.Dv) * 4);
+  L.a = take((size_t)p.Ttot * p.H * 4);
   L.part = take(p.H != p.Hg ? (size_t)p.Ttot * p.H * p.Dk * 8 : 0);
   L.dgp = take(p.head_decay ? heads * 4 : 0);
   L.total = o;
@@ -265,7 +283,9 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const vo
   b.dg = dg;
   b.dh0 = dh0;
   b.grads = at(L.grads);
-  b.chunks = at(L.chunks);
+  b.anchors = at(L.anchors);
+  b.a = at(L.a);
+  b.every = L.every;
   b.part = at(L.part);
   b.dgp = at(L.dgp);
   return gdn::launch_linear_bwd(p, b, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;

@@ -11,6 +11,7 @@ namespace gdn {
 constexpr int kLinearChunk = 64;     // tokens of a chunk in bf16
 constexpr int kLinearChunkF32 = 32;  // in fp32, whose tiles take twice the LDS
 constexpr int kLinearSlab = 128;     // value columns of a workgroup, at most
+constexpr int kLinearAnchor = 8;     // chunks from one state kept for the gradient to the next, at most
 
 // Segments are chunks of Lc tokens (a multiple of the tile chunk, or kScanNoSplit for whole
 // sequences) with the slots of ScanProblem (ssm.h); tile chunks have slots of the same form with the
@@ -37,18 +38,6 @@ struct LinearProblem {
 
 hipError_t launch_linear_fwd(const LinearProblem& p, hipStream_t st);
 
-// A pass over segments that makes states only: sums of x_t y_t^T.
-struct LinearPass {
-  const void* x;       // k, or q with reverse
-  const void* y;       // v, or dout
-  int64_t sx, sy;
-  bool reverse;        // from the segments' ends back
-  float* own;          // [slots, H, Dk, Dv] every segment's own sum
-  float* chunks;       // instead: every tile chunk's start state (LinearBwd::chunks)
-};
-hipError_t launch_linear_state(const LinearProblem& p, const LinearPass& a, hipStream_t st);
-hipError_t launch_linear_compose(const LinearProblem& p, hipStream_t st);
-
 struct LinearBwd {
   const void* dout;    // [B, T, H, Dv]
   const float* dht;    // [N, H, Dk, Dv] or null
@@ -58,10 +47,41 @@ struct LinearBwd {
   float* dg;           // [H] or [B, T, H], or null
   float* dh0;          // or null
   float* grads;        // workspace: [slots, H, Dk, Dv], as states but from the ends
-  float* chunks;       // workspace: the state at every tile chunk's start, in the kernels' tile order
+  float* anchors;      // workspace: the state at every `every`-th chunk's end, in the kernels' tile order
+  float* a;            // workspace: [Ttot, H] what q . dq takes from before the chunk
+  int every;
   float* part;         // workspace: [2, Ttot, H, Dk] dq and dk of every value head (shared q/k heads)
   float* dgp;          // workspace: [slots, H] sums of dg (head_decay)
 };
+
+// A pass over segments that makes states only: sums of x_t y_t^T.
+struct LinearPass {
+  const void* x;       // k, or q with reverse
+  const void* y;       // v, or dout
+  int64_t sx, sy;
+  bool reverse;        // from the segments' ends back
+  float* own;          // [slots, H, Dk, Dv] every segment's own sum
+};
+hipError_t launch_linear_state(const LinearProblem& p, const LinearPass& a, hipStream_t st);
+hipError_t launch_linear_compose(const LinearProblem& p, hipStream_t st);
+
+// The tensors of one pass of the recurrence: the forward's own, or those that make dq (linear.hip).
+// Heads: q and k rows have those of h / qrep, v (and x) rows those of h / vrep.
+struct LinearRun {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* x;
+  int64_t sq, sk, sv, sx;
+  int Dk, Dv, qrep, vrep;
+  void* out;           // [B, T, H, Dv]
+  float* a;
+  float* anchors;
+  int every;
+};
+// dq (or every value head's share of it), a and the anchors.
+hipError_t launch_linear_dq(const LinearProblem& p, const LinearBwd& b, hipStream_t st);
+
 // Tile sizes of the backward: 64 or 128 for head sizes up to that.
 inline int linear_tile(int D) { return D <= 64 ? 64 : 128; }
 inline int linear_chunk(bool f32) { return f32 ? kLinearChunkF32 : kLinearChunk; }

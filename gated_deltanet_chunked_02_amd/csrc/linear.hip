@@ -27,164 +27,267 @@ namespace gdn {
 
 namespace {
 
-template <typename E, int DK, int DV, int OCC>
-__global__ __launch_bounds__(DV * 4, OCC) void k_linear_fwd(LinearProblem p) {
+// GRAD: the same pass over other tensors makes dq.  With S^T as the state, whose rows run over the value
+// columns, dq_t = scale S_t dout_t is the recurrence with dout for q, v for k and k for v.  There the
+// state meets dout as three bf16 terms, because the sums q . dq that leave the chunk (a) are terms of dg,
+// an fp32 result; and the state is written out at every kLinearAnchor-th chunk's end for the other half
+// of the gradient.
+template <typename E, int DK, int DV, int NW, int OCC, bool GRAD, typename G>
+__global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, LinearRun r) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
-  constexpr int NTH = DV * 4, NW = DV / 16, KT = DK / 16, TT = C / 16, PAD = 16 / (int)sizeof(E);
-  constexpr int LK = DK + PAD, LV = DV + PAD, LP = C + PAD, KF = Mx<E>::KF, KS = C / KF;
-  constexpr int TERMS = Mx<E>::TERMS;
+  constexpr int NTH = NW * 64, CW = DV / 16 / NW, KT = DK / 16, TT = C / 16;
+  constexpr int KF = Mx<E>::KF, KS = C / KF, TERMS = Mx<E>::TERMS, EPL = Mx<E>::EPL;
+  constexpr int STEPS = sizeof(E) == 2 ? KT / 2 : KT, STERMS = GRAD ? TERMS : 1;
   typedef typename Mx<E>::frag frag;
-  __shared__ __align__(16) E Qs[C * LK];
-  __shared__ __align__(16) E Ks[C * LK];
-  __shared__ __align__(16) E Vs[C * LV];
-  __shared__ __align__(16) E Ps[C * LP];
+  typedef Tile<E, DK> TK;
+  typedef Tile<E, DV> TV;
+  typedef Tile<E, C> TP;
+  __shared__ __align__(256) E Qs[C * TK::LD];
+  __shared__ __align__(256) E Ks[C * TK::LD];
+  __shared__ __align__(256) E Vs[C * TV::LD];
+  __shared__ __align__(256) E Xs[GRAD ? C * TV::LD : 1];
+  __shared__ __align__(256) E Ps[C * TP::LD];
   __shared__ __align__(16) Decays<C> dec[2];
+  __shared__ float as[GRAD ? NW : 1][GRAD ? C : 1];
 
-  const int slabs = (p.Dv + DV - 1) / DV;
+  const int slabs = (r.Dv + DV - 1) / DV;
   const int unit = unit_of(blockIdx.x, gridDim.x, p.group);
   const int slab = unit % slabs, sh = unit / slabs, slot = sh / p.H, h = sh - slot * p.H;
   const Chunk c = uniform_chunk(p, slot);
   if (!c.ok) return;
-  const int l = lane_id(), wave = uniform(wave_id()), lc = l & 15, lg = l >> 4;
-  const int hk = h / (p.H / p.Hg), v0 = slab * DV, width = min(DV, p.Dv - v0);
-  const int col = v0 + 16 * wave + lc;  // this lane's state column
+  const int l = lane_id(), wave = uniform(wave_id());
+  const int v0 = slab * DV, width = min(DV, r.Dv - v0);
+  const int col0 = 16 * CW * wave;  // this wave's columns of the slab
   const long cell = (long)p.Dk * p.Dv;
 
-  f32x4 S[KT];
+  // The state in memory is [Dk, Dv]: this one's rows (GRAD: its columns) are the first axis.  Rows past
+  // the head lie past the buffer, or are sent there.
+  f32x4 S[CW][KT];
   const float* from = p.Lc != kScanNoSplit ? p.states + ((long)slot * p.H + h) * cell
                       : p.h0               ? p.h0 + ((long)c.n * p.H + h) * cell
                                            : nullptr;
+  const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
+  for (int w = 0; w < CW; ++w) {
+    const int col = col0 + 16 * w + (l & 15);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      S[t][i] = from && tile_row(t) + i < p.Dk && col < p.Dv
-                    ? from[(long)(tile_row(t) + i) * p.Dv + col] : 0.f;
+    for (int t = 0; t < KT; ++t) {
+      if constexpr (GRAD) {
+        S[w][t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            frs, col < width && tile_row(t, l) < r.Dk
+                     ? (uint32_t)(col * r.Dk + tile_row(t, l)) * 4 : kNoColumn, 0, 0));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          S[w][t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+              frs, col < width ? (uint32_t)((tile_row(t, l) + i) * r.Dv + v0 + col) * 4 : kNoColumn,
+              0, 0));
+      }
+    }
+  }
 
-  const E* qp = static_cast<const E*>(p.q) + c.t0 * p.sq + (long)hk * p.Dk;
-  const E* kp = static_cast<const E*>(p.k) + c.t0 * p.sk + (long)hk * p.Dk;
-  const E* vp = static_cast<const E*>(p.v) + c.t0 * p.sv + (long)h * p.Dv + v0;
-  const int64_t so = (int64_t)p.H * p.Dv;
-  E* op = static_cast<E*>(p.o) + c.t0 * so + (long)h * p.Dv + v0;
-  const uint32_t oat = 16 * wave + 4 * lg < width
-                           ? (uint32_t)((lc * so + 16 * wave + 4 * lg) * sizeof(E)) : kNoColumn;
-  const uint32_t ostep = 16 * wave + 4 * lg < width ? (uint32_t)(16 * so * sizeof(E)) : 0;
+  const E* qp = static_cast<const E*>(r.q) + c.t0 * r.sq + (long)(h / r.qrep) * r.Dk;
+  const E* kp = static_cast<const E*>(r.k) + c.t0 * r.sk + (long)(h / r.qrep) * r.Dk;
+  const E* vp = static_cast<const E*>(r.v) + c.t0 * r.sv + (long)(h / r.vrep) * r.Dv + v0;
+  const E* xp = static_cast<const E*>(r.x) + c.t0 * r.sx + (long)(h / r.vrep) * r.Dv + v0;
+  const int64_t so = (int64_t)p.H * r.Dv;
+  G* op = static_cast<G*>(r.out) + c.t0 * so + (long)h * r.Dv + v0;
 
   Rows<E, DK, C, NTH> q, k;
-  Rows<E, DV, C, NTH> v;
-  q.open(p.sq, p.Dk, LK);
-  k.open(p.sk, p.Dk, LK);
-  v.open(p.sv, width, LV);
+  Rows<E, DV, C, NTH> v, x;
   const int chunks = (c.len + C - 1) / C;
   float gnext = 0.f;
-  auto fetch = [&](int m) {
-    const int len = min(C, c.len - m * C);
-    q.load(qp + (long)m * C * p.sq, p.sq, p.Dk, len);
-    k.load(kp + (long)m * C * p.sk, p.sk, p.Dk, len);
-    v.load(vp + (long)m * C * p.sv, p.sv, width, len);
+  auto fetch = [&](int m, int tid) {
+    const int len = max(0, min(C, c.len - m * C));  // none past the last chunk
+    q.load(qp + (long)m * C * r.sq, r.sq, r.Dk, len, tid);
+    k.load(kp + (long)m * C * r.sk, r.sk, r.Dk, len, tid);
+    v.load(vp + (long)m * C * r.sv, r.sv, width, len, tid);
+    if constexpr (GRAD) x.load(xp + (long)m * C * r.sx, r.sx, width, len, tid);
+  };
+  auto decay_of = [&](int m) {
+    return load_decay(p, c.t0 + (long)m * C, max(0, min(C, c.len - m * C)), h);
   };
   if (chunks > 0) {
-    fetch(0);
-    if (wave == NW - 1) {
-      dec[0].make(load_decay(p, c.t0, l, min(C, c.len), h));
-      if (chunks > 1) gnext = load_decay(p, c.t0 + C, l, min(C, c.len - C), h);
-    }
+    fetch(0, threadIdx.x);
+    const float g = decay_of(0);
+    gnext = decay_of(1);
+    if (wave == NW - 1) dec[0].make(g);
     // scores above the diagonal's tiles are never written, and read where a product's k covers two
-    for (int i = threadIdx.x; i < C * LP; i += NTH) Ps[i] = (E)0.f;
+    for (int i = threadIdx.x; i < C * TP::LD; i += NTH) Ps[i] = (E)0.f;
   }
 
   for (int m = 0; m < chunks; ++m) {
     const int len = min(C, c.len - m * C);
     const Decays<C>& d = dec[m & 1];
-    q.store(Qs, LK);
-    k.store(Ks, LK);
-    v.store(Vs, LV);
+    int lo = l, tid = threadIdx.x;
+    opaque(lo);
+    opaque(tid);
+    const int lc = lo & 15, lg = lo >> 4;
+    q.store(Qs, tid);
+    k.store(Ks, tid);
+    v.store(Vs, tid);
+    if constexpr (GRAD) x.store(Xs, tid);
     __syncthreads();
-    if (m + 1 < chunks) fetch(m + 1);
+    // loads and stores of a chunk are the same in every wave and chunk, so that a wait for a load does
+    // not have to wait for later stores
+    fetch(m + 1, tid);
 
     // scores: the lower tiles, rows j of tile tj against columns i of tile ti
     for (int x = wave; x < TT * (TT + 1) / 2; x += NW) {
       const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-      if (16 * ti >= len) break;
       f32x4 a = zero4();
 #pragma unroll
       for (int s = 0; s < DK / KF; ++s)
-        a = Mx<E>::mma(mx_ld<E>(Ks, LK, 16 * tj, KF * s), mx_ld<E>(Qs, LK, 16 * ti, KF * s), a);
+        a = Mx<E>::mma(TK::ld(Ks, 16 * tj, KF * s, lo), TK::ld(Qs, 16 * ti, KF * s, lo), a);
       const int i = 16 * ti + lc, j = 16 * tj + 4 * lg;
       const double Gi = d.G[i];
-      E* to = Ps + i * LP + j;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x2 = a[e] * exp2_f32((float)(Gi - d.G[j + e]));
-        a[e] = j + e <= i ? x2 : 0.f;
+        a[e] = j + e <= i ? x2 * p.scale : 0.f;
       }
-      if constexpr (sizeof(E) == 2)
-        *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(a, bf16x4);
-      else
-        *reinterpret_cast<f32x4*>(to) = a;
+      put4<E, C>(Ps, i, j, a);
     }
-    if (wave == NW - 1 && m + 1 < chunks) {
-      dec[(m + 1) & 1].make(gnext);
-      if (m + 2 < chunks)
-        gnext = load_decay(p, c.t0 + (m + 2) * C, l, min(C, c.len - (m + 2) * C), h);
-    }
-    // the state's share
-    f32x4 acc[TT];
-    {
-      StateOperand<E, KT, 1> f;
-      f.from(S);
+    const float g = gnext;
+    gnext = decay_of(m + 2);
+    if (wave == NW - 1) dec[(m + 1) & 1].make(g);
+    // the state's share, a step's operands at a time
+    f32x4 acc[CW][TT];
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (16 * t < len) {
-          acc[t] = f.times(Qs, LK, 16 * t, zero4());
-          acc[t] *= d.into[16 * t + lc];
-        }
+    for (int w = 0; w < CW; ++w)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[w][t] = zero4();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      sched_fence();
+      frag f[CW][STERMS];
+#pragma unroll
+      for (int w = 0; w < CW; ++w) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e)
+          y[e] = sizeof(E) == 2 ? S[w][2 * s + e / 4][e % 4] : S[w][s][e % 4];
+        split<E, STERMS>(y, f[w]);
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const frag b = TK::ld_state(Qs, 16 * t, s, lo);
+#pragma unroll
+        for (int e = STERMS - 1; e >= 0; --e)
+#pragma unroll
+          for (int w = 0; w < CW; ++w) acc[w][t] = Mx<E>::mma(f[w][e], b, acc[w][t]);
+      }
+    }
+    sched_fence();
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float in = p.scale * d.into[16 * t + lc];
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < CW; ++w) {
+        acc[w][t] *= in;
+        if constexpr (GRAD) sum += dot4<E, DV>(Xs, 16 * t + lc, col0 + 16 * w + 4 * lg, acc[w][t]);
+      }
+      if constexpr (GRAD) {
+        sum = group_sum(sum);
+        if (lg == 0) as[wave][16 * t + lc] = sum;
+      }
     }
     __syncthreads();
 
-    frag vf[KS];
+    if constexpr (GRAD) {  // a_t, from every wave's columns in order
+      float sum = 0.f;
+      const int t = lo & (C - 1);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) vf[s] = mx_tr<E, false>(Vs, LV, KF * s, 16 * wave);
+      for (int w = 0; w < NW; ++w) sum += as[w][t];
+      const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(
+          r.a + (c.t0 + (long)m * C) * p.H + h, 0, ((len - 1) * p.H + 1) * 4, 0x00020000);
+      __builtin_amdgcn_raw_buffer_store_b32(
+          __float_as_uint(sum), ars, wave == 0 && lo < len ? (uint32_t)(t * p.H * 4) : kNoColumn, 0,
+          0);
+    }
+    frag vf[CW][KS];
+#pragma unroll
+    for (int w = 0; w < CW; ++w)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) vf[w][s] = TV::tr(Vs, KF * s, col0 + 16 * w, lo);
     const __amdgpu_buffer_rsrc_t ors = rows_of(op + (long)m * C * so, so, width, len);
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-      if (16 * t < len) {
+    for (int t = 0; t < TT; ++t) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-          if (KF * s < 16 * (t + 1))
-            acc[t] = Mx<E>::mma(vf[s], mx_ld<E>(Ps, LP, 16 * t, KF * s), acc[t]);
-        store4<E>(ors, oat + t * ostep, acc[t] * p.scale);
+      for (int s = 0; s < KS; ++s)
+        if (KF * s < 16 * (t + 1)) {
+          const frag b = TP::ld(Ps, 16 * t, KF * s, lo);
+#pragma unroll
+          for (int w = 0; w < CW; ++w) acc[w][t] = Mx<E>::mma(vf[w][s], b, acc[w][t]);
+        }
+#pragma unroll
+      for (int w = 0; w < CW; ++w) {
+        const int col = col0 + 16 * w + 4 * lg;
+        store4<G>(ors, col < width ? (uint32_t)((16 * t + lc) * (int)so + col) * (int)sizeof(G)
+                                   : kNoColumn, acc[w][t]);
       }
+    }
 
+    sched_fence();
     // the state: v times its decay as TERMS operands
     const float keep = d.into[C - 1];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) S[t] *= keep;
+    for (int w = 0; w < CW; ++w)
+#pragma unroll
+      for (int t = 0; t < KT; ++t) S[w][t] *= keep;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      float x[8];
+      sched_fence();
+      frag f[CW][TERMS];
 #pragma unroll
-      for (int e = 0; e < Mx<E>::EPL; ++e)
-        x[e] = (float)vf[s][e] * d.left[KF * s + Mx<E>::EPL * lg + e];
-      frag f[TERMS];
-      split<E>(x, f);
+      for (int w = 0; w < CW; ++w) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) x[e] = (float)vf[w][s][e] * d.left[KF * s + EPL * lg + e];
+        split<E>(x, f[w]);
+      }
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        const frag a = mx_tr<E, true>(Ks, LK, KF * s, tile_col(t));
+        if (t % 4 == 0) sched_fence();
+        const frag a = TK::tr_state(Ks, KF * s, t, lo);
 #pragma unroll
-        for (int e = TERMS - 1; e >= 0; --e) S[t] = Mx<E>::mma(a, f[e], S[t]);
+        for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+          for (int w = 0; w < CW; ++w) S[w][t] = Mx<E>::mma(a, f[w][e], S[w][t]);
+      }
+    }
+    if constexpr (GRAD) {
+      if ((m + 1) % r.every == 0 || m + 1 == chunks) {
+        float* to = r.anchors + ((long)anchor_of(p, c, m, r.every, C) * p.H + h) * (DK * DV) + 4 * lo;
+#pragma unroll
+        for (int w = 0; w < CW; ++w)
+#pragma unroll
+          for (int t = 0; t < KT; ++t)
+            *reinterpret_cast<f32x4*>(to + ((wave * CW + w) * KT + t) * 256) = S[w][t];
       }
     }
     __syncthreads();
   }
 
-  if (p.ht && c.i == c.count - 1 && col < p.Dv) {
-    float* to = p.ht + ((long)c.n * p.H + h) * cell + col;
+  if (!GRAD && p.ht && c.i == c.count - 1) {
+    const __amdgpu_buffer_rsrc_t trs = __builtin_amdgcn_make_buffer_rsrc(
+        p.ht + ((long)c.n * p.H + h) * cell, 0, (int)cell * 4, 0x00020000);
+    int lo = l;
+    opaque(lo);  // the addresses are made here, not kept from the loads
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int w = 0; w < CW; ++w) {
+      const int col = col0 + 16 * w + (lo & 15);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (tile_row(t) + i < p.Dk) to[(long)(tile_row(t) + i) * p.Dv] = S[t][i];
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          __builtin_amdgcn_raw_buffer_store_b32(
+              __float_as_uint(S[w][t][i]), trs,
+              col < width ? (uint32_t)((tile_row(t, lo) + i) * r.Dv + v0 + col) * 4 : kNoColumn, 0,
+              0);
+    }
   }
 }
 
@@ -218,19 +321,18 @@ __global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p) {
 
 // Sums of outer products x_t y_t^T over a segment, without its outputs: forward (x = k, y = v, decays
 // to the chunk's end), or in REV backward (x = q, y = dout, decays from the chunk's start, the last
-// chunk first: the gradients of states).  Wave w holds columns of x (rows of the state) as tiles over
-// y.  STORE: from the segment's start state on, every chunk's start state is written out in the
-// tiles' order; otherwise the segment's own sum alone, from zero, and its decay.
-template <typename E, int DK, int DV, bool REV, bool STORE>
-__global__ __launch_bounds__(DK < 128 ? DK * 4 : 512, 2) void k_linear_state(LinearProblem p,
-                                                                          LinearPass a) {
+// chunk first: the gradients of states), from zero, and the segment's decay.  Wave w holds columns of x
+// (rows of the state) as tiles over y.
+template <typename E, int DK, int DV, int NW, bool REV>
+__global__ __launch_bounds__(64 * NW, 2) void k_linear_state(LinearProblem p, LinearPass a) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
-  constexpr int NW = DK < 128 ? DK / 16 : 8, NTH = 64 * NW, TK = DK / 16 / NW, VT = DV / 16;
-  constexpr int PAD = 16 / (int)sizeof(E), LX = DK + PAD, LY = DV + PAD;
+  constexpr int NTH = 64 * NW, TK = DK / 16 / NW, VT = DV / 16;
   constexpr int KF = Mx<E>::KF, KS = C / KF, TERMS = Mx<E>::TERMS;
   typedef typename Mx<E>::frag frag;
-  __shared__ __align__(16) E Xs[C * LX];
-  __shared__ __align__(16) E Ys[C * LY];
+  typedef Tile<E, DK> TX;
+  typedef Tile<E, DV> TY;
+  __shared__ __align__(256) E Xs[C * TX::LD];
+  __shared__ __align__(256) E Ys[C * TY::LD];
   __shared__ __align__(16) Decays<C> dec[2];
 
   const int slabs = (p.Dv + DV - 1) / DV;
@@ -238,77 +340,52 @@ __global__ __launch_bounds__(DK < 128 ? DK * 4 : 512, 2) void k_linear_state(Lin
   const int slab = unit % slabs, sh = unit / slabs, slot = sh / p.H, h = sh - slot * p.H;
   const Chunk c = uniform_chunk(p, slot);
   // nothing comes after the last segment (before the first)
-  if (!c.ok || (!STORE && c.i == (REV ? 0 : c.count - 1))) return;
+  if (!c.ok || c.i == (REV ? 0 : c.count - 1)) return;
   const int l = lane_id(), wave = uniform(wave_id()), lc = l & 15, lg = l >> 4;
   const int hk = h / (p.H / p.Hg), v0 = slab * DV, width = min(DV, p.Dv - v0);
   const long cell = (long)p.Dk * p.Dv, at = ((long)slot * p.H + h) * cell;
 
   f32x4 S[TK][VT];
-  const float* from = !STORE                 ? nullptr
-                      : p.Lc != kScanNoSplit ? p.states + at
-                      : p.h0                 ? p.h0 + ((long)c.n * p.H + h) * cell
-                                             : nullptr;
 #pragma unroll
   for (int j = 0; j < TK; ++j)
 #pragma unroll
-    for (int t = 0; t < VT; ++t) {
-      const int row = 16 * (wave * TK + j) + lc, y = tile_row(t);
-      S[j][t] = from && row < p.Dk && y < width
-                    ? *reinterpret_cast<const f32x4*>(from + (long)row * p.Dv + v0 + y) : zero4();
-    }
+    for (int t = 0; t < VT; ++t) S[j][t] = zero4();
 
   const E* xp = static_cast<const E*>(a.x) + c.t0 * a.sx + (long)hk * p.Dk;
   const E* yp = static_cast<const E*>(a.y) + c.t0 * a.sy + (long)h * p.Dv + v0;
   Rows<E, DK, C, NTH> x;
   Rows<E, DV, C, NTH> y;
-  x.open(a.sx, p.Dk, LX);
-  y.open(a.sy, width, LY);
   const int chunks = (c.len + C - 1) / C;
   auto chunk_at = [&](int m) { return REV ? chunks - 1 - m : m; };
-  auto fetch = [&](int m) {
-    const int len = min(C, c.len - m * C);
-    x.load(xp + (long)m * C * a.sx, a.sx, p.Dk, len);
-    y.load(yp + (long)m * C * a.sy, a.sy, width, len);
+  auto fetch = [&](int m, int tid) {  // nothing past the last chunk
+    const int len = max(0, m < 0 ? 0 : min(C, c.len - m * C));
+    x.load(xp + (long)m * C * a.sx, a.sx, p.Dk, len, tid);
+    y.load(yp + (long)m * C * a.sy, a.sy, width, len, tid);
   };
   auto decay_of = [&](int m) {
-    return load_decay(p, c.t0 + m * C, l, min(C, c.len - m * C), h);
+    return load_decay(p, c.t0 + (long)m * C, max(0, m < 0 ? 0 : min(C, c.len - m * C)), h);
   };
   double sum = 0.0;
   float gnext = 0.f;
   if (chunks > 0) {
-    fetch(chunk_at(0));
-    if (wave == NW - 1) {
-      sum = dec[0].make(decay_of(chunk_at(0)));
-      if (chunks > 1) gnext = decay_of(chunk_at(1));
-    }
+    fetch(chunk_at(0), threadIdx.x);
+    const float g = decay_of(chunk_at(0));
+    gnext = decay_of(chunk_at(1));
+    if (wave == NW - 1) sum = dec[0].make(g);
   }
-  float* out = nullptr;
-  if constexpr (STORE) {
-    const ChunkMap map = {p.cu, p.T, p.Ttot, p.N, C};
-    const int first = uniform(p.cu ? chunk_first(map, c.n) : c.n * chunk_count(p.T, C));
-    out = a.chunks + ((long)(first + (c.t0 - c.bos) / C) * p.H + h) * (DK * DV);
-  }
-
   for (int m = 0; m < chunks; ++m) {
     const Decays<C>& d = dec[m & 1];
-    if constexpr (STORE) {
-      float* to = out + (long)m * p.H * (DK * DV) + 4 * l;
-#pragma unroll
-      for (int j = 0; j < TK; ++j)
-#pragma unroll
-        for (int t = 0; t < VT; ++t)
-          *reinterpret_cast<f32x4*>(to + ((wave * TK + j) * VT + t) * 256) = S[j][t];
-    }
-    x.store(Xs, LX);
-    y.store(Ys, LY);
+    int lo = l, tid = threadIdx.x;
+    opaque(lo);
+    opaque(tid);
+    const int lc = lo & 15, lg = lo >> 4;
+    x.store(Xs, tid);
+    y.store(Ys, tid);
     __syncthreads();
-    if (m + 1 < chunks) {
-      fetch(chunk_at(m + 1));
-      if (wave == NW - 1) {
-        sum += dec[(m + 1) & 1].make(gnext);
-        if (m + 2 < chunks) gnext = decay_of(chunk_at(m + 2));
-      }
-    }
+    fetch(chunk_at(m + 1), tid);
+    const float g = gnext;
+    gnext = decay_of(chunk_at(m + 2));
+    if (wave == NW - 1) sum += dec[(m + 1) & 1].make(g);
     const float keep = d.into[C - 1];
 #pragma unroll
     for (int j = 0; j < TK; ++j)
@@ -319,7 +396,7 @@ __global__ __launch_bounds__(DK < 128 ? DK * 4 : 512, 2) void k_linear_state(Lin
       frag f[TK][TERMS];
 #pragma unroll
       for (int j = 0; j < TK; ++j) {
-        const frag b = mx_tr<E, false>(Xs, LX, KF * s, 16 * (wave * TK + j));
+        const frag b = TX::tr(Xs, KF * s, 16 * (wave * TK + j), lo);
         float w[8];
 #pragma unroll
         for (int e = 0; e < Mx<E>::EPL; ++e) {
@@ -330,7 +407,7 @@ __global__ __launch_bounds__(DK < 128 ? DK * 4 : 512, 2) void k_linear_state(Lin
       }
 #pragma unroll
       for (int t = 0; t < VT; ++t) {
-        const frag r = mx_tr<E, true>(Ys, LY, KF * s, tile_col(t));
+        const frag r = TY::tr_state(Ys, KF * s, t, lo);
 #pragma unroll
         for (int j = 0; j < TK; ++j)
 #pragma unroll
@@ -339,39 +416,56 @@ __global__ __launch_bounds__(DK < 128 ? DK * 4 : 512, 2) void k_linear_state(Lin
     }
     __syncthreads();
   }
-  if constexpr (!STORE) {
 #pragma unroll
-    for (int j = 0; j < TK; ++j)
+  for (int j = 0; j < TK; ++j)
 #pragma unroll
-      for (int t = 0; t < VT; ++t) {
-        const int row = 16 * (wave * TK + j) + lc, y0 = tile_row(t);
-        if (row < p.Dk && y0 < width)
-          *reinterpret_cast<f32x4*>(a.own + at + (long)row * p.Dv + v0 + y0) = S[j][t];
-      }
-    if (slab == 0 && threadIdx.x == NTH - 1) p.sums[(long)slot * p.H + h] = (float)sum;
-  }
+    for (int t = 0; t < VT; ++t) {
+      const int row = 16 * (wave * TK + j) + lc, y0 = tile_row(t, l);
+      if (row < p.Dk && y0 < width)
+        *reinterpret_cast<f32x4*>(a.own + at + (long)row * p.Dv + v0 + y0) = S[j][t];
+    }
+  if (slab == 0 && threadIdx.x == NTH - 1) p.sums[(long)slot * p.H + h] = (float)sum;
 }
 
-template <typename E, int DK, int DV, int OCC>
-hipError_t launch_fwd(const LinearProblem& p, hipStream_t st) {
-  const int slabs = (p.Dv + DV - 1) / DV;
+template <typename E, int DK, int DV, int NW, int OCC>
+hipError_t launch_fwd(const LinearProblem& p, const LinearRun& r, hipStream_t st) {
+  const int slabs = (r.Dv + DV - 1) / DV;
   const int blocks = p.slots * p.H * slabs;
   LinearProblem q = p;
   q.group = group_of(p, slabs, blocks);
-  k_linear_fwd<E, DK, DV, OCC><<<blocks, DV * 4, 0, st>>>(q);
+  k_linear_fwd<E, DK, DV, NW, OCC, false, E><<<blocks, NW * 64, 0, st>>>(q, r);
   return hipGetLastError();
 }
 
 template <typename E>
-hipError_t launch_fwd_e(const LinearProblem& p, hipStream_t st) {
+hipError_t launch_fwd_e(const LinearProblem& p, const LinearRun& r, hipStream_t st) {
   if (p.Dv <= 64) {
-    if (p.Dk <= 64) return launch_fwd<E, 64, 64, 2>(p, st);
-    if (p.Dk <= 128) return launch_fwd<E, 128, 64, 2>(p, st);
-    return launch_fwd<E, 256, 64, 1>(p, st);
+    if (p.Dk <= 64) return launch_fwd<E, 64, 64, 4, 2>(p, r, st);
+    if (p.Dk <= 128) return launch_fwd<E, 128, 64, 4, 2>(p, r, st);
+    return launch_fwd<E, 256, 64, 4, 1>(p, r, st);
   }
-  if (p.Dk <= 64) return launch_fwd<E, 64, 128, 2>(p, st);
-  if (p.Dk <= 128) return launch_fwd<E, 128, 128, 4>(p, st);
-  return launch_fwd<E, 256, 128, 2>(p, st);
+  if (p.Dk <= 64) return launch_fwd<E, 64, 128, 4, 2>(p, r, st);
+  if (p.Dk <= 128) return launch_fwd<E, 128, 128, 8, 4>(p, r, st);
+  return launch_fwd<E, 256, 128, 8, 2>(p, r, st);
+}
+
+template <typename E, int DK, int DV>
+hipError_t launch_dq(const LinearProblem& p, const LinearRun& r, hipStream_t st) {
+  const int blocks = p.slots * p.H;
+  LinearProblem q = p;
+  q.group = group_of(p, 1, blocks);
+  constexpr int NW = DV / 16, OCC = DK == 128 && DV == 128 ? 4 : 2;
+  if (p.H != p.Hg)
+    k_linear_fwd<E, DK, DV, NW, OCC, true, float><<<blocks, NW * 64, 0, st>>>(q, r);
+  else
+    k_linear_fwd<E, DK, DV, NW, OCC, true, E><<<blocks, NW * 64, 0, st>>>(q, r);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_dq_e(const LinearProblem& p, const LinearRun& r, hipStream_t st) {
+  if (r.Dv <= 64) return r.Dk <= 64 ? launch_dq<E, 64, 64>(p, r, st) : launch_dq<E, 128, 64>(p, r, st);
+  return r.Dk <= 64 ? launch_dq<E, 64, 128>(p, r, st) : launch_dq<E, 128, 128>(p, r, st);
 }
 
 template <typename E, int DK, int DV>
@@ -380,15 +474,11 @@ hipError_t launch_state(const LinearProblem& p, const LinearPass& a, hipStream_t
   const int blocks = p.slots * p.H * slabs;
   LinearProblem q = p;
   q.group = group_of(p, slabs, blocks);
-  constexpr int NTH = DK < 128 ? DK * 4 : 512;
+  constexpr int NW = DK <= 64 ? 4 : 8;
   if (a.reverse)
-    k_linear_state<E, DK, DV, true, false><<<blocks, NTH, 0, st>>>(q, a);
-  else if (!a.chunks)
-    k_linear_state<E, DK, DV, false, false><<<blocks, NTH, 0, st>>>(q, a);
-  else if constexpr (DK <= 128)
-    k_linear_state<E, DK, DV, false, true><<<blocks, NTH, 0, st>>>(q, a);
+    k_linear_state<E, DK, DV, NW, true><<<blocks, NW * 64, 0, st>>>(q, a);
   else
-    return hipErrorInvalidValue;
+    k_linear_state<E, DK, DV, NW, false><<<blocks, NW * 64, 0, st>>>(q, a);
   return hipGetLastError();
 }
 
@@ -428,7 +518,40 @@ hipError_t launch_linear_fwd(const LinearProblem& p, hipStream_t st) {
     if (e == hipSuccess) e = launch_linear_compose(p, st);
     if (e != hipSuccess) return e;
   }
-  return p.f32 ? launch_fwd_e<float>(p, st) : launch_fwd_e<bf16>(p, st);
+  LinearRun r = {};
+  r.q = p.q;
+  r.k = p.k;
+  r.v = p.v;
+  r.sq = p.sq;
+  r.sk = p.sk;
+  r.sv = p.sv;
+  r.Dk = p.Dk;
+  r.Dv = p.Dv;
+  r.qrep = p.H / p.Hg;
+  r.vrep = 1;
+  r.out = p.o;
+  return p.f32 ? launch_fwd_e<float>(p, r, st) : launch_fwd_e<bf16>(p, r, st);
+}
+
+hipError_t launch_linear_dq(const LinearProblem& p, const LinearBwd& b, hipStream_t st) {
+  LinearRun r = {};
+  r.q = b.dout;
+  r.k = p.v;
+  r.v = p.k;
+  r.x = p.q;
+  r.sq = (int64_t)p.H * p.Dv;
+  r.sk = p.sv;
+  r.sv = p.sk;
+  r.sx = p.sq;
+  r.Dk = p.Dv;
+  r.Dv = p.Dk;
+  r.qrep = 1;
+  r.vrep = p.H / p.Hg;
+  r.out = p.H != p.Hg ? static_cast<void*>(b.part) : b.dq;
+  r.a = b.a;
+  r.anchors = b.anchors;
+  r.every = b.every;
+  return p.f32 ? launch_dq_e<float>(p, r, st) : launch_dq_e<bf16>(p, r, st);
 }
 
 }  // namespace gdn

@@ -13,16 +13,20 @@
 //   a_s = q_s . (scale e^{G_s} S dO_s),  b_s = k_s . (e^{G_C - G_s} dS v_s)
 //   r = rowsum(E) - colsum(E),  E = M * (Q K^T) below the diagonal
 //
-// Nothing here is a difference of sums that run over the sequence.  Within a chunk r does cancel, for
-// the pairs that lie on one side of t: both its sums are taken in fp64 of the same fp32 values, so what
-// is left is dg's own size however strong the decay at t.
+// Two passes over the tokens.  Forwards, dQ is the recurrence itself over other tensors
+// (k_linear_fwd with GRAD, which also leaves a); backwards, k_linear_bwd makes the rest with dS in
+// registers.  Neither has both states, so what passes through a chunk comes from <dS, S> at its end,
 //
-// Two passes over the tokens: k_linear_state writes the state at every chunk's start (fp32, in the
-// order of its tiles), then k_linear_bwd walks each segment's chunks from the last to the first with
-// dS in registers and makes everything else.  dS is held by key rows: a wave has 16 of them and all
-// value columns, so products over the value columns take it from registers; the one over key rows
-// (dV) takes a copy rounded to bf16 from LDS.  Rounded to bf16 are M, P and that copy, once each; the
-// products that make a, b and dS use three bf16 terms for what is not bf16 already.
+//   e^{G_C} <dS, S_start> = <dS, S_end> - sum b,    <dS, S>_start = <dS, S>_end + sum a - sum b,
+//
+// carried in fp64 from chunk to chunk and taken afresh every kLinearAnchor chunks, where the forward
+// pass leaves its state: a difference of sums over 512 tokens at most, each term good to fp32's last
+// bits, so dg keeps fp32's accuracy.  Within a chunk r cancels for the pairs on one side of t: both its
+// sums are taken in fp64 of the same fp32 values, so what is left has dg's own size.
+//
+// dS is held by key rows: a wave has 16 of them and all value columns, so the product over the value
+// columns (dK) takes it from registers as three bf16 terms (its b is a term of dg); the one over key rows
+// (dV) takes a copy rounded to bf16 from LDS.  Rounded to bf16 are that copy, M and P, once each.
 #include "linear_device.h"
 
 namespace gdn {
@@ -45,45 +49,56 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-template <typename E, int DK, int DV>
+template <bool FIRST, typename A, typename B> struct Pick { typedef A type; };
+template <typename A, typename B> struct Pick<false, A, B> { typedef B type; };
+
+// One workgroup walks a segment's chunks from the last to the first; a wave has 16 key rows of dS.
+template <typename E, int DK, int DV, bool SHARES>
 __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, LinearBwd b) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
   constexpr int NW = DK / 16, NTH = 64 * NW, VT = DV / 16, TT = C / 16;
-  constexpr int PAD = 16 / (int)sizeof(E), LK = DK + PAD, LV = DV + PAD, LP = C + PAD;
   constexpr int KF = Mx<E>::KF, KS = C / KF, TERMS = Mx<E>::TERMS, EPL = Mx<E>::EPL;
+  constexpr int STEPS = sizeof(E) == 2 ? VT / 2 : VT;
   typedef typename Mx<E>::frag frag;
-  __shared__ __align__(16) E Qs[C * LK];
-  __shared__ __align__(16) E Ks[C * LK];
-  __shared__ __align__(16) E Vs[C * LV];
-  __shared__ __align__(16) E Os[C * LV];   // dO
-  __shared__ __align__(16) E Ds[DK * LV];  // dS, rounded
-  __shared__ __align__(16) E Ps[C * LP];
-  __shared__ __align__(16) E Ms[C * LP];
+  typedef Tile<E, DK> TK;
+  typedef Tile<E, DV> TV;
+  typedef Tile<E, C> TP;
+  __shared__ __align__(256) E Qs[C * TK::LD];
+  __shared__ __align__(256) E Ks[C * TK::LD];
+  __shared__ __align__(256) E Vs[C * TV::LD];
+  __shared__ __align__(256) E Os[C * TV::LD];   // dO
+  __shared__ __align__(256) E Ds[DK * TV::LD];  // dS, rounded
+  __shared__ __align__(256) E Ps[C * TP::LD];
+  __shared__ __align__(256) E Ms[C * TP::LD];
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ double rows[TT][C];  // E summed over a tile's columns, by tile column
   __shared__ double cols[TT][C];  // and over its rows, by tile row
-  __shared__ float as[NW][C], bs[NW][C], cs[NW];
+  __shared__ float bs[NW][C], cs[2][NW];  // two anchors may follow each other
+  __shared__ double sums[C];  // of dg over the chunks (head_decay)
 
   const int unit = unit_of(blockIdx.x, gridDim.x, p.group);
   const int slot = unit / p.H, h = unit - slot * p.H;
-  const int l = lane_id(), wave = uniform(wave_id()), lc = l & 15, lg = l >> 4;
+  const int l = lane_id(), wave = uniform(wave_id());
   const Chunk c = uniform_chunk(p, slot);
   if (!c.ok) {
-    if (b.dg && p.head_decay && threadIdx.x == 0) b.dgp[unit] = 0.f;
+    if (p.head_decay && threadIdx.x == 0) b.dgp[unit] = 0.f;
     return;
   }
   const int hk = h / (p.H / p.Hg);
   const long cell = (long)p.Dk * p.Dv;
-  const int row = 16 * wave + lc;  // this lane's key row of the state
 
-  f32x4 dS[VT];
   const float* from = p.Lc != kScanNoSplit ? b.grads + (long)unit * cell
                       : b.dht              ? b.dht + ((long)c.n * p.H + h) * cell
                                            : nullptr;
+  // a state's rows through a buffer: this lane's, four columns at a time
+  const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
+  f32x4 dS[VT];
 #pragma unroll
   for (int t = 0; t < VT; ++t)
-    dS[t] = from && row < p.Dk && tile_row(t) < p.Dv
-                ? *reinterpret_cast<const f32x4*>(from + (long)row * p.Dv + tile_row(t)) : zero4();
+    dS[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+        frs, tile_row(t, l) < p.Dv
+                 ? (uint32_t)((16 * wave + (l & 15)) * p.Dv + tile_row(t, l)) * 4 : kNoColumn, 0, 0));
 
   const int64_t so = (int64_t)p.H * p.Dv;
   const E* qp = static_cast<const E*>(p.q) + c.t0 * p.sq + (long)hk * p.Dk;
@@ -91,81 +106,82 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   const E* vp = static_cast<const E*>(p.v) + c.t0 * p.sv + (long)h * p.Dv;
   const E* op = static_cast<const E*>(b.dout) + c.t0 * so + (long)h * p.Dv;
   E* dvp = static_cast<E*>(b.dv) + c.t0 * so + (long)h * p.Dv;
-  // shared q/k heads: every value head's share in fp32, added by k_linear_shares
-  const bool shares = p.H != p.Hg;
-  const int64_t sg = (int64_t)p.H * p.Dk;  // p.H = p.Hg rows, or shares of p.H heads
-  const long gat = c.t0 * sg + (long)h * p.Dk;
-  const bool mine = 16 * wave + 4 * lg < p.Dk;
+  // dk, or with shared q/k heads every value head's share of it in fp32 (added up by
+  // k_linear_shares): rows of H heads either way
+  typedef typename Pick<SHARES, float, E>::type G;
+  const int64_t sg = (int64_t)p.H * p.Dk;
+  G* gp = (SHARES ? reinterpret_cast<G*>(b.part) + (long)p.Ttot * sg : static_cast<G*>(b.dk)) +
+          c.t0 * sg + (long)h * p.Dk;
 
   Rows<E, DK, C, NTH> q, k;
   Rows<E, DV, C, NTH> v, o;
-  q.open(p.sq, p.Dk, LK);
-  k.open(p.sk, p.Dk, LK);
-  v.open(p.sv, p.Dv, LV);
-  o.open(so, p.Dv, LV);
   const int chunks = (c.len + C - 1) / C;
-  auto fetch = [&](int m) {
-    const int len = min(C, c.len - m * C);
-    q.load(qp + (long)m * C * p.sq, p.sq, p.Dk, len);
-    k.load(kp + (long)m * C * p.sk, p.sk, p.Dk, len);
-    v.load(vp + (long)m * C * p.sv, p.sv, p.Dv, len);
-    o.load(op + (long)m * C * so, so, p.Dv, len);
+  auto fetch = [&](int m, int tid) {  // nothing before the first chunk
+    const int len = m < 0 ? 0 : min(C, c.len - m * C);
+    q.load(qp + (long)m * C * p.sq, p.sq, p.Dk, len, tid);
+    k.load(kp + (long)m * C * p.sk, p.sk, p.Dk, len, tid);
+    v.load(vp + (long)m * C * p.sv, p.sv, p.Dv, len, tid);
+    o.load(op + (long)m * C * so, so, p.Dv, len, tid);
   };
   auto decay_of = [&](int m) {
-    return load_decay(p, c.t0 + m * C, l, min(C, c.len - m * C), h);
+    return load_decay(p, c.t0 + (long)m * C, m < 0 ? 0 : min(C, c.len - m * C), h);
   };
   float gnext = 0.f;
   if (chunks > 0) {
-    fetch(chunks - 1);
-    if (wave == NW - 1) {
-      dec[(chunks - 1) & 1].make(decay_of(chunks - 1));
-      if (chunks > 1) gnext = decay_of(chunks - 2);
-    }
-    // scores above the diagonal's tiles, and of the last chunk's rows past its end, stay zero
-    for (int i = threadIdx.x; i < C * LP; i += NTH) Ps[i] = (E)0.f, Ms[i] = (E)0.f;
+    fetch(chunks - 1, threadIdx.x);
+    const float g = decay_of(chunks - 1);
+    gnext = decay_of(chunks - 2);
+    if (wave == NW - 1) dec[(chunks - 1) & 1].make(g);
+    // scores above the diagonal's tiles stay zero
+    for (int i = threadIdx.x; i < C * TP::LD; i += NTH) Ps[i] = (E)0.f, Ms[i] = (E)0.f;
   }
-  const ChunkMap map = {p.cu, p.T, p.Ttot, p.N, C};
-  const int first = uniform(p.cu ? chunk_first(map, c.n) : c.n * chunk_count(p.T, C));
-  const float* states = b.chunks + ((long)(first + (c.t0 - c.bos) / C) * p.H + h) * (DK * DV) +
-                        wave * (DV * 16) + 4 * l;
-  double gsum = 0.0;
+  if (wave == 0 && l < C) sums[l] = 0.0;  // this wave alone uses them
+  double pass = 0.0;  // <dS, S> at the chunk's end (wave 0)
 
   for (int m = chunks - 1; m >= 0; --m) {
     const int len = min(C, c.len - m * C);
     const Decays<C>& d = dec[m & 1];
-    q.store(Qs, LK);
-    k.store(Ks, LK);
-    v.store(Vs, LV);
-    o.store(Os, LV);
+    int lo = l, tid = threadIdx.x;
+    opaque(lo);
+    opaque(tid);
+    const int lc = lo & 15, lg = lo >> 4;
+    const bool anchor = (m + 1) % b.every == 0 || m == chunks - 1;
+    if (anchor) {
+      const float* at = b.anchors + ((long)anchor_of(p, c, m, b.every, C) * p.H + h) * (DK * DV) +
+                        wave * (DV * 16) + 4 * lo;
+      float x = 0.f;
 #pragma unroll
-    for (int t = 0; t < VT; t += 2) {
-      E* to = Ds + row * LV + tile_row(t);
-      if constexpr (sizeof(E) == 2) {
-        const bf16x4 x = __builtin_convertvector(dS[t], bf16x4),
-                     y = __builtin_convertvector(dS[t + 1], bf16x4);
-        *reinterpret_cast<bf16x8*>(to) = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-      } else {
-        *reinterpret_cast<f32x4*>(to) = dS[t];
-        *reinterpret_cast<f32x4*>(to + 4) = dS[t + 1];
+      for (int t = 0; t < VT; ++t) {
+        const f32x4 S = *reinterpret_cast<const f32x4*>(at + t * 256);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x = fmaf(S[e], dS[t][e], x);
       }
+      x = group_sum(row_sum(x));
+      if (lo == 0) cs[m & 1][wave] = x;
     }
-    __syncthreads();
-    if (m > 0) fetch(m - 1);
-    f32x4 S[VT];
+    q.store(Qs, tid);
+    k.store(Ks, tid);
+    v.store(Vs, tid);
+    o.store(Os, tid);
 #pragma unroll
-    for (int t = 0; t < VT; ++t)
-      S[t] = *reinterpret_cast<const f32x4*>(states + (long)m * p.H * (DK * DV) + t * 256);
+    for (int t = 0; t < VT; ++t) put4<E, DV>(Ds, 16 * wave + lc, tile_row(t, lo), dS[t]);
+    __syncthreads();
+    // a of this chunk, for its last step
+    const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(
+        b.a + (c.t0 + (long)m * C) * p.H + h, 0, ((len - 1) * p.H + 1) * 4, 0x00020000);
+    const float a = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        ars, lo < len ? (uint32_t)(lo * p.H * 4) : kNoColumn, 0, 0));
+    fetch(m - 1, tid);
 
     for (int x = wave; x < TT * (TT + 1) / 2; x += NW) {
       const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-      if (16 * ti >= len) break;
       f32x4 qk = zero4(), ov = zero4();
 #pragma unroll
       for (int s = 0; s < DK / KF; ++s)
-        qk = Mx<E>::mma(mx_ld<E>(Ks, LK, 16 * tj, KF * s), mx_ld<E>(Qs, LK, 16 * ti, KF * s), qk);
+        qk = Mx<E>::mma(TK::ld(Ks, 16 * tj, KF * s, lo), TK::ld(Qs, 16 * ti, KF * s, lo), qk);
 #pragma unroll
       for (int s = 0; s < DV / KF; ++s)
-        ov = Mx<E>::mma(mx_ld<E>(Vs, LV, 16 * tj, KF * s), mx_ld<E>(Os, LV, 16 * ti, KF * s), ov);
+        ov = Mx<E>::mma(TV::ld(Vs, 16 * tj, KF * s, lo), TV::ld(Os, 16 * ti, KF * s, lo), ov);
       const int i = 16 * ti + lc, j = 16 * tj + 4 * lg;
       const double Gi = d.G[i];
       f32x4 pp, mm, ee;
@@ -176,184 +192,166 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
         mm[e] = j + e <= i ? ov[e] * w : 0.f;
         ee[e] = j + e < i ? mm[e] * qk[e] : 0.f;
       }
-      E *tp = Ps + i * LP + j, *tm = Ms + i * LP + j;
-      if constexpr (sizeof(E) == 2) {
-        *reinterpret_cast<bf16x4*>(tp) = __builtin_convertvector(pp, bf16x4);
-        *reinterpret_cast<bf16x4*>(tm) = __builtin_convertvector(mm, bf16x4);
-      } else {
-        *reinterpret_cast<f32x4*>(tp) = pp;
-        *reinterpret_cast<f32x4*>(tm) = mm;
-      }
-      if (b.dg) {
-        double r = ((double)ee[0] + ee[1]) + ((double)ee[2] + ee[3]);
-        r += __shfl_xor(r, 16);
-        r += __shfl_xor(r, 32);
-        if (lg == 0) rows[tj][i] = r;
+      put4<E, C>(Ps, i, j, pp);
+      put4<E, C>(Ms, i, j, mm);
+      double r = ((double)ee[0] + ee[1]) + ((double)ee[2] + ee[3]);
+      r += __shfl_xor(r, 16);
+      r += __shfl_xor(r, 32);
+      if (lg == 0) rows[tj][i] = r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const double s = row_sum((double)ee[e]);
-          if (lc == 0) cols[ti][j + e] = s;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const double s = row_sum((double)ee[e]);
+        if (lc == 0) cols[ti][j + e] = s;
       }
     }
-    if (wave == NW - 1 && m > 0) {
-      dec[(m - 1) & 1].make(gnext);
-      if (m > 1) gnext = decay_of(m - 2);
+    const float g = gnext;
+    gnext = decay_of(m - 2);
+    if (wave == NW - 1) dec[(m - 1) & 1].make(g);
+    // dK from dS and V, a step's operands at a time
+    f32x4 acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = zero4();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      sched_fence();
+      frag f[TERMS];
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) x[e] = sizeof(E) == 2 ? dS[2 * s + e / 4][e % 4] : dS[s][e % 4];
+      split<E>(x, f);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const frag y = TV::ld_state(Vs, 16 * t, s, lo);
+#pragma unroll
+        for (int e = TERMS - 1; e >= 0; --e) acc[t] = Mx<E>::mma(f[e], y, acc[t]);
+      }
+    }
+    sched_fence();
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      acc[t] *= d.left[16 * t + lc];
+      const float r = group_sum(dot4<E, DK>(Ks, 16 * t + lc, 16 * wave + 4 * lg, acc[t]));
+      if (lg == 0) bs[wave][16 * t + lc] = r;
     }
     __syncthreads();
 
     const float keep = d.into[C - 1];
-    if (b.dg) {
-      float x = 0.f;
+    frag own[KS];  // Q transposed: this wave's 16 columns
 #pragma unroll
-      for (int t = 0; t < VT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x = fmaf(S[t][e], dS[t][e], x);
-      x = row_sum(x);
-      x = group_sum(x);
-      if (l == 0) cs[wave] = x;
-    }
-    const int n = (len + 15) / 16;
-    const long at = gat + (long)m * C * sg;
-    auto put = [&](int which, void* to, int t, f32x4 x) {
-      if (shares) {
-        const auto rs = rows_of(b.part + (which ? (long)p.Ttot * sg : 0) + at, sg, p.Dk, len);
-        store4<float>(rs, mine ? (uint32_t)((16 * t + lc) * sg + 16 * wave + 4 * lg) * 4 : kNoColumn,
-                      x);
-      } else {
-        const auto rs = rows_of(static_cast<E*>(to) + at, sg, p.Dk, len);
-        store4<E>(rs, mine ? (uint32_t)((16 * t + lc) * sg + 16 * wave + 4 * lg) * (int)sizeof(E)
-                           : kNoColumn, x);
-      }
-    };
-    // dQ
+    for (int s = 0; s < KS; ++s) own[s] = TK::tr(Qs, KF * s, 16 * wave, lo);
     {
-      StateOperand<E, VT, TERMS> f;
-      f.from(S);
-      frag kf[KS];
+      const __amdgpu_buffer_rsrc_t rs = rows_of(gp + (long)m * C * sg, sg, p.Dk, len);
+      const int col = 16 * wave + 4 * lg;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) kf[s] = mx_tr<E, false>(Ks, LK, KF * s, 16 * wave);
+      for (int t = 0; t < TT; ++t) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (t < n) {
-          f32x4 x = f.times(Os, LV, 16 * t, zero4());
-          x *= p.scale * d.into[16 * t + lc];
-          if (b.dg) {
-            float r = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              r = fmaf(x[e], (float)Qs[(16 * t + lc) * LK + 16 * wave + 4 * lg + e], r);
-            r = group_sum(r);
-            if (lg == 0) as[wave][16 * t + lc] = r;
-          }
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-            if (KF * s < 16 * (t + 1))
-              x = Mx<E>::mma(kf[s], mx_ld<E>(Ms, LP, 16 * t, KF * s), x);
-          put(0, b.dq, t, x);
-        }
-    }
-    // dK, and dS for the chunk before
-    {
-      StateOperand<E, VT, TERMS> f;
-      f.from(dS);
-      frag qf[KS];
-#pragma unroll
-      for (int s = 0; s < KS; ++s) qf[s] = mx_tr<E, false>(Qs, LK, KF * s, 16 * wave);
-#pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (t < n) {
-          f32x4 x = f.times(Vs, LV, 16 * t, zero4());
-          x *= d.left[16 * t + lc];
-          if (b.dg) {
-            float r = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              r = fmaf(x[e], (float)Ks[(16 * t + lc) * LK + 16 * wave + 4 * lg + e], r);
-            r = group_sum(r);
-            if (lg == 0) bs[wave][16 * t + lc] = r;
-          }
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-            if (KF * (s + 1) > 16 * t)
-              x = Mx<E>::mma(qf[s], mx_tr<E, false>(Ms, LP, KF * s, 16 * t), x);
-          put(1, b.dk, t, x);
-        }
-#pragma unroll
-      for (int t = 0; t < VT; ++t) dS[t] *= keep;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < EPL; ++e)
-          w[e] = (float)qf[s][e] * (p.scale * d.into[KF * s + EPL * lg + e]);
-        frag x[TERMS];
-        split<E>(w, x);
-#pragma unroll
-        for (int t = 0; t < VT; ++t) {
-          const frag r = mx_tr<E, true>(Os, LV, KF * s, tile_col(t));
-#pragma unroll
-          for (int e = TERMS - 1; e >= 0; --e) dS[t] = Mx<E>::mma(r, x[e], dS[t]);
-        }
+        for (int s = 0; s < KS; ++s)
+          if (KF * (s + 1) > 16 * t)
+            acc[t] = Mx<E>::mma(own[s], TP::tr(Ms, KF * s, 16 * t, lo), acc[t]);
+        store4<G>(rs, col < p.Dk ? (uint32_t)((16 * t + lc) * (int)sg + col) * (int)sizeof(G)
+                                 : kNoColumn, acc[t]);
       }
     }
     // dV
-    for (int vt = wave; vt < VT; vt += NW) {
-      frag of[KS], sf[DK / KF];
+    const __amdgpu_buffer_rsrc_t rs = rows_of(dvp + (long)m * C * so, so, p.Dv, len);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) of[s] = mx_tr<E, false>(Os, LV, KF * s, 16 * vt);
+    for (int w = 0; w < (VT + NW - 1) / NW; ++w) {
+      const int vt = wave + w * NW;
+      if (VT % NW != 0 && vt >= VT) break;
 #pragma unroll
-      for (int s = 0; s < DK / KF; ++s) sf[s] = mx_tr<E, false>(Ds, LV, KF * s, 16 * vt);
-      const auto rs = rows_of(dvp + (long)m * C * so, so, p.Dv, len);
+      for (int t = 0; t < TT; ++t) acc[t] = zero4();
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (t < n) {
-          f32x4 x = zero4();
+      for (int s = 0; s < DK / KF; ++s) {
+        sched_fence();
+        const frag sf = TV::tr(Ds, KF * s, 16 * vt, lo);
 #pragma unroll
-          for (int s = 0; s < DK / KF; ++s)
-            x = Mx<E>::mma(sf[s], mx_ld<E>(Ks, LK, 16 * t, KF * s), x);
-          x *= d.left[16 * t + lc];
+        for (int t = 0; t < TT; ++t)
+          acc[t] = Mx<E>::mma(sf, TK::ld(Ks, 16 * t, KF * s, lo), acc[t]);
+      }
+      frag of[KS];
 #pragma unroll
-          for (int s = 0; s < KS; ++s)
-            if (KF * (s + 1) > 16 * t)
-              x = Mx<E>::mma(of[s], mx_tr<E, false>(Ps, LP, KF * s, 16 * t), x);
-          store4<E>(rs, 16 * vt + 4 * lg < p.Dv
-                            ? (uint32_t)((16 * t + lc) * so + 16 * vt + 4 * lg) * (int)sizeof(E)
-                            : kNoColumn, x);
-        }
+      for (int s = 0; s < KS; ++s) of[s] = TV::tr(Os, KF * s, 16 * vt, lo);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        acc[t] *= d.left[16 * t + lc];
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          if (KF * (s + 1) > 16 * t)
+            acc[t] = Mx<E>::mma(of[s], TP::tr(Ps, KF * s, 16 * t, lo), acc[t]);
+        const int col = 16 * vt + 4 * lg;
+        store4<E>(rs, col < p.Dv ? (uint32_t)((16 * t + lc) * (int)so + col) * (int)sizeof(E)
+                                 : kNoColumn, acc[t]);
+      }
+    }
+    // dS for the chunk before
+#pragma unroll
+    for (int t = 0; t < VT; ++t) dS[t] *= keep;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      sched_fence();
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)
+        w[e] = (float)own[s][e] * (p.scale * d.into[KF * s + EPL * lg + e]);
+      frag f[TERMS];
+      split<E>(w, f);
+#pragma unroll
+      for (int t = 0; t < VT; ++t) {
+        if (t % 4 == 0) sched_fence();
+        const frag r = TV::tr_state(Os, KF * s, t, lo);
+#pragma unroll
+        for (int e = TERMS - 1; e >= 0; --e) dS[t] = Mx<E>::mma(r, f[e], dS[t]);
+      }
     }
     __syncthreads();
-    // the others go on to the next chunk, which writes none of these before its second barrier
-    if (b.dg && wave == 0) {
-      double up = 0.0, down = 0.0, through = 0.0;
-      if (l < len) {
-        for (int t = 0; t <= l / 16; ++t) up += rows[t][l];
-        for (int t = l / 16; t < n; ++t) up -= cols[t][l];
-        for (int w = 0; w < NW; ++w) up += as[w][l], down += bs[w][l];
+    // the others go on to the next chunk, whose first barrier comes before its first write of any of these (but cs's other half)
+    if (wave == 0) {
+      double up = a, down = 0.0, in = 0.0;
+      const int t = min(lo, C - 1);
+      for (int x = 0; x < TT; ++x) {
+        if (x <= t / 16) in += rows[x][t];
+        if (x >= t / 16) in -= cols[x][t];
       }
-      for (int w = 0; w < NW; ++w) through += cs[w];
-      const double from0 = wave_incl_scan(up), before = wave_incl_scan(down) - down;
-      double x = (last_lane(from0) - from0 + up) + before + keep * through;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) down += bs[w][t];
+      if (anchor) {
+        pass = 0.0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) pass += cs[m & 1][w];
+      }
+      up = lo < len ? up : 0.0;
+      down = lo < len ? down : 0.0;
+      in = lo < len ? in : 0.0;
+      const double suffix = wave_incl_scan(up + in), prefix = wave_incl_scan(down);
+      const double all = last_lane(prefix);
+      double x = (last_lane(suffix) - suffix + up + in) + (prefix - down) + (pass - all);
+      pass += last_lane(wave_incl_scan(up)) - all;
       // nothing passes a decay that is 0 in fp32
-      if (l < len && d.G[l] - (l > 0 ? d.G[l - 1] : 0.0) < -150.0) x = 0.0;
-      if (l < len) {
+      if (d.G[t] - (t > 0 ? d.G[t - 1] : 0.0) < -150.0) x = 0.0;
+      if (lo < len) {
         if (p.head_decay)
-          gsum += x;
-        else
-          b.dg[(long)(c.t0 + m * C + l) * p.H + h] = (float)x;
+          sums[lo] += x;
+        else if (b.dg)
+          b.dg[(c.t0 + (long)m * C + lo) * p.H + h] = (float)x;
       }
     }
   }
 
-  if (b.dg && p.head_decay && wave == 0) {
-    const double x = wave_incl_scan(gsum);
+  if (p.head_decay && wave == 0) {
+    const double x = wave_incl_scan(l < C ? sums[l] : 0.0);
     if (l == 63) b.dgp[unit] = (float)x;
   }
-  if (b.dh0 && c.i == 0 && row < p.Dk) {
-    float* to = b.dh0 + ((long)c.n * p.H + h) * cell + (long)row * p.Dv;
+  if (b.dh0 && c.i == 0) {
+    const __amdgpu_buffer_rsrc_t trs = __builtin_amdgcn_make_buffer_rsrc(
+        b.dh0 + ((long)c.n * p.H + h) * cell, 0, (int)cell * 4, 0x00020000);
+    int lo = l;
+    opaque(lo);  // addresses are made here, not kept from the loads
 #pragma unroll
     for (int t = 0; t < VT; ++t)
-      if (tile_row(t) < p.Dv) *reinterpret_cast<f32x4*>(to + tile_row(t)) = dS[t];
+      __builtin_amdgcn_raw_buffer_store_b128(
+          __builtin_bit_cast(u32x4, dS[t]), trs,
+          tile_row(t, lo) < p.Dv ? (uint32_t)((16 * wave + (lo & 15)) * p.Dv + tile_row(t, lo)) * 4
+                                 : kNoColumn, 0, 0);
   }
 }
 
@@ -416,7 +414,10 @@ hipError_t launch_grads(const LinearProblem& p, const LinearBwd& b, hipStream_t 
   const int blocks = p.slots * p.H;
   LinearProblem q = p;
   q.group = group_of(p, 1, blocks);
-  k_linear_bwd<E, DK, DV><<<blocks, DK * 4, 0, st>>>(q, b);
+  if (p.H != p.Hg)
+    k_linear_bwd<E, DK, DV, true><<<blocks, DK * 4, 0, st>>>(q, b);
+  else
+    k_linear_bwd<E, DK, DV, false><<<blocks, DK * 4, 0, st>>>(q, b);
   return hipGetLastError();
 }
 
@@ -461,9 +462,7 @@ hipError_t launch_linear_bwd(const LinearProblem& p, const LinearBwd& b, hipStre
       k_linear_compose_bwd<<<(unsigned)blocks, 256, 0, st>>>(p, b);
       e = hipGetLastError();
     }
-    a.own = nullptr;
-    a.chunks = b.chunks;
-    if (e == hipSuccess && p.Ttot > 0) e = launch_linear_state(p, a, st);
+    if (e == hipSuccess && p.Ttot > 0) e = launch_linear_dq(p, b, st);
     if (e == hipSuccess)
       e = p.f32 ? launch_grads_e<float>(p, b, st) : launch_grads_e<bf16>(p, b, st);
     if (e == hipSuccess && p.H != p.Hg && p.Ttot > 0)

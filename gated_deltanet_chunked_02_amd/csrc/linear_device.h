@@ -18,6 +18,7 @@ namespace gdn {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Products of 16-byte fragments: 32 k of bf16 in one instruction, 16 k of fp32 in four.  Lane
 // group g holds k = k0 + EPL g .. + EPL - 1 of row (or column) lane % 16.
@@ -39,50 +40,97 @@ template <> struct Mx<float> {
   }
 };
 
-// Row (or column) r = lane % 16 of a k-contiguous LDS matrix.
-template <typename E>
-__device__ __forceinline__ typename Mx<E>::frag mx_ld(const E* m, int ld, int row0, int k0) {
-  const int l = lane_id();
-  return *reinterpret_cast<const typename Mx<E>::frag*>(m + (row0 + (l & 15)) * ld + k0 +
-                                                       Mx<E>::EPL * (l >> 4));
-}
+// A tile of rows in LDS, D values each.  In bf16 a row has no padding and its 16-byte pieces are
+// exchanged by the row (piece j lies at j ^ turn(row)), so that no two of the lanes that one cycle
+// serves meet in a bank: not the 8 rows of a row fragment's cycle, nor the 4 rows x 4 pieces of a
+// transposing read's.  fp32 rows, read transposed one value at a time, are padded by 16 bytes.
+// l: the lane, or the lane made opaque in a loop, so that addresses are made where they are used and
+// not kept in registers throughout.
+template <typename E, int D>
+struct Tile {
+  static constexpr int LD = sizeof(E) == 2 ? D : D + 4;
+  static __device__ __forceinline__ int turn(int row) {
+    if constexpr (sizeof(E) == 4) return 0;
+    if constexpr (D == 64) return (row >> 1 & 1) * 4 + (row >> 2 & 3);
+    return (row & 3) * 4 + (row >> 2 & 3);
+  }
+  // Element offset of piece j (16 bytes) of a row.
+  static __device__ __forceinline__ int piece(int row, int j) {
+    return row * LD + (j ^ turn(row)) * (16 / (int)sizeof(E));
+  }
+  // Rows row0 + lane % 16, k from k0 on (row0 a multiple of 16, k0 of KF).
+  static __device__ __forceinline__ typename Mx<E>::frag ld(const E* m, int row0, int k0, int l) {
+    const int c = l & 15, g = l >> 4;
+    return *reinterpret_cast<const typename Mx<E>::frag*>(
+        m + row0 * LD + c * LD + ((k0 / Mx<E>::EPL) ^ (g ^ turn(c))) * Mx<E>::EPL);
+  }
+  // The same rows of a product over a state's rows, step s of it: the tiles 2 s and 2 s + 1 in bf16, tile
+  // s in fp32.
+  static __device__ __forceinline__ typename Mx<E>::frag ld_state(const E* m, int row0, int s,
+                                                                        int l) {
+    if constexpr (sizeof(E) == 2) return ld(m, row0, 32 * s, l);
+    return *reinterpret_cast<const typename Mx<E>::frag*>(
+        m + (row0 + (l & 15)) * LD + 32 * (s >> 1) + 4 * (s & 1) + 8 * (l >> 4));
+  }
+  // Transposed: rows k0 .. of the tile run along k, and lane % 16 counts columns from n0 on.
+  static __device__ __forceinline__ typename Mx<E>::frag tr(const E* m, int k0, int n0, int l) {
+    const int c = l & 15, g = l >> 4;
+    if constexpr (sizeof(E) == 2) {
+      const int row = 8 * g + (c >> 2);
+      const int j = (n0 / 8) ^ ((c >> 1 & 1) ^ turn(row));
+      return pair(m + k0 * LD + row * LD + 4 * (c & 1), j);
+    } else {
+      return column(m + (k0 + 4 * g) * LD + n0 + c);
+    }
+  }
+  // Transposed, the columns that state tile t has as rows.
+  static __device__ __forceinline__ typename Mx<E>::frag tr_state(const E* m, int k0, int t, int l) {
+    const int c = l & 15, g = l >> 4;
+    if constexpr (sizeof(E) == 2) {
+      const int row = 8 * g + (c >> 2);
+      const int j = (4 * (t >> 1)) ^ ((c & 3) ^ turn(row));
+      return pair(m + k0 * LD + row * LD + 4 * (t & 1), j);
+    } else {
+      return column(m + (k0 + 4 * g) * LD + 32 * (t >> 1) + 4 * (t & 1) + 8 * (c >> 2) + (c & 3));
+    }
+  }
 
-// The same fragment of a matrix stored [k][n]: column n0 + lane % 16, or with PERM the row of a
-// state tile (tile t of pair P, n0 = 32 P + 4 t).
-template <typename E, bool PERM>
-__device__ __forceinline__ typename Mx<E>::frag mx_tr(const E* m, int ld, int k0, int n0) {
-  const int l = lane_id(), c = l & 15, g = l >> 4;
-  if constexpr (sizeof(E) == 2) {
-    const E* p = m + (k0 + 8 * g + (c >> 2)) * ld + n0 + (PERM ? 8 : 4) * (c & 3);
-    const bf16x4 a = read_tr4(p), b = read_tr4(p + 4 * ld);
+ private:
+  // turn(row + 4) = turn(row) ^ 1 for the rows of the first half
+  static __device__ __forceinline__ bf16x8 pair(const E* row, int j) {
+    const bf16x4 a = read_tr4(row + j * 8), b = read_tr4(row + 4 * LD + (j ^ 1) * 8);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  } else {
-    const E* p = m + (k0 + 4 * g) * ld + n0 + (PERM ? 8 * (c >> 2) + (c & 3) : c);
+  }
+  static __device__ __forceinline__ f32x4 column(const E* p) {
     f32x4 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = p[i * ld];
+    for (int i = 0; i < 4; ++i) r[i] = p[i * LD];
     return r;
   }
-}
+};
 
-// Column offset (n0 of mx_tr with PERM) of state tile t.
+// Column offset of state tile t.
 __device__ __forceinline__ int tile_col(int t) { return 32 * (t >> 1) + 4 * (t & 1); }
 // A lane's first row of state tile t; it holds four.
-__device__ __forceinline__ int tile_row(int t) { return tile_col(t) + 8 * (lane_id() >> 4); }
+__device__ __forceinline__ int tile_row(int t, int l) { return tile_col(t) + 8 * (l >> 4); }
 
 // x as TERMS operands whose sum is x to fp32's last bits: three bf16 terms carry 24 bits, so a
 // state or a weighted row in a product with bf16 data loses nothing that fp32 would keep.
 template <typename E, int TERMS = Mx<E>::TERMS>
 __device__ __forceinline__ void split(const float* x, typename Mx<E>::frag* out) {
   if constexpr (sizeof(E) == 2) {
+    // two values at a time: one conversion makes both, and each is half of its 32 bits
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float r = x[e];
+    for (int e = 0; e < 8; e += 2) {
+      f32x2 r = {x[e], x[e + 1]};
 #pragma unroll
       for (int t = 0; t < TERMS; ++t) {
-        const bf16 b = (bf16)r;
-        out[t][e] = b;
-        r -= (float)b;
+        const bf16x2_t b = __builtin_convertvector(r, bf16x2_t);
+        out[t][e] = b[0];
+        out[t][e + 1] = b[1];
+        const uint32_t u = __builtin_bit_cast(uint32_t, b);
+        r[0] -= __uint_as_float(u << 16);
+        r[1] -= __uint_as_float(u & 0xFFFF0000u);
       }
     }
   } else {
@@ -91,70 +139,56 @@ __device__ __forceinline__ void split(const float* x, typename Mx<E>::frag* out)
   }
 }
 
-// Operand fragments of a state over its NT row tiles: NT / 2 of bf16, NT of fp32, TERMS each.
-template <typename E, int NT, int TERMS>
-struct StateOperand {
-  static constexpr int STEPS = sizeof(E) == 2 ? NT / 2 : NT;
-  typename Mx<E>::frag f[STEPS][TERMS];
-  __device__ __forceinline__ void from(const f32x4* tiles) {
+// A chunk's rows of one head; nothing where there are none.
+template <typename E>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const E* base, int64_t stride, int width,
+                                                          int len) {
+  // rows are at least as far apart as wide: no rows, no bytes
+  const int bytes = max(((len - 1) * (int)stride + width) * (int)sizeof(E), 0);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(base), 0, bytes, 0x00020000);
+}
+
+// x . four consecutive columns of a tile's row
+template <typename E, int D>
+__device__ __forceinline__ float dot4(const E* m, int row, int col, f32x4 x) {
+  typedef E four __attribute__((ext_vector_type(4)));
+  constexpr int V = 16 / (int)sizeof(E);
+  const four y = *reinterpret_cast<const four*>(m + Tile<E, D>::piece(row, col / V) + col % V);
+  float r = 0.f;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      float x[8];
-      if constexpr (sizeof(E) == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = tiles[2 * s][i], x[4 + i] = tiles[2 * s + 1][i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = tiles[s][i];
-      }
-      split<E, TERMS>(x, f[s]);
-    }
-  }
-  // acc[state column, row of m] += sum over the state's rows r of state[r][.] m[.][r]
-  __device__ __forceinline__ f32x4 times(const E* m, int ld, int row0, f32x4 acc) const {
-    const int l = lane_id();
-    const E* p = m + (row0 + (l & 15)) * ld + 8 * (l >> 4);
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const auto b = *reinterpret_cast<const typename Mx<E>::frag*>(
-          p + (sizeof(E) == 2 ? 32 * s : tile_col(s)));
-#pragma unroll
-      for (int t = TERMS - 1; t >= 0; --t) acc = Mx<E>::mma(f[s][t], b, acc);
-    }
-    return acc;
-  }
-};
+  for (int e = 0; e < 4; ++e) r = fmaf(x[e], (float)y[e], r);
+  return r;
+}
 
 // A chunk's rows of one head, C x D values (D a tile size; the head's own `width` may be less), on
 // their way from memory to LDS through registers.  A buffer resource ends behind the chunk's last
 // row, so rows past it and columns past the head read as zeros.
 template <typename E, int D, int C, int NTH>
 struct Rows {
-  static constexpr int V = 16 / (int)sizeof(E), VPR = D / V, N = C * VPR / NTH;
-  static_assert(C * VPR % NTH == 0 && NTH % VPR == 0, "block shape");
-  uint32_t off;  // bytes of this thread's first vector
-  int step;      // bytes to the next one
-  int at;        // elements into LDS rows
+  typedef Tile<E, D> T;
+  static constexpr int V = 16 / (int)sizeof(E), VPR = D / V, RS = NTH / VPR;
+  // vectors a thread; a small tile leaves the last threads without
+  static constexpr int N = C * VPR < NTH ? 1 : C * VPR / NTH;
+  static_assert((C * VPR % NTH == 0 || C * VPR < NTH) && NTH % VPR == 0, "block shape");
   u32x4 reg[N];
-  __device__ __forceinline__ void open(int64_t stride, int width, int ld) {
-    const int row = threadIdx.x / VPR, col = threadIdx.x % VPR;
-    off = col * V < width ? (uint32_t)(row * (int)stride * (int)sizeof(E) + col * 16) : kNoColumn;
-    step = col * V < width ? NTH / VPR * (int)stride * (int)sizeof(E) : 0;
-    at = row * ld + col * V;
-  }
-  // base: the chunk's first row of this head; len: its rows; all uniform
-  __device__ __forceinline__ void load(const E* base, int64_t stride, int width, int len) {
-    const int bytes = len > 0 ? (int)(((len - 1) * stride + width) * (int64_t)sizeof(E)) : 0;
-    const __amdgpu_buffer_rsrc_t rs =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(base), 0, bytes, 0x00020000);
+  // base: the chunk's first row of this head; len: its rows; all uniform.  t: the thread, or its number
+  // made opaque in a loop.
+  __device__ __forceinline__ void load(const E* base, int64_t stride, int width, int len, int t) {
+    const __amdgpu_buffer_rsrc_t rs = rows_of(base, stride, width, len);
+    const int row = t / VPR, col = t % VPR, bytes = (int)stride * (int)sizeof(E);
+    // steps of less than 2^31 bytes leave kNoColumn past every buffer
+    const uint32_t off = col * V < width && row < C ? (uint32_t)(row * bytes + col * 16) : kNoColumn;
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      reg[j] = __builtin_amdgcn_raw_buffer_load_b128(rs, off + (uint32_t)(j * step), 0, 0);
+      reg[j] = __builtin_amdgcn_raw_buffer_load_b128(
+          rs, off + (uint32_t)j * (uint32_t)(RS * bytes), 0, 0);
   }
-  __device__ __forceinline__ void store(E* lds, int ld) const {
+  __device__ __forceinline__ void store(E* lds, int t) const {
+    const int row = t / VPR, col = t % VPR;
+    if (C * VPR < NTH && row >= C) return;
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      *reinterpret_cast<u32x4*>(lds + at + j * (NTH / VPR) * ld) = reg[j];
+      *reinterpret_cast<u32x4*>(lds + T::piece(row + j * RS, col)) = reg[j];
   }
 };
 
@@ -169,12 +203,17 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t rs, uint32_t off, 
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rs, off, 0, 0);
 }
 
-template <typename E>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(E* base, int64_t stride, int width,
-                                                          int len) {
-  const int bytes = len > 0 ? (int)(((len - 1) * stride + width) * (int64_t)sizeof(E)) : 0;
-  return __builtin_amdgcn_make_buffer_rsrc(base, 0, bytes, 0x00020000);
+// The same into an LDS tile of D columns.
+template <typename E, int D>
+__device__ __forceinline__ void put4(E* m, int row, int col, f32x4 x) {
+  constexpr int V = 16 / (int)sizeof(E);
+  E* to = m + Tile<E, D>::piece(row, col / V) + col % V;
+  if constexpr (sizeof(E) == 2)
+    *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(x, bf16x4);
+  else
+    *reinterpret_cast<f32x4*>(to) = x;
 }
+
 
 __device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -236,9 +275,15 @@ struct Decays {
   }
 };
 
-// The log-decay of token t of a chunk that starts at token t0 (0 past its end).
-__device__ __forceinline__ float load_decay(const LinearProblem& p, long t0, int t, int len, int h) {
-  return t < len ? p.g[p.head_decay ? h : (t0 + t) * p.H + h] : 0.f;
+// The log-decay of the lane's token of a chunk that starts at token t0 (0 past its end): always one
+// load, so that the number of loads in flight is known.
+__device__ __forceinline__ float load_decay(const LinearProblem& p, long t0, int len, int h) {
+  const int t = lane_id(), step = p.head_decay ? 0 : p.H;
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(p.g) + (p.head_decay ? 0 : t0 * p.H) + h, 0,
+      len > 0 ? ((len - 1) * step + 1) * 4 : 0, 0x00020000);
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+      rs, t < len ? (uint32_t)(t * step * 4) : kNoColumn, 0, 0));
 }
 
 // Workgroup b's unit of work: the `group` units in a row that read the same q and k rows run on one
@@ -259,6 +304,15 @@ inline int group_of(const LinearProblem& p, int slabs, int blocks) {
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The slot of the state kept at the end of a segment's chunk m (slots of the form of ssm.h, every * C
+// tokens long; a segment is no longer than that or a multiple of it).
+__device__ __forceinline__ int anchor_of(const LinearProblem& p, const Chunk& c, int m, int every,
+                                         int C) {
+  const ChunkMap map = {p.cu, p.T, p.Ttot, p.N, every * C};
+  const int first = p.cu ? chunk_first(map, c.n) : c.n * chunk_count(p.T, every * C);
+  return uniform(first + (c.t0 - c.bos) / (every * C) + m / every);
+}
 
 // A segment slot's chunk (see ssm_device.h), its values known to be the same in every lane.
 __device__ __forceinline__ Chunk uniform_chunk(const LinearProblem& p, int slot) {

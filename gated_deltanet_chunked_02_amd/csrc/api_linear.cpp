@@ -59,11 +59,13 @@ gdn_status check_linear(const gdn_linear_desc* d, bool packed, gdn::LinearProble
   return GDN_OK;
 }
 
-// Segment length: sequences stay whole where their heads (times the value slabs) make half of the
-// `fill` workgroups that run at once, and are cut into as many segments as fill them elsewhere, of
-// at least kMinSegment tokens; a packed batch is cut at twice its mean length at least, so that one
-// long sequence does not run alone.
-constexpr int kMinSegment = 128;
+// Segment length.  A sequence stays whole where its heads (times the value slabs) give every CU a
+// workgroup: 8 x 2048 tokens of 32 heads take 162 us whole and 212 in two segments each, whose states
+// another pass has to make.  Fewer are cut into as many segments as make `fill` workgroups, of two chunks
+// at least (16384 tokens of 32 heads: 221 us in 16 segments, 270 in 8), but not sequences of fewer than
+// six chunks, whose few steps take less than two more launches.  A packed batch is cut for one head a CU
+// as well, because its sequences are of unlike lengths, and at twice its mean length in any case.
+constexpr int kUnits = 256;  // CUs
 
 int slots_of(const gdn::LinearProblem& p, bool packed) {
   return p.N == 0 ? 0
@@ -73,17 +75,19 @@ int slots_of(const gdn::LinearProblem& p, bool packed) {
 
 void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
   p->Lc = gdn::kScanNoSplit;
-  if (p->N > 0 && p->Ttot > 0) {
-    const long long units = (long long)p->H * slabs, longest = packed ? p->Ttot : p->T;
+  const int C = gdn::linear_chunk(p->f32);
+  const long long longest = packed ? p->Ttot : p->T;
+  if (p->N > 0 && longest >= 6 * C) {
+    const long long units = (long long)p->H * slabs;
     long long L = longest;
-    if (units * p->N * 2 <= fill) {
+    if (units * p->N < (packed ? kUnits + 1 : kUnits)) {
       const long long each = packed ? fill / units : fill / (units * p->N);
-      L = (longest + each - 1) / each;
+      L = each > 0 ? (longest + each - 1) / each : longest;
     } else if (packed) {
       L = 2LL * ((p->Ttot + p->N - 1) / p->N);
     }
+    if (L < 2 * C) L = 2 * C;
     L = (L + gdn::kLinearChunk - 1) / gdn::kLinearChunk * gdn::kLinearChunk;
-    if (L < kMinSegment) L = kMinSegment;
     if (L < longest) p->Lc = (int)L;
   }
   p->slots = slots_of(*p, packed);
@@ -91,7 +95,7 @@ void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
 
 int slabs_of(const gdn::LinearProblem& p) { return (p.Dv + gdn::kLinearSlab - 1) / gdn::kLinearSlab; }
 
-constexpr int kFwdFill = 512;  // two workgroups a CU
+constexpr int kFwdFill = 512;
 constexpr int kBwdFill = 256;  // one
 
 void plan_fwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, slabs_of(*p), kFwdFill); }
@@ -106,12 +110,14 @@ void plan_bwd(gdn::LinearProblem* p, bool packed) {
   }
 }
 
-// A launch has fewer than 2^32 threads: segments' heads and slabs in workgroups of up to 512, the
-// composition's four values a thread, and the shared heads' sums.
+// A launch has fewer than 2^32 threads: segments' heads and slabs in workgroups of up to 512, there and
+// back; the composition's four values a thread, likewise; the shared heads' sums, four values of dq and
+// of dk a thread and another row of the grid.
 bool grids_ok(const gdn::LinearProblem& p) {
   const long long most = 1LL << 32, cell = ((long long)p.Dk * p.Dv / 4 + 255) / 256 * 256;
-  return (long long)p.slots * p.H * slabs_of(p) * 512 < most && (long long)p.N * p.H * cell < most &&
-         (long long)p.Ttot * p.Hg * p.Dk / 4 + 256 < most;
+  return (long long)p.slots * p.H * slabs_of(p) * 512 * 2 < most &&
+         (long long)p.N * p.H * cell * 2 < most &&
+         ((long long)p.Ttot * p.Hg * p.Dk / 4 + p.H * 16LL + 1024) * 3 < most;
 }
 
 struct FwdLayout {

@@ -56,14 +56,13 @@ struct LinearBwd {
 
 // A pass over segments that makes states only: sums of x_t y_t^T.
 struct LinearPass {
-  const void* x;       // k, or q with reverse
-  const void* y;       // v, or dout
+  const void* x;       // k; back: q
+  const void* y;       // v; back: dout
   int64_t sx, sy;
-  bool reverse;        // from the segments' ends back
   float* own;          // [slots, H, Dk, Dv] every segment's own sum
 };
-hipError_t launch_linear_state(const LinearProblem& p, const LinearPass& a, hipStream_t st);
-hipError_t launch_linear_compose(const LinearProblem& p, hipStream_t st);
+// The segments' start states (p.states) and, with b, the gradients at their ends (b->grads).
+hipError_t launch_linear_states(const LinearProblem& p, const LinearBwd* b, hipStream_t st);
 
 // The tensors of one pass of the recurrence: the forward's own, or those that make dq (linear.hip).
 // Heads: q and k rows have those of h / qrep, v (and x) rows those of h / vrep.

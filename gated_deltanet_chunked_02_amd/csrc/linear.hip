@@ -291,31 +291,47 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   }
 }
 
-// Start states from the segments' own end states, in place: a thread has four values of a state
-// and walks its sequence's segments.
-__global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p) {
+// Start states from the segments' own end states, in place: a thread has four values of a state and
+// walks its sequence's segments, four loads ahead of the one it is at.  The grid's second row makes the
+// gradients at the segments' ends from their own shares, last to first.
+struct LinearEnds {
+  const float* from;  // dht or null
+  float* grads;
+};
+__global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p, LinearEnds b) {
+  constexpr int AHEAD = 4;
   const long cell = (long)p.Dk * p.Dv;
   const int blocks = (int)((cell / 4 + 255) / 256);
   const int nh = blockIdx.x / blocks, n = nh / p.H, h = nh - n * p.H;
   const long at = ((long)(blockIdx.x - nh * blocks) * 256 + threadIdx.x) * 4;
   if (at >= cell) return;
+  const bool back = blockIdx.y != 0;
   const ChunkMap m = {p.cu, p.T, p.Ttot, p.N, p.Lc};
   int bos, eos;
   chunk_seq(m, n, bos, eos);
   const int count = chunk_count(eos - bos, p.Lc);
   const int first = p.cu ? chunk_first(m, n) : n * count;
+  const float* from = back ? b.from : p.h0;
+  float* states = back ? b.grads : p.states;
   f32x4 s = zero4();
-  if (p.h0) s = *reinterpret_cast<const f32x4*>(p.h0 + ((long)n * p.H + h) * cell + at);
-  for (int i = 0; i < count; ++i) {
-    const long sh = (long)(first + i) * p.H + h;
-    f32x4* x = reinterpret_cast<f32x4*>(p.states + sh * cell + at);
-    if (i + 1 < count) {
-      const f32x4 own = *x;
-      *x = s;
-      s = s * exp2_f32(p.sums[sh]) + own;
-    } else {
-      *x = s;
-    }
+  if (from) s = *reinterpret_cast<const f32x4*>(from + ((long)n * p.H + h) * cell + at);
+  // the i-th segment on the way
+  auto slot = [&](int i) { return ((long)first + (back ? count - 1 - i : i)) * p.H + h; };
+  for (int i = 0; i < count; i += AHEAD) {
+    f32x4 own[AHEAD];
+    float keep[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i + j + 1 < count) {
+        own[j] = *reinterpret_cast<const f32x4*>(states + slot(i + j) * cell + at);
+        keep[j] = p.sums[slot(i + j)];
+      }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (i + j < count) {
+        *reinterpret_cast<f32x4*>(states + slot(i + j) * cell + at) = s;
+        if (i + j + 1 < count) s = s * exp2_f32(keep[j]) + own[j];
+      }
   }
 }
 
@@ -324,7 +340,7 @@ __global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p) {
 // chunk first: the gradients of states), from zero, and the segment's decay.  Wave w holds columns of x
 // (rows of the state) as tiles over y.
 template <typename E, int DK, int DV, int NW, bool REV>
-__global__ __launch_bounds__(64 * NW, 2) void k_linear_state(LinearProblem p, LinearPass a) {
+__device__ __forceinline__ void linear_state(const LinearProblem& p, const LinearPass& a) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
   constexpr int NTH = 64 * NW, TK = DK / 16 / NW, VT = DV / 16;
   constexpr int KF = Mx<E>::KF, KS = C / KF, TERMS = Mx<E>::TERMS;
@@ -424,7 +440,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_linear_state(LinearProblem p, Li
       if (row < p.Dk && y0 < width)
         *reinterpret_cast<f32x4*>(a.own + at + (long)row * p.Dv + v0 + y0) = S[j][t];
     }
-  if (slab == 0 && threadIdx.x == NTH - 1) p.sums[(long)slot * p.H + h] = (float)sum;
+  // each segment's decay once: the way back leaves the last one's, which the way there leaves out
+  if (slab == 0 && threadIdx.x == NTH - 1 && (!REV || c.i == c.count - 1))
+    p.sums[(long)slot * p.H + h] = (float)sum;
+}
+
+// Both directions in one launch: the grid's second row goes back.
+template <typename E, int DK, int DV, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_linear_state(LinearProblem p, LinearPass a,
+                                                             LinearPass back) {
+  if (blockIdx.y == 0)
+    linear_state<E, DK, DV, NW, false>(p, a);
+  else
+    linear_state<E, DK, DV, NW, true>(p, back);
 }
 
 template <typename E, int DK, int DV, int NW, int OCC>
@@ -469,53 +497,61 @@ hipError_t launch_dq_e(const LinearProblem& p, const LinearRun& r, hipStream_t s
 }
 
 template <typename E, int DK, int DV>
-hipError_t launch_state(const LinearProblem& p, const LinearPass& a, hipStream_t st) {
+hipError_t launch_state(const LinearProblem& p, const LinearPass& a, const LinearPass* back,
+                        hipStream_t st) {
   const int slabs = (p.Dv + DV - 1) / DV;
   const int blocks = p.slots * p.H * slabs;
   LinearProblem q = p;
   q.group = group_of(p, slabs, blocks);
   constexpr int NW = DK <= 64 ? 4 : 8;
-  if (a.reverse)
-    k_linear_state<E, DK, DV, NW, true><<<blocks, NW * 64, 0, st>>>(q, a);
-  else
-    k_linear_state<E, DK, DV, NW, false><<<blocks, NW * 64, 0, st>>>(q, a);
+  k_linear_state<E, DK, DV, NW>
+      <<<dim3(blocks, back ? 2 : 1), NW * 64, 0, st>>>(q, a, back ? *back : LinearPass{});
   return hipGetLastError();
 }
 
 template <typename E>
-hipError_t launch_state_e(const LinearProblem& p, const LinearPass& a, hipStream_t st) {
+hipError_t launch_state_e(const LinearProblem& p, const LinearPass& a, const LinearPass* back,
+                          hipStream_t st) {
   if (p.Dv <= 64) {
-    if (p.Dk <= 64) return launch_state<E, 64, 64>(p, a, st);
-    if (p.Dk <= 128) return launch_state<E, 128, 64>(p, a, st);
-    return launch_state<E, 256, 64>(p, a, st);
+    if (p.Dk <= 64) return launch_state<E, 64, 64>(p, a, back, st);
+    if (p.Dk <= 128) return launch_state<E, 128, 64>(p, a, back, st);
+    return launch_state<E, 256, 64>(p, a, back, st);
   }
-  if (p.Dk <= 64) return launch_state<E, 64, 128>(p, a, st);
-  if (p.Dk <= 128) return launch_state<E, 128, 128>(p, a, st);
-  return launch_state<E, 256, 128>(p, a, st);
+  if (p.Dk <= 64) return launch_state<E, 64, 128>(p, a, back, st);
+  if (p.Dk <= 128) return launch_state<E, 128, 128>(p, a, back, st);
+  return launch_state<E, 256, 128>(p, a, back, st);
 }
 
 }  // namespace
 
-hipError_t launch_linear_state(const LinearProblem& p, const LinearPass& a, hipStream_t st) {
-  return p.f32 ? launch_state_e<float>(p, a, st) : launch_state_e<bf16>(p, a, st);
-}
-
-hipError_t launch_linear_compose(const LinearProblem& p, hipStream_t st) {
+hipError_t launch_linear_states(const LinearProblem& p, const LinearBwd* b, hipStream_t st) {
+  LinearPass a = {}, back = {};
+  a.x = p.k;
+  a.y = p.v;
+  a.sx = p.sk;
+  a.sy = p.sv;
+  a.own = p.states;
+  LinearEnds ends = {};
+  if (b) {
+    back.x = p.q;
+    back.y = b->dout;
+    back.sx = p.sq;
+    back.sy = (int64_t)p.H * p.Dv;
+    back.own = b->grads;
+    ends.from = b->dht;
+    ends.grads = b->grads;
+  }
+  const hipError_t e = p.f32 ? launch_state_e<float>(p, a, b ? &back : nullptr, st)
+                             : launch_state_e<bf16>(p, a, b ? &back : nullptr, st);
+  if (e != hipSuccess) return e;
   const long blocks = ((long)p.Dk * p.Dv / 4 + 255) / 256 * p.N * p.H;
-  k_linear_compose<<<(unsigned)blocks, 256, 0, st>>>(p);
+  k_linear_compose<<<dim3((unsigned)blocks, b ? 2 : 1), 256, 0, st>>>(p, ends);
   return hipGetLastError();
 }
 
 hipError_t launch_linear_fwd(const LinearProblem& p, hipStream_t st) {
   if (p.Lc != kScanNoSplit) {
-    LinearPass a = {};
-    a.x = p.k;
-    a.y = p.v;
-    a.sx = p.sk;
-    a.sy = p.sv;
-    a.own = p.states;
-    hipError_t e = launch_linear_state(p, a, st);
-    if (e == hipSuccess) e = launch_linear_compose(p, st);
+    const hipError_t e = launch_linear_states(p, nullptr, st);
     if (e != hipSuccess) return e;
   }
   LinearRun r = {};

@@ -355,58 +355,32 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   }
 }
 
-// The gradients of the states at the segments' ends from the segments' own shares, in place, last to
-// first (k_linear_compose the other way round).
-__global__ __launch_bounds__(256) void k_linear_compose_bwd(LinearProblem p, LinearBwd b) {
-  const long cell = (long)p.Dk * p.Dv;
-  const int blocks = (int)((cell / 4 + 255) / 256);
-  const int nh = blockIdx.x / blocks, n = nh / p.H, h = nh - n * p.H;
-  const long at = ((long)(blockIdx.x - nh * blocks) * 256 + threadIdx.x) * 4;
-  if (at >= cell) return;
-  const ChunkMap m = {p.cu, p.T, p.Ttot, p.N, p.Lc};
-  int bos, eos;
-  chunk_seq(m, n, bos, eos);
-  const int count = chunk_count(eos - bos, p.Lc);
-  const int first = p.cu ? chunk_first(m, n) : n * count;
-  f32x4 s = zero4();
-  if (b.dht) s = *reinterpret_cast<const f32x4*>(b.dht + ((long)n * p.H + h) * cell + at);
-  for (int i = count - 1; i >= 0; --i) {
-    const long sh = (long)(first + i) * p.H + h;
-    f32x4* x = reinterpret_cast<f32x4*>(b.grads + sh * cell + at);
-    if (i > 0) {
-      const f32x4 own = *x;
-      *x = s;
-      s = s * exp2_f32(p.sums[sh]) + own;
-    } else {
-      *x = s;
-    }
-  }
-}
-
-// dq and dk of a q/k head: the sum of its value heads' shares, in order, four values a thread.
+// What is left after the passes, each grid row a part: dq (0) and dk (1) of a q/k head, the sum of its
+// value heads' shares in order, four values a thread; dg of a head (2), the sum over its segments.
 template <typename E>
-__global__ __launch_bounds__(256) void k_linear_shares(LinearProblem p, LinearBwd b) {
+__global__ __launch_bounds__(kColumnThreads) void k_linear_sums(LinearProblem p, LinearBwd b, int first) {
+  const int part = first + blockIdx.y;
+  if (part == 2) {
+    if ((int)blockIdx.x >= (p.H + 63) / 64) return;
+    const int c = blockIdx.x * 64 + lane_id();
+    const float s = column_sum(b.dgp, p.H, p.slots, c, p.H);
+    if (threadIdx.x < 64 && c < p.H) b.dg[c] = s;
+    return;
+  }
   const long vecs = (long)p.Hg * p.Dk / 4, total = p.cu ? min(max(p.cu[p.N], 0), p.Ttot) : p.Ttot;
-  const long at = (long)blockIdx.x * 256 + threadIdx.x;
+  const long at = (long)blockIdx.x * kColumnThreads + threadIdx.x;
   if (at >= total * vecs) return;
   const long t = at / vecs;
   const int x = (int)(at - t * vecs) * 4, hk = x / p.Dk, col = x - hk * p.Dk, rep = p.H / p.Hg;
-  const float* from = b.part + (blockIdx.y ? (long)p.Ttot * p.H * p.Dk : 0) +
+  const float* from = b.part + (part ? (long)p.Ttot * p.H * p.Dk : 0) +
                       (t * p.H + (long)hk * rep) * p.Dk + col;
   f32x4 s = zero4();
   for (int r = 0; r < rep; ++r) s += *reinterpret_cast<const f32x4*>(from + (long)r * p.Dk);
-  E* to = static_cast<E*>(blockIdx.y ? b.dk : b.dq) + at * 4;
+  E* to = static_cast<E*>(part ? b.dk : b.dq) + at * 4;
   if constexpr (sizeof(E) == 2)
     *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(s, bf16x4);
   else
     *reinterpret_cast<f32x4*>(to) = s;
-}
-
-__global__ __launch_bounds__(kColumnThreads) void k_linear_heads(const float* part, float* dg,
-                                                                 int slots, int H) {
-  const int c = blockIdx.x * 64 + lane_id();
-  const float s = column_sum(part, H, slots, c, H);
-  if (threadIdx.x < 64 && c < H) dg[c] = s;
 }
 
 template <typename E, int DK, int DV>
@@ -429,9 +403,12 @@ hipError_t launch_grads_e(const LinearProblem& p, const LinearBwd& b, hipStream_
 }
 
 template <typename E>
-hipError_t launch_shares(const LinearProblem& p, const LinearBwd& b, hipStream_t st) {
-  const long vecs = (long)p.Ttot * p.Hg * p.Dk / 4;
-  k_linear_shares<E><<<dim3((unsigned)((vecs + 255) / 256), 2), 256, 0, st>>>(p, b);
+hipError_t launch_sums(const LinearProblem& p, const LinearBwd& b, bool shares, bool heads,
+                       hipStream_t st) {
+  const long vecs = shares ? (long)p.Ttot * p.Hg * p.Dk / 4 : 0, cols = heads ? (p.H + 63) / 64 : 0;
+  const long blocks = (vecs + kColumnThreads - 1) / kColumnThreads;
+  k_linear_sums<E><<<dim3((unsigned)(blocks > cols ? blocks : cols), 2 * shares + heads),
+                     kColumnThreads, 0, st>>>(p, b, shares ? 0 : 2);
   return hipGetLastError();
 }
 
@@ -440,39 +417,17 @@ hipError_t launch_shares(const LinearProblem& p, const LinearBwd& b, hipStream_t
 hipError_t launch_linear_bwd(const LinearProblem& p, const LinearBwd& b, hipStream_t st) {
   hipError_t e = hipSuccess;
   if (p.slots > 0) {
-    LinearPass a = {};
-    a.x = p.k;
-    a.y = p.v;
-    a.sx = p.sk;
-    a.sy = p.sv;
-    if (p.Lc != kScanNoSplit) {
-      a.own = p.states;
-      e = launch_linear_state(p, a, st);
-      if (e == hipSuccess) e = launch_linear_compose(p, st);
-      LinearPass r = {};
-      r.x = p.q;
-      r.y = b.dout;
-      r.sx = p.sq;
-      r.sy = (int64_t)p.H * p.Dv;
-      r.reverse = true;
-      r.own = b.grads;
-      if (e == hipSuccess) e = launch_linear_state(p, r, st);
-      if (e != hipSuccess) return e;
-      const long blocks = ((long)p.Dk * p.Dv / 4 + 255) / 256 * p.N * p.H;
-      k_linear_compose_bwd<<<(unsigned)blocks, 256, 0, st>>>(p, b);
-      e = hipGetLastError();
-    }
+    if (p.Lc != kScanNoSplit) e = launch_linear_states(p, &b, st);
     if (e == hipSuccess && p.Ttot > 0) e = launch_linear_dq(p, b, st);
     if (e == hipSuccess)
       e = p.f32 ? launch_grads_e<float>(p, b, st) : launch_grads_e<bf16>(p, b, st);
-    if (e == hipSuccess && p.H != p.Hg && p.Ttot > 0)
-      e = p.f32 ? launch_shares<float>(p, b, st) : launch_shares<bf16>(p, b, st);
     if (e != hipSuccess) return e;
   }
-  if (b.dg && p.head_decay) {
-    k_linear_heads<<<(p.H + 63) / 64, kColumnThreads, 0, st>>>(b.dgp, b.dg, p.slots, p.H);
-    e = hipGetLastError();
-  }
+  // without a sequence there is no gradient to write but the heads' zeros
+  const bool shares = p.H != p.Hg && p.Ttot > 0 && p.slots > 0, heads = b.dg && p.head_decay;
+  if (shares || heads)
+    e = p.f32 ? launch_sums<float>(p, b, shares, heads, st)
+              : launch_sums<bf16>(p, b, shares, heads, st);
   return e;
 }
 

@@ -108,11 +108,10 @@ struct Slice {
 // A parameter's values of a thread's channels (ones when absent).
 template <int VEC>
 __device__ __forceinline__ void params(const float* p, int t, int width, int C, float* v) {
+  Slice<float, VEC> s;
+  if (p) s.load(p, t, width, C);
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int c = ((i / VEC) * width + t) * VEC + i % VEC;
-    v[i] = p && c < C ? p[c] : 1.f;
-  }
+  for (int i = 0; i < kEach; ++i) v[i] = p ? s[i] : 1.f;
 }
 
 __device__ __forceinline__ float wave_sum(float x) {
@@ -250,14 +249,25 @@ __global__ __launch_bounds__(MOST) void k_block_norm_bwd(BlockNormProblem p) {
   const int C = p.C, t = w.t, width = 64 * w.waves;
   RowSum<3> sum{&lds};
   float w1[kEach], al[kEach], w2[kEach], d1[kEach], ds[kEach], d2[kEach];
-  params<VEC>(p.w2, t, width, C, w2);
 #pragma unroll
   for (int i = 0; i < kEach; ++i) d1[i] = ds[i] = d2[i] = 0.f;
-  if constexpr (PARTS > 0) {
-    params<VEC>(p.w1, t, width, C, w1);
-    params<VEC>(p.scale, t, width, C, al);
+  auto place = [&]() {  // t; without registers to spare, offsets are made at each use
+    int own = t;
+    if (!AHEAD) opaque(own);
+    return own;
+  };
+  auto weights = [&]() {  // of the block's half; read at each use, from the caches
+    const int own = place();
+    if constexpr (PARTS > 0) {
+      params<VEC>(p.w1, own, width, C, w1);
+      params<VEC>(p.scale, own, width, C, al);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) al[i] *= p.residual_scale;
+      for (int i = 0; i < kEach; ++i) al[i] *= p.residual_scale;
+    }
+  };
+  if (AHEAD) {
+    params<VEC>(p.w2, t, width, C, w2);
+    weights();
   }
   const float inv = 1.f / (float)C;
   Slice<R, VEC> xs, dxs;
@@ -268,21 +278,26 @@ __global__ __launch_bounds__(MOST) void k_block_norm_bwd(BlockNormProblem p) {
 #pragma unroll
   for (int i = 0; i < Slice<E, VEC>::kWords; ++i) dys.u[i] = 0;
   auto fetch = [&](int row) {
-    xs.load(static_cast<const R*>(p.x) + (long)row * C, t, width, C);
+    const int own = place();
+    xs.load(static_cast<const R*>(p.x) + (long)row * C, own, width, C);
     if constexpr (PARTS > 0) {
-      hs.load(static_cast<const E*>(p.h) + row * p.sh, t, width, C);
+      hs.load(static_cast<const E*>(p.h) + row * p.sh, own, width, C);
       if (p.post) rstd1 = p.rstd1[row];
     }
-    if constexpr (PARTS > 1) gs.load(static_cast<const E*>(p.gate) + row * p.sg, t, width, C);
-    if (p.dxo) dxs.load(static_cast<const R*>(p.dxo) + (long)row * C, t, width, C);
+    if constexpr (PARTS > 1) gs.load(static_cast<const E*>(p.gate) + row * p.sg, own, width, C);
+    if (p.dxo) dxs.load(static_cast<const R*>(p.dxo) + (long)row * C, own, width, C);
     if (p.dy) {
-      dys.load(static_cast<const E*>(p.dy) + (long)row * C, t, width, C);
+      dys.load(static_cast<const E*>(p.dy) + (long)row * C, own, width, C);
       rstd2 = p.rstd2[row];
     }
   };
   if (AHEAD && w.first < p.rows) fetch(w.first);
   for (int row = w.first; row < p.rows; row += w.step) {
-    if (!AHEAD) fetch(row);
+    if (!AHEAD) {
+      fetch(row);
+      params<VEC>(p.w2, place(), width, C, w2);
+      weights();
+    }
     float hat[kEach], dR[kEach];
     float s[3] = {0.f, 0.f, 0.f};
     const float r1 = rstd1, r2 = rstd2;
@@ -308,8 +323,9 @@ __global__ __launch_bounds__(MOST) void k_block_norm_bwd(BlockNormProblem p) {
     const float m1 = (s[1] - m * s[2]) * inv;  // E[dn w1 xh]
 #pragma unroll
     for (int i = 0; i < kEach; ++i) dR[i] = fmaf(-hat[i], m, dR[i]);
-    Slice<R, VEC>::store(static_cast<R*>(p.dx) + (long)row * C, t, width, C, dR);
+    Slice<R, VEC>::store(static_cast<R*>(p.dx) + (long)row * C, place(), width, C, dR);
     if constexpr (PARTS > 0) {
+      if (!AHEAD) weights();
       float dg[kEach];
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -324,9 +340,9 @@ __global__ __launch_bounds__(MOST) void k_block_norm_bwd(BlockNormProblem p) {
         d1[i] = fmaf(dn, xh, d1[i]);
         dR[i] = p.post ? r1 * fmaf(dn, w1[i], -xh * m1) : dn;
       }
-      Slice<E, VEC>::store(static_cast<E*>(p.dh) + (long)row * C, t, width, C, dR);
+      Slice<E, VEC>::store(static_cast<E*>(p.dh) + (long)row * C, place(), width, C, dR);
       if constexpr (PARTS > 1)
-        Slice<E, VEC>::store(static_cast<E*>(p.dgate) + (long)row * C, t, width, C, dg);
+        Slice<E, VEC>::store(static_cast<E*>(p.dgate) + (long)row * C, place(), width, C, dg);
     }
   }
   float* part = p.part + (long)(w.waves == 1 ? w.first : (int)blockIdx.x) * 3 * C;

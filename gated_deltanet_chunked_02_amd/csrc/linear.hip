@@ -134,21 +134,37 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
     fetch(m + 1, tid);
 
     // scores: the lower tiles, rows j of tile tj against columns i of tile ti
-    for (int x = wave; x < TT * (TT + 1) / 2; x += NW) {
-      const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-      f32x4 a = zero4();
+    lower_tiles<TT, NW, !GRAD>(wave, [&](auto count, int first) {
+      constexpr int N = decltype(count)::value;
+      int ti[N], tj[N];
+      f32x4 a[N];
+      int lx = lo;
+      if constexpr (GRAD) opaque(lx);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int x = first + n * NW;
+        ti[n] = tile_i(x);
+        tj[n] = x - ti[n] * (ti[n] + 1) / 2;
+        a[n] = zero4();
+      }
 #pragma unroll
       for (int s = 0; s < DK / KF; ++s)
-        a = Mx<E>::mma(TK::ld(Ks, 16 * tj, KF * s, lo), TK::ld(Qs, 16 * ti, KF * s, lo), a);
-      const int i = 16 * ti + lc, j = 16 * tj + 4 * lg;
-      const double Gi = d.G[i];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x2 = a[e] * exp2_f32((float)(Gi - d.G[j + e]));
-        a[e] = j + e <= i ? x2 * p.scale : 0.f;
+        for (int n = 0; n < N; ++n)
+          a[n] = Mx<E>::mma(TK::ld(Ks, 16 * tj[n], KF * s, lx), TK::ld(Qs, 16 * ti[n], KF * s, lx),
+                            a[n]);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int i = 16 * ti[n] + (lx & 15), j = 16 * tj[n] + 4 * (lx >> 4);
+        const double Gi = d.G[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x2 = a[n][e] * exp2_f32((float)(Gi - d.G[j + e]));
+          a[n][e] = j + e <= i ? x2 * p.scale : 0.f;
+        }
+        put4<E, C>(Ps, i, j, a[n]);
       }
-      put4<E, C>(Ps, i, j, a);
-    }
+    });
     const float g = gnext;
     gnext = decay_of(m + 2);
     if (wave == NW - 1) dec[(m + 1) & 1].make(g);
@@ -335,10 +351,12 @@ __global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p, LinearE
   }
 }
 
-// Sums of outer products x_t y_t^T over a segment, without its outputs: forward (x = k, y = v, decays
-// to the chunk's end), or in REV backward (x = q, y = dout, decays from the chunk's start, the last
-// chunk first: the gradients of states), from zero, and the segment's decay.  Wave w holds columns of x
-// (rows of the state) as tiles over y.
+// Sums of outer products x_t y_t^T over a segment, without its outputs, and the segment's decay: the end
+// state from zero (x = k, y = v, decays to the segment's end), or in REV the gradient at its start
+// (x = q, y = dout, decays from there).  Wave w holds columns of x (rows of the state) as tiles over y.
+// Both take the last chunk first, so that the passes after this one, which begin with the first, find
+// those rows in the last-level cache; the end state then needs no scaling from chunk to chunk, as a
+// chunk's rows bring the decay of all that follow.
 template <typename E, int DK, int DV, int NW, bool REV>
 __device__ __forceinline__ void linear_state(const LinearProblem& p, const LinearPass& a) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
@@ -372,7 +390,7 @@ __device__ __forceinline__ void linear_state(const LinearProblem& p, const Linea
   Rows<E, DK, C, NTH> x;
   Rows<E, DV, C, NTH> y;
   const int chunks = (c.len + C - 1) / C;
-  auto chunk_at = [&](int m) { return REV ? chunks - 1 - m : m; };
+  auto chunk_at = [&](int m) { return chunks - 1 - m; };
   auto fetch = [&](int m, int tid) {  // nothing past the last chunk
     const int len = max(0, m < 0 ? 0 : min(C, c.len - m * C));
     x.load(xp + (long)m * C * a.sx, a.sx, p.Dk, len, tid);
@@ -382,7 +400,7 @@ __device__ __forceinline__ void linear_state(const LinearProblem& p, const Linea
     return load_decay(p, c.t0 + (long)m * C, max(0, m < 0 ? 0 : min(C, c.len - m * C)), h);
   };
   double sum = 0.0;
-  float gnext = 0.f;
+  float gnext = 0.f, after = 1.f;  // the decay of the chunks after this one
   if (chunks > 0) {
     fetch(chunk_at(0), threadIdx.x);
     const float g = decay_of(chunk_at(0));
@@ -403,10 +421,12 @@ __device__ __forceinline__ void linear_state(const LinearProblem& p, const Linea
     gnext = decay_of(chunk_at(m + 2));
     if (wave == NW - 1) sum += dec[(m + 1) & 1].make(g);
     const float keep = d.into[C - 1];
+    if constexpr (REV) {
 #pragma unroll
-    for (int j = 0; j < TK; ++j)
+      for (int j = 0; j < TK; ++j)
 #pragma unroll
-      for (int t = 0; t < VT; ++t) S[j][t] *= keep;
+        for (int t = 0; t < VT; ++t) S[j][t] *= keep;
+    }
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       frag f[TK][TERMS];
@@ -417,7 +437,7 @@ __device__ __forceinline__ void linear_state(const LinearProblem& p, const Linea
 #pragma unroll
         for (int e = 0; e < Mx<E>::EPL; ++e) {
           const int i = KF * s + Mx<E>::EPL * lg + e;
-          w[e] = (float)b[e] * (REV ? p.scale * d.into[i] : d.left[i]);
+          w[e] = (float)b[e] * (REV ? p.scale * d.into[i] : after * d.left[i]);
         }
         split<E>(w, f[j]);
       }
@@ -430,6 +450,7 @@ __device__ __forceinline__ void linear_state(const LinearProblem& p, const Linea
           for (int e = TERMS - 1; e >= 0; --e) S[j][t] = Mx<E>::mma(r, f[j][e], S[j][t]);
       }
     }
+    after *= keep;
     __syncthreads();
   }
 #pragma unroll

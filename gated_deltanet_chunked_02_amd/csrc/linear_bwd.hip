@@ -173,37 +173,54 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
         ars, lo < len ? (uint32_t)(lo * p.H * 4) : kNoColumn, 0, 0));
     fetch(m - 1, tid);
 
-    for (int x = wave; x < TT * (TT + 1) / 2; x += NW) {
-      const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-      f32x4 qk = zero4(), ov = zero4();
+    lower_tiles<TT, NW, true>(wave, [&](auto count, int first) {
+      constexpr int N = decltype(count)::value;
+      int ti[N], tj[N];
+      f32x4 qk[N], ov[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int x = first + n * NW;
+        ti[n] = tile_i(x);
+        tj[n] = x - ti[n] * (ti[n] + 1) / 2;
+        qk[n] = ov[n] = zero4();
+      }
 #pragma unroll
       for (int s = 0; s < DK / KF; ++s)
-        qk = Mx<E>::mma(TK::ld(Ks, 16 * tj, KF * s, lo), TK::ld(Qs, 16 * ti, KF * s, lo), qk);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          qk[n] = Mx<E>::mma(TK::ld(Ks, 16 * tj[n], KF * s, lo), TK::ld(Qs, 16 * ti[n], KF * s, lo),
+                             qk[n]);
 #pragma unroll
       for (int s = 0; s < DV / KF; ++s)
-        ov = Mx<E>::mma(TV::ld(Vs, 16 * tj, KF * s, lo), TV::ld(Os, 16 * ti, KF * s, lo), ov);
-      const int i = 16 * ti + lc, j = 16 * tj + 4 * lg;
-      const double Gi = d.G[i];
-      f32x4 pp, mm, ee;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w = p.scale * exp2_f32((float)(Gi - d.G[j + e]));
-        pp[e] = j + e <= i ? qk[e] * w : 0.f;
-        mm[e] = j + e <= i ? ov[e] * w : 0.f;
-        ee[e] = j + e < i ? mm[e] * qk[e] : 0.f;
-      }
-      put4<E, C>(Ps, i, j, pp);
-      put4<E, C>(Ms, i, j, mm);
-      double r = ((double)ee[0] + ee[1]) + ((double)ee[2] + ee[3]);
-      r += __shfl_xor(r, 16);
-      r += __shfl_xor(r, 32);
-      if (lg == 0) rows[tj][i] = r;
+        for (int n = 0; n < N; ++n)
+          ov[n] = Mx<E>::mma(TV::ld(Vs, 16 * tj[n], KF * s, lo), TV::ld(Os, 16 * ti[n], KF * s, lo),
+                             ov[n]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const double s = row_sum((double)ee[e]);
-        if (lc == 0) cols[ti][j + e] = s;
+      for (int n = 0; n < N; ++n) {
+        const int i = 16 * ti[n] + lc, j = 16 * tj[n] + 4 * lg;
+        const double Gi = d.G[i];
+        f32x4 pp, mm, ee;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = p.scale * exp2_f32((float)(Gi - d.G[j + e]));
+          pp[e] = j + e <= i ? qk[n][e] * w : 0.f;
+          mm[e] = j + e <= i ? ov[n][e] * w : 0.f;
+          ee[e] = j + e < i ? mm[e] * qk[n][e] : 0.f;
+        }
+        put4<E, C>(Ps, i, j, pp);
+        put4<E, C>(Ms, i, j, mm);
+        double r = ((double)ee[0] + ee[1]) + ((double)ee[2] + ee[3]);
+        r += __shfl_xor(r, 16);
+        r += __shfl_xor(r, 32);
+        if (lg == 0) rows[tj[n]][i] = r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const double s = row_sum((double)ee[e]);
+          if (lc == 0) cols[ti[n]][j + e] = s;
+        }
       }
-    }
+    });
     const float g = gnext;
     gnext = decay_of(m - 2);
     if (wave == NW - 1) dec[(m - 1) & 1].make(g);

@@ -314,6 +314,23 @@ __device__ __forceinline__ int anchor_of(const LinearProblem& p, const Chunk& c,
   return uniform(first + (c.t0 - c.bos) / (every * C) + m / every);
 }
 
+// A wave's share of the TT (TT + 1) / 2 lower tiles of a chunk's scores, every NW-th: handed to `f` at
+// once (f(Count<N>, the first's number)), so that their products overlap, or one after the other where
+// registers are short.
+template <int N> struct Count { static constexpr int value = N; };
+template <int TT, int NW, bool TOGETHER, typename F>
+__device__ __forceinline__ void lower_tiles(int wave, F f) {
+  constexpr int TILES = TT * (TT + 1) / 2, MOST = (TILES + NW - 1) / NW;
+  if constexpr (!TOGETHER) {
+    for (int x = wave; x < TILES; x += NW) f(Count<1>(), x);
+  } else if (wave + (MOST - 1) * NW < TILES) {
+    f(Count<MOST>(), wave);
+  } else if constexpr (MOST > 1) {
+    f(Count<MOST - 1>(), wave);
+  }
+}
+__device__ __forceinline__ int tile_i(int x) { return x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3; }
+
 // A segment slot's chunk (see ssm_device.h), its values known to be the same in every lane.
 __device__ __forceinline__ Chunk uniform_chunk(const LinearProblem& p, int slot) {
   const ChunkMap m = {p.cu, p.T, p.Ttot, p.N, p.Lc};

@@ -126,15 +126,25 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   auto decay_of = [&](int m) {
     return load_decay(p, c.t0 + (long)m * C, m < 0 ? 0 : min(C, c.len - m * C), h);
   };
+  f32x4 S[VT];  // at the next anchor, this wave's part
+  const int anchors = first_anchor(p, c, b.every, C);
+  auto fetch_state = [&](int m, int l) {
+    const float* at = b.anchors + ((long)(anchors + m / b.every) * p.H + h) * (DK * DV) +
+                      wave * (DV * 16) + 4 * l;
+#pragma unroll
+    for (int t = 0; t < VT; ++t) S[t] = *reinterpret_cast<const f32x4*>(at + t * 256);
+  };
   float gnext = 0.f;
   if (chunks > 0) {
     fetch(chunks - 1, threadIdx.x);
+    fetch_state(chunks - 1, l);
     const float g = decay_of(chunks - 1);
     gnext = decay_of(chunks - 2);
     if (wave == NW - 1) dec[(chunks - 1) & 1].make(g);
     // scores above the diagonal's tiles stay zero
     for (int i = threadIdx.x; i < C * TP::LD; i += NTH) Ps[i] = (E)0.f, Ms[i] = (E)0.f;
   }
+  loads_done();
   if (wave == 0 && l < C) sums[l] = 0.0;  // this wave alone uses them
   double pass = 0.0;  // <dS, S> at the chunk's end (wave 0)
 
@@ -147,15 +157,11 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     const int lc = lo & 15, lg = lo >> 4;
     const bool anchor = (m + 1) % b.every == 0 || m == chunks - 1;
     if (anchor) {
-      const float* at = b.anchors + ((long)anchor_of(p, c, m, b.every, C) * p.H + h) * (DK * DV) +
-                        wave * (DV * 16) + 4 * lo;
       float x = 0.f;
 #pragma unroll
-      for (int t = 0; t < VT; ++t) {
-        const f32x4 S = *reinterpret_cast<const f32x4*>(at + t * 256);
+      for (int t = 0; t < VT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x = fmaf(S[e], dS[t][e], x);
-      }
+        for (int e = 0; e < 4; ++e) x = fmaf(S[t][e], dS[t][e], x);
       x = group_sum(row_sum(x));
       if (lo == 0) cs[m & 1][wave] = x;
     }
@@ -172,6 +178,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     const float a = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
         ars, lo < len ? (uint32_t)(lo * p.H * 4) : kNoColumn, 0, 0));
     fetch(m - 1, tid);
+    if (m > 0 && m % b.every == 0) fetch_state(m - 1, lo);
 
     lower_tiles<TT, NW, true>(wave, [&](auto count, int first) {
       constexpr int N = decltype(count)::value;
@@ -265,7 +272,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
         for (int s = 0; s < KS; ++s)
           if (KF * (s + 1) > 16 * t)
             acc[t] = Mx<E>::mma(own[s], TP::tr(Ms, KF * s, 16 * t, lo), acc[t]);
-        store4<G>(rs, col < p.Dk ? (uint32_t)((16 * t + lc) * (int)sg + col) * (int)sizeof(G)
+        store4<G>(rs, col < p.Dk ? (row_at(16 * t + lc, sg) + col) * (int)sizeof(G)
                                  : kNoColumn, acc[t]);
       }
     }
@@ -296,7 +303,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
           if (KF * (s + 1) > 16 * t)
             acc[t] = Mx<E>::mma(of[s], TP::tr(Ps, KF * s, 16 * t, lo), acc[t]);
         const int col = 16 * vt + 4 * lg;
-        store4<E>(rs, col < p.Dv ? (uint32_t)((16 * t + lc) * (int)so + col) * (int)sizeof(E)
+        store4<E>(rs, col < p.Dv ? (row_at(16 * t + lc, so) + col) * (int)sizeof(E)
                                  : kNoColumn, acc[t]);
       }
     }

@@ -192,6 +192,12 @@ struct Rows {
   }
 };
 
+// Element offset of a row of a chunk: fewer than 64 rows, less than 2^23 elements apart, in one 24-bit
+// multiplication.
+__device__ __forceinline__ uint32_t row_at(int row, int64_t stride) {
+  return __umul24((uint32_t)row, (uint32_t)stride);
+}
+
 // Four consecutive columns of a row, rounded once, through a buffer resource that drops rows past
 // the chunk's end.
 template <typename E>
@@ -303,15 +309,19 @@ inline int group_of(const LinearProblem& p, int slabs, int blocks) {
   return group;
 }
 
+// Waits for every load.  Before a loop that keeps loads in flight: its waits then count the loop's own
+// loads and stores, and need not suit a first round that came without stores as well, which would have
+// each later round wait for the stores of the one before.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// The slot of the state kept at the end of a segment's chunk m (slots of the form of ssm.h, every * C
-// tokens long; a segment is no longer than that or a multiple of it).
-__device__ __forceinline__ int anchor_of(const LinearProblem& p, const Chunk& c, int m, int every,
-                                         int C) {
+// The slot of the state kept at the end of a segment's chunk m is this + m / every (slots of the form of
+// ssm.h, every * C tokens long; a segment is no longer than that or a multiple of it).
+__device__ __forceinline__ int first_anchor(const LinearProblem& p, const Chunk& c, int every, int C) {
   const ChunkMap map = {p.cu, p.T, p.Ttot, p.N, every * C};
   const int first = p.cu ? chunk_first(map, c.n) : c.n * chunk_count(p.T, every * C);
-  return uniform(first + (c.t0 - c.bos) / (every * C) + m / every);
+  return uniform(first + (c.t0 - c.bos) / (every * C));
 }
 
 // A wave's share of the TT (TT + 1) / 2 lower tiles of a chunk's scores, every NW-th: handed to `f` at

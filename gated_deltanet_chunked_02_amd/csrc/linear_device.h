@@ -41,9 +41,13 @@ template <> struct Mx<float> {
 };
 
 // A tile of rows in LDS, D values each.  In bf16 a row has no padding and its 16-byte pieces are
-// exchanged by the row (piece j lies at j ^ turn(row)), so that no two of the lanes that one cycle
-// serves meet in a bank: not the 8 rows of a row fragment's cycle, nor the 4 rows x 4 pieces of a
-// transposing read's.  fp32 rows, read transposed one value at a time, are padded by 16 bytes.
+// exchanged by the row (piece j lies at j ^ turn(row)).  LDS gives 256 bytes a cycle where the lanes it
+// serves in one have banks of their own: for a row fragment, rows 0-3 and 12-15 of one piece with rows
+// 4-11 of its neighbour (or the other way round), hence turns that agree in rows r and r + 4 but differ
+// otherwise; for a transposing read of two pieces, 4 rows each of two lane groups (4 and 2 cycles a
+// read, with none lost).  A transposing read of halves of four pieces (tr_state) and a write of halves
+// take twice their least, whatever the order.  fp32 rows, read transposed one value at a time, are padded
+// by 16 bytes.
 // l: the lane, or the lane made opaque in a loop, so that addresses are made where they are used and
 // not kept in registers throughout.
 template <typename E, int D>
@@ -51,8 +55,8 @@ struct Tile {
   static constexpr int LD = sizeof(E) == 2 ? D : D + 4;
   static __device__ __forceinline__ int turn(int row) {
     if constexpr (sizeof(E) == 4) return 0;
-    if constexpr (D == 64) return (row >> 1 & 1) * 4 + (row >> 2 & 3);
-    return (row & 3) * 4 + (row >> 2 & 3);
+    if constexpr (D == 64) return (row >> 3 & 1) * 4 + (row >> 1 & 1) * 2 + (row & 1);
+    return (row >> 3 & 1) * 9 + (row & 3) * 2;
   }
   // Element offset of piece j (16 bytes) of a row.
   static __device__ __forceinline__ int piece(int row, int j) {
@@ -96,9 +100,9 @@ struct Tile {
   }
 
  private:
-  // turn(row + 4) = turn(row) ^ 1 for the rows of the first half
+  // turn(row + 4) = turn(row) for the rows of the first half
   static __device__ __forceinline__ bf16x8 pair(const E* row, int j) {
-    const bf16x4 a = read_tr4(row + j * 8), b = read_tr4(row + 4 * LD + (j ^ 1) * 8);
+    const bf16x4 a = read_tr4(row + j * 8), b = read_tr4(row + 4 * LD + j * 8);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   static __device__ __forceinline__ f32x4 column(const E* p) {

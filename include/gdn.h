@@ -2,7 +2,9 @@
  * libgdn — chunked Gated DeltaNet on AMD Instinct MI355X (gfx950): the forward pass, its
  * backward pass, the decode operator with in-kernel gates and the causal conv1d before it; and
  * the operators of a selective state-space layer: the scan for prompts, its gradient and its
- * single-token form, the conv1d's gradient, and the group norm after a mixing layer.
+ * single-token form, the conv1d's gradient, and the group norm after a mixing layer; and those of a
+ * linear attention block: the attention with a decay for each head for prompts, its gradient and its
+ * single-token form, and the norms before and after a block with its gate and residual scale.
  *
  * The operation (one call): for every sequence n and value head h, with q/k head
  * hk = h / (H / Hg), starting from S = h0[n, h]^T (zero when h0 is NULL), for each token t
@@ -363,9 +365,11 @@ size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_desc* d, gdn_status* 
  *   dh0     [N, H, Dk, Dv] f32, or NULL (not written); may be dht's buffer
  * Dk and Dv up to 128 (GDN_ERR_UNSUPPORTED beyond).  Sums have a fixed order (no atomics).  Gradients
  * of tokens of a packed batch that no sequence has are not written.
- * The workspace holds the state at every chunk's start in fp32: 4 Dk Dv bytes (sizes rounded up to 64
- * or 128) a value head and 64 tokens (32 in f32), 1 KB a token and head of 128 x 128; and, where q/k
- * heads are shared, every value head's dq and dk in fp32, 8 Dk bytes a token and head. */
+ * The workspace holds a state in fp32 for every 512 tokens of a sequence (256 in f32; fewer where it is
+ * split into shorter segments): 4 Dk Dv bytes a value head, sizes rounded up to 64 or 128, which is 128
+ * bytes a token and head of 128 x 128; a number for each token and head; where sequences are split, two
+ * more states a segment; and, where q/k heads are shared, every value head's dq and dk in fp32, 8 Dk
+ * bytes a token and head. */
 gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const void* k,
                                const void* v, const float* g, const float* h0,
                                const int32_t* cu_seqlens, const void* dout, const float* dht,

@@ -229,6 +229,7 @@ gdn_status gdn_linear_attn_fwd(const gdn_linear_desc* d, const void* q, const vo
   p.cu = cu_seqlens;
   p.o = o;
   p.ht = ht;
+  p.direct = !h0 || h0 != ht;
   return gdn::launch_linear_fwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
@@ -280,6 +281,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const vo
   p.g = g;
   p.h0 = h0;
   p.cu = cu_seqlens;
+  p.direct = true;  // this call writes no final states
   gdn::LinearBwd b;
   b.dout = dout;
   b.dht = dht;
@@ -288,6 +290,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const vo
   b.dv = dv;
   b.dg = dg;
   b.dh0 = dh0;
+  b.direct = !dht || dht != dh0;
   b.grads = at(L.grads);
   b.anchors = at(L.anchors);
   b.a = at(L.a);

@@ -33,6 +33,7 @@ struct LinearProblem {
   void* o;
   float* ht;           // [N, H, Dk, Dv] or null
   float* states;       // workspace: [slots, H, Dk, Dv], each segment's own end state, then its start
+  bool direct;         // first segments start from h0 itself: no other reads it after ht is written
   float* sums;         // workspace: [slots, H], each segment's sum of log2 decays
 };
 
@@ -47,6 +48,7 @@ struct LinearBwd {
   float* dg;           // [H] or [B, T, H], or null
   float* dh0;          // or null
   float* grads;        // workspace: [slots, H, Dk, Dv], as states but from the ends
+  bool direct;         // last segments end with dht itself, likewise
   float* anchors;      // workspace: the state at every `every`-th chunk's end, in the kernels' tile order
   float* a;            // workspace: [Ttot, H] what q . dq takes from before the chunk
   int every;

@@ -66,9 +66,10 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   // The state in memory is [Dk, Dv]: this one's rows (GRAD: its columns) are the first axis.  Rows past
   // the head lie past the buffer, or are sent there.
   f32x4 S[CW][KT];
-  const float* from = p.Lc != kScanNoSplit ? p.states + ((long)slot * p.H + h) * cell
-                      : p.h0               ? p.h0 + ((long)c.n * p.H + h) * cell
-                                           : nullptr;
+  const bool made = p.Lc != kScanNoSplit && (c.i > 0 || !p.direct);
+  const float* from = made   ? p.states + ((long)slot * p.H + h) * cell
+                      : p.h0 ? p.h0 + ((long)c.n * p.H + h) * cell
+                             : nullptr;
   const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
 #pragma unroll
@@ -313,10 +314,12 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
 
 // Start states from the segments' own end states, in place: a thread has four values of a state and
 // walks its sequence's segments, four loads ahead of the one it is at.  The grid's second row makes the
-// gradients at the segments' ends from their own shares, last to first.
+// gradients at the segments' ends from their own shares, last to first.  Where the passes after this
+// one take the first segment's start (the last one's end) from the caller's buffer, it is not copied.
 struct LinearEnds {
   const float* from;  // dht or null
   float* grads;
+  bool direct;
 };
 __global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p, LinearEnds b) {
   constexpr int AHEAD = 4;
@@ -325,11 +328,12 @@ __global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p, LinearE
   const int nh = blockIdx.x / blocks, n = nh / p.H, h = nh - n * p.H;
   const long at = ((long)(blockIdx.x - nh * blocks) * 256 + threadIdx.x) * 4;
   if (at >= cell) return;
-  const bool back = blockIdx.y != 0;
+  const bool back = blockIdx.y != 0, direct = back ? b.direct : p.direct;
   const ChunkMap m = {p.cu, p.T, p.Ttot, p.N, p.Lc};
   int bos, eos;
   chunk_seq(m, n, bos, eos);
   const int count = chunk_count(eos - bos, p.Lc);
+  if (count == 1 && direct) return;
   const int first = p.cu ? chunk_first(m, n) : n * count;
   const float* from = back ? b.from : p.h0;
   float* states = back ? b.grads : p.states;
@@ -349,7 +353,7 @@ __global__ __launch_bounds__(256) void k_linear_compose(LinearProblem p, LinearE
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j)
       if (i + j < count) {
-        *reinterpret_cast<f32x4*>(states + slot(i + j) * cell + at) = s;
+        if (i + j > 0 || !direct) *reinterpret_cast<f32x4*>(states + slot(i + j) * cell + at) = s;
         if (i + j + 1 < count) s = s * exp2_f32(keep[j]) + own[j];
       }
   }
@@ -566,6 +570,7 @@ hipError_t launch_linear_states(const LinearProblem& p, const LinearBwd* b, hipS
     back.own = b->grads;
     ends.from = b->dht;
     ends.grads = b->grads;
+    ends.direct = b->direct;
   }
   const hipError_t e = p.f32 ? launch_state_e<float>(p, a, b ? &back : nullptr, st)
                              : launch_state_e<bf16>(p, a, b ? &back : nullptr, st);

@@ -87,9 +87,10 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   const int hk = h / (p.H / p.Hg);
   const long cell = (long)p.Dk * p.Dv;
 
-  const float* from = p.Lc != kScanNoSplit ? b.grads + (long)unit * cell
-                      : b.dht              ? b.dht + ((long)c.n * p.H + h) * cell
-                                           : nullptr;
+  const bool made = p.Lc != kScanNoSplit && (c.i + 1 < c.count || !b.direct);
+  const float* from = made    ? b.grads + (long)unit * cell
+                      : b.dht ? b.dht + ((long)c.n * p.H + h) * cell
+                              : nullptr;
   // a state's rows through a buffer: this lane's, four columns at a time
   const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);

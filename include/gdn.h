@@ -320,8 +320,8 @@ gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const fl
  * pointers aligned to 16 bytes (g, cu_seqlens, indices: 4) and rows a multiple of 16 bytes apart.
  * GDN_ERR_UNSUPPORTED beyond 2^30 tokens, 65536 sequences, rows of 2^23 elements or launches of 2^32
  * threads.  Errors are returned before any launch; nothing is synchronised or allocated.
- * q, k, v, g, o are required unless B*T = 0.  h0 and ht may be the same buffer.  o of tokens of a
- * packed batch that no sequence has is not written.
+ * q, k, v, g, o are required unless B*T = 0.  h0 and ht may be the same buffer; no other output may
+ * overlap an input.  o of tokens of a packed batch that no sequence has is not written.
  * States and sums are fp32.  In bf16, the scores within a chunk of 64 tokens and the state that meets
  * q are each rounded once to bf16 on their way to o (relative error of o about 2.4e-3, of which its own
  * rounding is 1.7e-3); ht is as exact as fp32 sums.  Few or long sequences are split into segments

@@ -13,14 +13,20 @@
 // k_linear_fwd: a workgroup has one head of one segment of a sequence and up to 128 of its value
 // columns, 16 a wave, whose state stays in registers (as tiles that are operands themselves,
 // linear_device.h) from the segment's first chunk to its last.  q, k and v go through LDS, the next
-// chunk's in registers meanwhile; the C x C scores are shared out over the waves and come back as
-// bf16.  Two tensors are rounded to bf16 on the way to o, the scores and the state that meets q, one
-// rounding on each of the two paths; the state itself and what is added to it are held to fp32's last
-// bits (v times its decay enters as three bf16 terms).
+// chunk's in registers meanwhile; the C x C scores are shared out over the waves and come back as two
+// bf16 terms.  One tensor is rounded to bf16 on the way to o, the state that meets q (its rounding
+// errors average over Dk rows; a second term took 8 x 2048 tokens from 165 to 180 us); the state itself
+// and what is added to it are held to fp32's last bits (v times its decay enters as three bf16 terms).
 //
 // Few or long sequences are cut into segments: k_linear_state makes each segment's own end state
 // (k and v alone), k_linear_compose turns those into start states in order, and k_linear_fwd runs
 // the segments side by side.
+//
+// Measured (bf16, heads of 128 x 128): 8 x 2048 tokens of 32 heads 155 us in a run of calls, whose loads
+// and stores alone take 113 with this order of accesses (4.7 TB/s), the matrix units busy 22 % and the
+// vector units 36 %; 16384 tokens of 32 heads 65 + 12 + 134 us.  Four waves of 32 columns instead of
+// eight of 16 took 170; a single barrier a chunk, with two or three buffers of everything, no less; 64
+// narrow heads (4096 tokens, 64 columns) are one wave a SIMD and wait on each other's results.
 #include "linear_device.h"
 
 namespace gdn {
@@ -49,7 +55,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   __shared__ __align__(256) E Ks[C * TK::LD];
   __shared__ __align__(256) E Vs[C * TV::LD];
   __shared__ __align__(256) E Xs[GRAD ? C * TV::LD : 1];
-  __shared__ __align__(256) E Ps[C * TP::LD];
+  __shared__ Scores<E, C> Ps;
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ float as[GRAD ? NW : 1][GRAD ? C : 1];
 
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
     gnext = decay_of(1);
     if (wave == NW - 1) dec[0].make(g);
     // scores above the diagonal's tiles are never written, and read where a product's k covers two
-    for (int i = threadIdx.x; i < C * TP::LD; i += NTH) Ps[i] = (E)0.f;
+    Ps.clear(threadIdx.x, NTH);
   }
   loads_done();
 
@@ -167,7 +173,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
           const float x2 = a[n][e] * exp2_f32((float)(Gi - d.G[j + e]));
           a[n][e] = j + e <= i ? x2 * p.scale : 0.f;
         }
-        put4<E, C>(Ps, i, j, a[n]);
+        Ps.put(i, j, a[n]);
       }
     });
     const float g = gnext;
@@ -239,9 +245,12 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
 #pragma unroll
       for (int s = 0; s < KS; ++s)
         if (KF * s < 16 * (t + 1)) {
-          const frag b = TP::ld(Ps, 16 * t, KF * s, lo);
 #pragma unroll
-          for (int w = 0; w < CW; ++w) acc[w][t] = Mx<E>::mma(vf[w][s], b, acc[w][t]);
+          for (int e = Ps.TERMS - 1; e >= 0; --e) {
+            const frag b = TP::ld(Ps.m[e], 16 * t, KF * s, lo);
+#pragma unroll
+            for (int w = 0; w < CW; ++w) acc[w][t] = Mx<E>::mma(vf[w][s], b, acc[w][t]);
+          }
         }
 #pragma unroll
       for (int w = 0; w < CW; ++w) {

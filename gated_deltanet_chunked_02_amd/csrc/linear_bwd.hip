@@ -26,7 +26,13 @@
 //
 // dS is held by key rows: a wave has 16 of them and all value columns, so the product over the value
 // columns (dK) takes it from registers as three bf16 terms (its b is a term of dg); the one over key rows
-// (dV) takes a copy rounded to bf16 from LDS.  Rounded to bf16 are that copy, M and P, once each.
+// (dV) takes a copy rounded to bf16 from LDS, the one rounding on any way to an output.  M and P go
+// through LDS as two terms.
+//
+// Measured (8 x 2048 tokens, 32 heads of 128 x 128, bf16): dQ's pass 226 us and this one 310 to 320 in a
+// run of calls, a workgroup a CU (140 KB of LDS), vector units busy 40 %, matrix units 19 %, LDS 25 %, the
+// waves waiting 43 % of their cycles.  Left out one at a time, the scores took 37 us of it, dK's product
+// 35, dV's 25, dS's update 55; loads, stores and what goes through LDS 195.
 #include "linear_device.h"
 
 namespace gdn {
@@ -68,8 +74,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   __shared__ __align__(256) E Vs[C * TV::LD];
   __shared__ __align__(256) E Os[C * TV::LD];   // dO
   __shared__ __align__(256) E Ds[DK * TV::LD];  // dS, rounded
-  __shared__ __align__(256) E Ps[C * TP::LD];
-  __shared__ __align__(256) E Ms[C * TP::LD];
+  __shared__ Scores<E, C> Ps, Ms;
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ double rows[TT][C];  // E summed over a tile's columns, by tile column
   __shared__ double cols[TT][C];  // and over its rows, by tile row
@@ -143,7 +148,8 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     gnext = decay_of(chunks - 2);
     if (wave == NW - 1) dec[(chunks - 1) & 1].make(g);
     // scores above the diagonal's tiles stay zero
-    for (int i = threadIdx.x; i < C * TP::LD; i += NTH) Ps[i] = (E)0.f, Ms[i] = (E)0.f;
+    Ps.clear(threadIdx.x, NTH);
+    Ms.clear(threadIdx.x, NTH);
   }
   loads_done();
   if (wave == 0 && l < C) sums[l] = 0.0;  // this wave alone uses them
@@ -216,8 +222,8 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
           mm[e] = j + e <= i ? ov[n][e] * w : 0.f;
           ee[e] = j + e < i ? mm[e] * qk[n][e] : 0.f;
         }
-        put4<E, C>(Ps, i, j, pp);
-        put4<E, C>(Ms, i, j, mm);
+        Ps.put(i, j, pp);
+        Ms.put(i, j, mm);
         double r = ((double)ee[0] + ee[1]) + ((double)ee[2] + ee[3]);
         r += __shfl_xor(r, 16);
         r += __shfl_xor(r, 32);
@@ -272,7 +278,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
 #pragma unroll
         for (int s = 0; s < KS; ++s)
           if (KF * (s + 1) > 16 * t)
-            acc[t] = Mx<E>::mma(own[s], TP::tr(Ms, KF * s, 16 * t, lo), acc[t]);
+#pragma unroll
+            for (int e = Ms.TERMS - 1; e >= 0; --e)
+              acc[t] = Mx<E>::mma(own[s], TP::tr(Ms.m[e], KF * s, 16 * t, lo), acc[t]);
         store4<G>(rs, col < p.Dk ? (row_at(16 * t + lc, sg) + col) * (int)sizeof(G)
                                  : kNoColumn, acc[t]);
       }
@@ -302,7 +310,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
 #pragma unroll
         for (int s = 0; s < KS; ++s)
           if (KF * (s + 1) > 16 * t)
-            acc[t] = Mx<E>::mma(of[s], TP::tr(Ps, KF * s, 16 * t, lo), acc[t]);
+#pragma unroll
+            for (int e = Ps.TERMS - 1; e >= 0; --e)
+              acc[t] = Mx<E>::mma(of[s], TP::tr(Ps.m[e], KF * s, 16 * t, lo), acc[t]);
         const int col = 16 * vt + 4 * lg;
         store4<E>(rs, col < p.Dv ? (row_at(16 * t + lc, so) + col) * (int)sizeof(E)
                                  : kNoColumn, acc[t]);

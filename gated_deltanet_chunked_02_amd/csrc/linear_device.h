@@ -224,6 +224,24 @@ __device__ __forceinline__ void put4(E* m, int row, int col, f32x4 x) {
     *reinterpret_cast<f32x4*>(to) = x;
 }
 
+// Scores in LDS: C x C values as two bf16 terms (16 bits or more of each), or as themselves in fp32.  One
+// term would be a rounding that all of a token's columns share, which shows in a short sequence's o.
+template <typename E, int C>
+struct Scores {
+  typedef Tile<E, C> T;
+  static constexpr int TERMS = sizeof(E) == 2 ? 2 : 1;
+  __align__(256) E m[TERMS][C * T::LD];
+  __device__ __forceinline__ void clear(int t, int threads) {
+    for (int i = t; i < TERMS * C * T::LD; i += threads) m[0][i] = (E)0.f;
+  }
+  __device__ __forceinline__ void put(int row, int col, f32x4 x) {
+    put4<E, C>(m[0], row, col, x);
+    if constexpr (TERMS == 2) {
+      const bf16x4 b = __builtin_convertvector(x, bf16x4);
+      put4<E, C>(m[TERMS - 1], row, col, x - __builtin_convertvector(b, f32x4));
+    }
+  }
+};
 
 __device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
 

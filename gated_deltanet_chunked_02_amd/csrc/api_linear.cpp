@@ -102,7 +102,7 @@ void plan_fwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, slabs_of(*p)
 void plan_bwd(gdn::LinearProblem* p, bool packed) {
   plan(p, packed, 1, kBwdFill);
   // a segment holds whole spans between the states kept for the gradient, or is one
-  const int span = gdn::kLinearAnchor * gdn::linear_chunk(p->f32);
+  const int span = gdn::linear_anchor(*p) * gdn::linear_chunk(p->f32);
   if (p->Lc != gdn::kScanNoSplit && p->Lc > span) {
     p->Lc = (p->Lc + span - 1) / span * span;
     if (p->Lc >= (packed ? p->Ttot : p->T)) p->Lc = gdn::kScanNoSplit;
@@ -147,9 +147,9 @@ BwdLayout bwd_layout(const gdn::LinearProblem& p, bool packed) {
     return at;
   };
   const size_t heads = (size_t)p.slots * p.H;
-  // the states kept for the gradient: at every 8th chunk's end, or a shorter segment's
+  // the states kept for the gradient: at some chunks' ends, or a shorter segment's
   const int C = gdn::linear_chunk(p.f32);
-  L.every = p.Lc < gdn::kLinearAnchor * C ? p.Lc / C : gdn::kLinearAnchor;
+  L.every = p.Lc < gdn::linear_anchor(p) * C ? p.Lc / C : gdn::linear_anchor(p);
   const size_t span = (size_t)L.every * C;
   const size_t anchors = p.Ttot == 0 ? 0
                          : packed    ? (size_t)p.Ttot / span + p.N
@@ -159,9 +159,9 @@ BwdLayout bwd_layout(const gdn::LinearProblem& p, bool packed) {
   L.sums = take(split ? heads * 4 : 0);
   L.grads = take(split ? heads * p.Dk * p.Dv * 4 : 0);
   L.anchors = take(anchors * p.H * gdn::linear_tile(p.Dk) * gdn::linear_tile(p.Dv) * 4);
-  L.a = take((size_t)p.Ttot * p.H * 4);
+  L.a = take((size_t)p.Ttot * p.H * 8);
   L.part = take(p.H != p.Hg ? (size_t)p.Ttot * p.H * p.Dk * 8 : 0);
-  L.dgp = take(p.head_decay ? heads * 4 : 0);
+  L.dgp = take(p.head_decay ? heads * 8 : 0);
   L.total = o;
   return L;
 }
@@ -293,10 +293,10 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const vo
   b.direct = !dht || dht != dh0;
   b.grads = at(L.grads);
   b.anchors = at(L.anchors);
-  b.a = at(L.a);
+  b.a = reinterpret_cast<double*>(ws + L.a);
   b.every = L.every;
   b.part = at(L.part);
-  b.dgp = at(L.dgp);
+  b.dgp = reinterpret_cast<double*>(ws + L.dgp);
   return gdn::launch_linear_bwd(p, b, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 

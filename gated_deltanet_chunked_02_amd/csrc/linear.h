@@ -11,7 +11,9 @@ namespace gdn {
 constexpr int kLinearChunk = 64;     // tokens of a chunk in bf16
 constexpr int kLinearChunkF32 = 32;  // in fp32, whose tiles take twice the LDS
 constexpr int kLinearSlab = 128;     // value columns of a workgroup, at most
-constexpr int kLinearAnchor = 8;     // chunks from one state kept for the gradient to the next, at most
+// Chunks from one state kept for the gradient to the next, at most.  A head's own decay gathers what the
+// differences between them are off by over all tokens, so it has twice as many.
+constexpr int kLinearAnchor = 8, kLinearAnchorHead = 4;
 
 // Segments are chunks of Lc tokens (a multiple of the tile chunk, or kScanNoSplit for whole
 // sequences) with the slots of ScanProblem (ssm.h); tile chunks have slots of the same form with the
@@ -50,10 +52,10 @@ struct LinearBwd {
   float* grads;        // workspace: [slots, H, Dk, Dv], as states but from the ends
   bool direct;         // last segments end with dht itself, likewise
   float* anchors;      // workspace: the state at every `every`-th chunk's end, in the kernels' tile order
-  float* a;            // workspace: [Ttot, H] what q . dq takes from before the chunk
+  double* a;           // workspace: [Ttot, H] what q . dq takes from before the chunk
   int every;
   float* part;         // workspace: [2, Ttot, H, Dk] dq and dk of every value head (shared q/k heads)
-  float* dgp;          // workspace: [slots, H] sums of dg (head_decay)
+  double* dgp;         // workspace: [slots, H] sums of dg (head_decay)
 };
 
 // A pass over segments that makes states only: sums of x_t y_t^T.
@@ -76,7 +78,7 @@ struct LinearRun {
   int64_t sq, sk, sv, sx;
   int Dk, Dv, qrep, vrep;
   void* out;           // [B, T, H, Dv]
-  float* a;
+  double* a;
   float* anchors;
   int every;
 };
@@ -85,6 +87,9 @@ hipError_t launch_linear_dq(const LinearProblem& p, const LinearBwd& b, hipStrea
 
 // Tile sizes of the backward: 64 or 128 for head sizes up to that.
 inline int linear_tile(int D) { return D <= 64 ? 64 : 128; }
+inline int linear_anchor(const LinearProblem& p) {
+  return p.head_decay ? kLinearAnchorHead : kLinearAnchor;
+}
 inline int linear_chunk(bool f32) { return f32 ? kLinearChunkF32 : kLinearChunk; }
 hipError_t launch_linear_bwd(const LinearProblem& p, const LinearBwd& b, hipStream_t st);
 

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   __shared__ __align__(256) E Xs[GRAD ? C * TV::LD : 1];
   __shared__ Scores<E, C> Ps;
   __shared__ __align__(16) Decays<C> dec[2];
-  __shared__ float as[GRAD ? NW : 1][GRAD ? C : 1];
+  __shared__ double as[GRAD ? NW : 1][GRAD ? C : 1];
 
   const int slabs = (r.Dv + DV - 1) / DV;
   const int unit = unit_of(blockIdx.x, gridDim.x, p.group);
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       const float in = p.scale * d.into[16 * t + lc];
-      float sum = 0.f;
+      double sum = 0.0;
 #pragma unroll
       for (int w = 0; w < CW; ++w) {
         acc[w][t] *= in;
@@ -224,15 +224,15 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
     __syncthreads();
 
     if constexpr (GRAD) {  // a_t, from every wave's columns in order
-      float sum = 0.f;
+      double sum = 0.0;
       const int t = lo & (C - 1);
 #pragma unroll
       for (int w = 0; w < NW; ++w) sum += as[w][t];
       const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(
-          r.a + (c.t0 + (long)m * C) * p.H + h, 0, ((len - 1) * p.H + 1) * 4, 0x00020000);
-      __builtin_amdgcn_raw_buffer_store_b32(
-          __float_as_uint(sum), ars, wave == 0 && lo < len ? (uint32_t)(t * p.H * 4) : kNoColumn, 0,
-          0);
+          r.a + (c.t0 + (long)m * C) * p.H + h, 0, ((len - 1) * p.H + 1) * 8, 0x00020000);
+      __builtin_amdgcn_raw_buffer_store_b64(
+          __builtin_bit_cast(u32x2, sum), ars,
+          wave == 0 && lo < len ? (uint32_t)(t * p.H * 8) : kNoColumn, 0, 0);
     }
     frag vf[CW][KS];
 #pragma unroll

@@ -19,10 +19,14 @@
 //
 //   e^{G_C} <dS, S_start> = <dS, S_end> - sum b,    <dS, S>_start = <dS, S>_end + sum a - sum b,
 //
-// carried in fp64 from chunk to chunk and taken afresh every kLinearAnchor chunks, where the forward
+// carried in fp64 from chunk to chunk and taken afresh at the anchors (every 8 chunks), where the forward
 // pass leaves its state: a difference of sums over 512 tokens at most, each term good to fp32's last
-// bits, so dg keeps fp32's accuracy.  Within a chunk r cancels for the pairs on one side of t: both its
-// sums are taken in fp64 of the same fp32 values, so what is left has dg's own size.
+// bits, so dg keeps fp32's accuracy.  A head's own decay sums all of a sequence's dg, and with it one error
+// many times over: there anchors are twice as many, and what the carried value is off by at each is
+// taken off the sum, as having grown evenly since the last (dg of 64 heads, 824 tokens, fp32: relative
+// error 1.1e-6 without that, 4.5e-7 with it at every 8 chunks).  Within a chunk r cancels for the pairs on
+// one side of t: both its sums are taken in fp64 of the same fp32 values, so what is left has dg's own
+// size.
 //
 // dS is held by key rows: a wave has 16 of them and all value columns, so the product over the value
 // columns (dK) takes it from registers as three bf16 terms (its b is a term of dg); the one over key rows
@@ -78,7 +82,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ double rows[TT][C];  // E summed over a tile's columns, by tile column
   __shared__ double cols[TT][C];  // and over its rows, by tile row
-  __shared__ float bs[NW][C], cs[2][NW];  // two anchors may follow each other
+  __shared__ double bs[NW][C], cs[2][NW];  // two anchors may follow each other
   __shared__ double sums[C];  // of dg over the chunks (head_decay)
 
   const int unit = unit_of(blockIdx.x, gridDim.x, p.group);
@@ -86,7 +90,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   const int l = lane_id(), wave = uniform(wave_id());
   const Chunk c = uniform_chunk(p, slot);
   if (!c.ok) {
-    if (p.head_decay && threadIdx.x == 0) b.dgp[unit] = 0.f;
+    if (p.head_decay && threadIdx.x == 0) b.dgp[unit] = 0.0;
     return;
   }
   const int hk = h / (p.H / p.Hg);
@@ -154,6 +158,10 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   loads_done();
   if (wave == 0 && l < C) sums[l] = 0.0;  // this wave alone uses them
   double pass = 0.0;  // <dS, S> at the chunk's end (wave 0)
+  // What the carried value turns out to be off by at the next anchor had grown over the tokens since the
+  // last: half of it for each of them (head_decay, wave 0)
+  double off = 0.0;
+  int since = 0;
 
   for (int m = chunks - 1; m >= 0; --m) {
     const int len = min(C, c.len - m * C);
@@ -164,11 +172,11 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     const int lc = lo & 15, lg = lo >> 4;
     const bool anchor = (m + 1) % b.every == 0 || m == chunks - 1;
     if (anchor) {
-      float x = 0.f;
+      double x = 0.0;
 #pragma unroll
       for (int t = 0; t < VT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x = fmaf(S[t][e], dS[t][e], x);
+        for (int e = 0; e < 4; ++e) x = fma((double)S[t][e], (double)dS[t][e], x);
       x = group_sum(row_sum(x));
       if (lo == 0) cs[m & 1][wave] = x;
     }
@@ -181,9 +189,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     __syncthreads();
     // a of this chunk, for its last step
     const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(
-        b.a + (c.t0 + (long)m * C) * p.H + h, 0, ((len - 1) * p.H + 1) * 4, 0x00020000);
-    const float a = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        ars, lo < len ? (uint32_t)(lo * p.H * 4) : kNoColumn, 0, 0));
+        b.a + (c.t0 + (long)m * C) * p.H + h, 0, ((len - 1) * p.H + 1) * 8, 0x00020000);
+    const double a = __builtin_bit_cast(double, __builtin_amdgcn_raw_buffer_load_b64(
+        ars, lo < len ? (uint32_t)(lo * p.H * 8) : kNoColumn, 0, 0));
     fetch(m - 1, tid);
     if (m > 0 && m % b.every == 0) fetch_state(m - 1, lo);
 
@@ -261,7 +269,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       acc[t] *= d.left[16 * t + lc];
-      const float r = group_sum(dot4<E, DK>(Ks, 16 * t + lc, 16 * wave + 4 * lg, acc[t]));
+      const double r = group_sum((double)dot4<E, DK>(Ks, 16 * t + lc, 16 * wave + 4 * lg, acc[t]));
       if (lg == 0) bs[wave][16 * t + lc] = r;
     }
     __syncthreads();
@@ -350,10 +358,14 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
 #pragma unroll
       for (int w = 0; w < NW; ++w) down += bs[w][t];
       if (anchor) {
-        pass = 0.0;
+        double x = 0.0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) pass += cs[m & 1][w];
+        for (int w = 0; w < NW; ++w) x += cs[m & 1][w];
+        off += (x - pass) * since;
+        pass = x;
+        since = 0;
       }
+      since += len;
       up = lo < len ? up : 0.0;
       down = lo < len ? down : 0.0;
       in = lo < len ? in : 0.0;
@@ -372,9 +384,34 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     }
   }
 
-  if (p.head_decay && wave == 0) {
-    const double x = wave_incl_scan(l < C ? sums[l] : 0.0);
-    if (l == 63) b.dgp[unit] = (float)x;
+  if (p.head_decay) {
+    // the start's <dS, S> too
+    const float* at = c.i > 0 ? p.states + (long)unit * cell
+                      : p.h0  ? p.h0 + ((long)c.n * p.H + h) * cell
+                              : nullptr;
+    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(at), 0, at ? (int)cell * 4 : 0, 0x00020000);
+    double x = 0.0;
+#pragma unroll
+    for (int t = 0; t < VT; ++t) {
+      const f32x4 s0 = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          srs, tile_row(t, l) < p.Dv
+                   ? (uint32_t)((16 * wave + (l & 15)) * p.Dv + tile_row(t, l)) * 4 : kNoColumn, 0,
+          0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x = fma((double)s0[e], (double)dS[t][e], x);
+    }
+    x = group_sum(row_sum(x));
+    if (l == 0) cs[1][wave] = x;  // chunk 0 may be an anchor and has the other half
+    __syncthreads();
+    if (wave == 0) {
+      x = 0.0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) x += cs[1][w];
+      off += (x - pass) * since;
+      x = wave_incl_scan(l < C ? sums[l] : 0.0) + 0.5 * off;
+      if (l == 63) b.dgp[unit] = x;
+    }
   }
   if (b.dh0 && c.i == 0) {
     const __amdgpu_buffer_rsrc_t trs = __builtin_amdgcn_make_buffer_rsrc(
@@ -396,10 +433,17 @@ template <typename E>
 __global__ __launch_bounds__(kColumnThreads) void k_linear_sums(LinearProblem p, LinearBwd b, int first) {
   const int part = first + blockIdx.y;
   if (part == 2) {
+    __shared__ double sums[kColumnThreads / 64][64];
     if ((int)blockIdx.x >= (p.H + 63) / 64) return;
     const int c = blockIdx.x * 64 + lane_id();
-    const float s = column_sum(b.dgp, p.H, p.slots, c, p.H);
-    if (threadIdx.x < 64 && c < p.H) b.dg[c] = s;
+    double s = 0.0;
+    if (c < p.H)
+      for (int r = wave_id(); r < p.slots; r += kColumnThreads / 64) s += b.dgp[(long)r * p.H + c];
+    sums[wave_id()][lane_id()] = s;
+    __syncthreads();
+    if (threadIdx.x >= 64 || c >= p.H) return;
+    for (int w = 1; w < kColumnThreads / 64; ++w) s += sums[w][lane_id()];
+    b.dg[c] = (float)s;
     return;
   }
   const long vecs = (long)p.Hg * p.Dk / 4, total = p.cu ? min(max(p.cu[p.N], 0), p.Ttot) : p.Ttot;

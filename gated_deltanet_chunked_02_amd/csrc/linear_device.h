@@ -278,6 +278,12 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
+__device__ __forceinline__ double group_sum(double x) {
+  x += __shfl_xor(x, 16);
+  x += __shfl_xor(x, 32);
+  return x;
+}
+
 // A chunk's decays.  G_t, the sum of log2 decays up to token t, is held in fp64: the decay between
 // two tokens is a difference of two of them, which in fp32 would lose its last bits behind tokens of
 // strong decay.  A log2 decay below -1000 (an infinity, or a mask's lowest value: a state forgotten)

@@ -365,11 +365,11 @@ size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_desc* d, gdn_status* 
  *   dh0     [N, H, Dk, Dv] f32, or NULL (not written); may be dht's buffer
  * Dk and Dv up to 128 (GDN_ERR_UNSUPPORTED beyond).  Sums have a fixed order (no atomics).  Gradients
  * of tokens of a packed batch that no sequence has are not written.
- * The workspace holds a state in fp32 for every 512 tokens of a sequence (256 in f32; fewer where it is
- * split into shorter segments): 4 Dk Dv bytes a value head, sizes rounded up to 64 or 128, which is 128
- * bytes a token and head of 128 x 128; a number for each token and head; where sequences are split, two
- * more states a segment; and, where q/k heads are shared, every value head's dq and dk in fp32, 8 Dk
- * bytes a token and head. */
+ * The workspace holds a state in fp32 for every 512 tokens of a sequence (256 in f32; half of that with
+ * head_decay; fewer where it is split into shorter segments): 4 Dk Dv bytes a value head, sizes rounded
+ * up to 64 or 128, which is 128 bytes a token and head of 128 x 128; 8 bytes for each token and head;
+ * where sequences are split, two more states a segment; and, where q/k heads are shared, every value
+ * head's dq and dk in fp32, 8 Dk bytes a token and head. */
 gdn_status gdn_linear_attn_bwd(const gdn_linear_desc* d, const void* q, const void* k,
                                const void* v, const float* g, const float* h0,
                                const int32_t* cu_seqlens, const void* dout, const float* dht,

@@ -97,8 +97,12 @@ def test_linear_workspace():
     # a gradient keeps a state every 512 bf16 tokens, 256 fp32 ones
     plain = dict(B=8, N=8, T=2048, H=32, Hg=32, Dk=128, Dv=128)
     states = 8 * 4 * 32 * 128 * 128 * 4
-    assert size(SIZES[1], linear_desc(**plain)) == (0, states + 8 * 2048 * 32 * 4)
-    assert size(SIZES[1], linear_desc(**{**plain, "dtype": 0})) == (0, 2 * states + 8 * 2048 * 32 * 4)
+    # (half of that where a head's own decay is wanted), and a number for each token and head
+    numbers = 8 * 2048 * 32 * 8
+    assert size(SIZES[1], linear_desc(**plain)) == (0, states + numbers)
+    assert size(SIZES[1], linear_desc(**{**plain, "dtype": 0})) == (0, 2 * states + numbers)
+    sums = 8 * 32 * 8  # of each sequence's dg
+    assert size(SIZES[1], linear_desc(**{**plain, "head_decay": 1})) == (0, 2 * states + numbers + sums)
 
 
 def test_linear_step_refusals():

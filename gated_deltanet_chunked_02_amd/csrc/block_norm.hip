@@ -20,8 +20,13 @@
 // follows from two more sums of the first reduction (E[dn w1 xh] is linear in E[dhat hat]), so it has
 // one exchange between waves, not two.
 //
-// Rows of more than 8192 values go through memory again instead (k_block_norm_wide*), the second
-// reading from the caches, their parameters' gradients through a workgroup's own partial row.
+// Rows of more than 8192 values go through memory again instead (k_block_norm_wide*), the second and
+// third reading from the caches, their parameters' gradients through a workgroup's own partial row.
+//
+// Measured: 16384 rows of 4096 channels, gated, bf16 130 us (5.1 TB/s), beside an fp32 stream 171 and, with
+// the gradient, 447 (5.3 TB/s).  Replayed from a graph, whose start is about 14 us of each: 8192 rows of
+// 8192 136 and 250 (no registers for the next row's loads); 4096 rows of 16384 205 and 513 (728 and 1221
+// with a value a thread at a time); 16384 rows of 1024 33 and 77.
 #include "block_norm.h"
 #include "ssm_device.h"
 
@@ -31,7 +36,8 @@ namespace {
 
 constexpr int kEach = 8;               // values a thread holds
 constexpr int kMostRow = 1024 * kEach;  // values of a row held in registers
-constexpr int kWide = 1024;             // threads of the wide kernels
+// Threads of the wide kernels: values loaded one at a time take registers for their offsets as well.
+constexpr int wide_threads(int VEC) { return VEC == 8 ? 1024 : 512; }
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -357,12 +363,14 @@ __global__ __launch_bounds__(MOST) void k_block_norm_bwd(BlockNormProblem p) {
   }
 }
 
-// One row a workgroup at a time, its values read again for each step.
-template <typename E, typename R>
-__global__ __launch_bounds__(kWide) void k_block_norm_wide(BlockNormProblem p) {
+// One row a workgroup at a time, in blocks of eight values a thread, read again for each
+// step.
+template <typename E, typename R, int VEC>
+__global__ __launch_bounds__(wide_threads(VEC)) void k_block_norm_wide(BlockNormProblem p) {
   __shared__ float lds[2][1][16];
+  constexpr int WIDE = wide_threads(VEC), BLOCK = WIDE * kEach;
   RowSum<1> sum{&lds};
-  const int C = p.C;
+  const int C = p.C, t = threadIdx.x;
   const float inv = 1.f / (float)C;
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const R* x = static_cast<const R*>(p.x) + (long)row * C;
@@ -370,86 +378,150 @@ __global__ __launch_bounds__(kWide) void k_block_norm_wide(BlockNormProblem p) {
     const E* g = static_cast<const E*>(p.gate) + row * p.sg;
     float s[1] = {0.f}, rstd1 = 1.f;
     if (p.h && p.post) {
-      for (int c = threadIdx.x; c < C; c += kWide) s[0] = fmaf((float)h[c], (float)h[c], s[0]);
-      sum(s, kWide / 64);
-      rstd1 = rsqrtf(s[0] * inv + p.eps);
-      if (p.rstd1 && threadIdx.x == 0) p.rstd1[row] = rstd1;
-    }
-    auto value = [&](int c) {
-      float v = (float)x[c];
-      if (p.h) {
-        const float a = (p.gate ? gate_act((float)g[c], p.silu) : 1.f) * (p.w1 ? p.w1[c] : 1.f) *
-                        (p.scale ? p.scale[c] : 1.f) * p.residual_scale;
-        v = fmaf((float)h[c] * rstd1, a, v);
+      for (int b = 0; b < C; b += BLOCK) {
+        Slice<E, VEC> hs;
+        hs.load(h + b, t, WIDE, C - b);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) s[0] = fmaf(hs[i], hs[i], s[0]);
       }
-      return v;
+      sum(s, WIDE / 64);
+      rstd1 = rsqrtf(s[0] * inv + p.eps);
+      if (p.rstd1 && t == 0) p.rstd1[row] = rstd1;
+    }
+    auto values = [&](int b, float (&v)[kEach]) {
+      Slice<R, VEC> xs;
+      xs.load(x + b, t, WIDE, C - b);
+      if (!p.h) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] = xs[i];
+        return;
+      }
+      Slice<E, VEC> hs, gs;
+      hs.load(h + b, t, WIDE, C - b);
+      if (p.gate) gs.load(g + b, t, WIDE, C - b);
+      float w[kEach], al[kEach];
+      params<VEC>(p.w1 ? p.w1 + b : nullptr, t, WIDE, C - b, w);
+      params<VEC>(p.scale ? p.scale + b : nullptr, t, WIDE, C - b, al);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const float a = (p.gate ? gate_act(gs[i], p.silu) : 1.f) * w[i] * al[i] * p.residual_scale;
+        v[i] = fmaf(hs[i] * rstd1, a, xs[i]);
+      }
     };
-    float rstd2 = 0.f;
+    float v[kEach], rstd2 = 0.f;
     if (p.y) {
       s[0] = 0.f;
-      for (int c = threadIdx.x; c < C; c += kWide) {
-        const float v = value(c);
-        s[0] = fmaf(v, v, s[0]);
+      for (int b = 0; b < C; b += BLOCK) {
+        values(b, v);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) s[0] = fmaf(v[i], v[i], s[0]);
       }
-      sum(s, kWide / 64);
+      sum(s, WIDE / 64);
       rstd2 = rsqrtf(s[0] * inv + p.eps);
-      if (p.rstd2 && threadIdx.x == 0) p.rstd2[row] = rstd2;
+      if (p.rstd2 && t == 0) p.rstd2[row] = rstd2;
     }
     // x' last: it may be x's buffer
-    for (int c = threadIdx.x; c < C; c += kWide) {
-      const float v = value(c);
-      if (p.y) static_cast<E*>(p.y)[(long)row * C + c] = (E)(v * (rstd2 * (p.w2 ? p.w2[c] : 1.f)));
-      if (p.h) static_cast<R*>(p.xo)[(long)row * C + c] = (R)v;
+    for (int b = 0; b < C; b += BLOCK) {
+      values(b, v);
+      if (p.h)
+        Slice<R, VEC>::store(static_cast<R*>(p.xo) + (long)row * C + b, t, WIDE, C - b, v);
+      if (p.y) {
+        float w[kEach];
+        params<VEC>(p.w2 ? p.w2 + b : nullptr, t, WIDE, C - b, w);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] *= rstd2 * w[i];
+        Slice<E, VEC>::store(static_cast<E*>(p.y) + (long)row * C + b, t, WIDE, C - b, v);
+      }
     }
   }
 }
 
-template <typename E, typename R>
-__global__ __launch_bounds__(kWide) void k_block_norm_wide_bwd(BlockNormProblem p) {
+struct No { static constexpr bool value = false; };
+struct Yes { static constexpr bool value = true; };
+
+// The parameters' gradients gather in the workgroup's partial row.
+template <typename E, typename R, int VEC>
+__global__ __launch_bounds__(wide_threads(VEC)) void k_block_norm_wide_bwd(BlockNormProblem p) {
   __shared__ float lds[2][3][16];
+  constexpr int WIDE = wide_threads(VEC), BLOCK = WIDE * kEach;
   RowSum<3> sum{&lds};
   const int C = p.C;
   const float inv = 1.f / (float)C;
   float* part = p.part + (long)blockIdx.x * 3 * C;
-  for (int c = threadIdx.x; c < 3 * C; c += kWide) part[c] = 0.f;
-  __syncthreads();
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const long at = (long)row * C;
-    const E* h = static_cast<const E*>(p.h) + row * p.sh;
-    const E* gt = static_cast<const E*>(p.gate) + row * p.sg;
     const float r1 = p.h && p.post ? p.rstd1[row] : 1.f, r2 = p.dy ? p.rstd2[row] : 0.f;
     float s[3] = {0.f, 0.f, 0.f}, m = 0.f, m1 = 0.f;
-    for (int step = 0; step < 2; ++step) {
-      for (int c = threadIdx.x; c < C; c += kWide) {
-        const float w1 = p.w1 ? p.w1[c] : 1.f, w2 = p.w2 ? p.w2[c] : 1.f;
-        const float al = (p.scale ? p.scale[c] : 1.f) * p.residual_scale;
-        const float g = p.gate ? (float)gt[c] : 1.f, a = p.gate ? gate_act(g, p.silu) : 1.f;
-        const float xh = p.h ? (float)h[c] * r1 : 0.f, n = xh * w1;
-        const float hat = fmaf(n * a, al, (float)static_cast<const R*>(p.x)[at + c]) * r2;
-        const float dy = p.dy ? (float)static_cast<const E*>(p.dy)[at + c] : 0.f;
-        float dR = fmaf(r2, dy * w2, p.dxo ? (float)static_cast<const R*>(p.dxo)[at + c] : 0.f);
-        if (step == 0) {
-          const float f = al * a * n;
-          s[0] = fmaf(dy * w2, hat, s[0]);
-          s[1] = fmaf(f, dR, s[1]);
-          s[2] = fmaf(f, hat, s[2]);
-        } else {
-          dR = fmaf(-hat, m, dR);
-          const float dz = al * dR, dn = dz * a;
-          part[c] = fmaf(dn, xh, part[c]);
-          part[C + c] = fmaf(dR * p.residual_scale, n * a, part[C + c]);
-          part[2 * C + c] = fmaf(dy, hat, part[2 * C + c]);
-          static_cast<R*>(p.dx)[at + c] = (R)dR;
-          if (p.h) static_cast<E*>(p.dh)[at + c] = (E)(p.post ? r1 * fmaf(dn, w1, -xh * m1) : dn);
-          if (p.gate) static_cast<E*>(p.dgate)[at + c] = (E)(dz * n * gate_slope(g, p.silu));
+    auto walk = [&](auto second) {  // three sums of the row, then what follows from them
+      constexpr bool SECOND = decltype(second)::value;
+      auto place = [] {  // offsets are made at each use
+        int t = threadIdx.x;
+        opaque(t);
+        return t;
+      };
+      for (int b = 0; b < C; b += BLOCK) {
+        Slice<R, VEC> xs, dxs;
+        Slice<E, VEC> hs, gs, dys;
+        float w1[kEach], al[kEach], w2[kEach];
+        xs.load(static_cast<const R*>(p.x) + at + b, place(), WIDE, C - b);
+        if (p.dxo) dxs.load(static_cast<const R*>(p.dxo) + at + b, place(), WIDE, C - b);
+        if (p.dy) dys.load(static_cast<const E*>(p.dy) + at + b, place(), WIDE, C - b);
+        if (p.h) hs.load(static_cast<const E*>(p.h) + row * p.sh + b, place(), WIDE, C - b);
+        if (p.gate) gs.load(static_cast<const E*>(p.gate) + row * p.sg + b, place(), WIDE, C - b);
+        params<VEC>(p.w1 ? p.w1 + b : nullptr, place(), WIDE, C - b, w1);
+        params<VEC>(p.scale ? p.scale + b : nullptr, place(), WIDE, C - b, al);
+        params<VEC>(p.w2 ? p.w2 + b : nullptr, place(), WIDE, C - b, w2);
+        float dR[kEach], dh[kEach], dg[kEach], d1[kEach], ds[kEach], d2[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const float alpha = al[i] * p.residual_scale;
+          const float a = p.gate ? gate_act(gs[i], p.silu) : 1.f;
+          const float xh = p.h ? hs[i] * r1 : 0.f, n = xh * w1[i];
+          const float hat = fmaf(n * a, alpha, xs[i]) * r2;
+          const float dy = p.dy ? dys[i] : 0.f;
+          dR[i] = fmaf(r2, dy * w2[i], p.dxo ? dxs[i] : 0.f);
+          if constexpr (!SECOND) {
+            const float f = alpha * a * n;
+            s[0] = fmaf(dy * w2[i], hat, s[0]);
+            s[1] = fmaf(f, dR[i], s[1]);
+            s[2] = fmaf(f, hat, s[2]);
+          } else {
+            dR[i] = fmaf(-hat, m, dR[i]);
+            const float dz = alpha * dR[i], dn = dz * a;
+            d1[i] = dn * xh;
+            ds[i] = dR[i] * p.residual_scale * (n * a);
+            d2[i] = dy * hat;
+            dg[i] = p.gate ? dz * n * gate_slope(gs[i], p.silu) : 0.f;
+            dh[i] = p.post ? r1 * fmaf(dn, w1[i], -xh * m1) : dn;
+          }
+        }
+        if constexpr (SECOND) {
+          auto gather = [&](float* to, float (&v)[kEach]) {
+            const int t = place();
+            if (row != (int)blockIdx.x) {
+              Slice<float, VEC> before;
+              before.load(to + b, t, WIDE, C - b);
+#pragma unroll
+              for (int i = 0; i < kEach; ++i) v[i] += before[i];
+            }
+            Slice<float, VEC>::store(to + b, t, WIDE, C - b, v);
+            sched_fence();
+          };
+          if (p.dw1) gather(part, d1);
+          if (p.dscale) gather(part + C, ds);
+          if (p.dw2) gather(part + 2 * C, d2);
+          Slice<R, VEC>::store(static_cast<R*>(p.dx) + at + b, place(), WIDE, C - b, dR);
+          if (p.h) Slice<E, VEC>::store(static_cast<E*>(p.dh) + at + b, place(), WIDE, C - b, dh);
+          if (p.gate)
+            Slice<E, VEC>::store(static_cast<E*>(p.dgate) + at + b, place(), WIDE, C - b, dg);
         }
       }
-      if (step == 0) {
-        sum(s, kWide / 64);
-        m = r2 * s[0] * inv;
-        m1 = (s[1] - m * s[2]) * inv;
-      }
-    }
+    };
+    walk(No());
+    sum(s, WIDE / 64);
+    m = r2 * s[0] * inv;
+    m1 = (s[1] - m * s[2]) * inv;
+    walk(Yes());
   }
 }
 
@@ -466,7 +538,10 @@ int waves_of(int C) { return (C + 64 * kEach - 1) / (64 * kEach); }
 // Workgroups: no more than run at once (32 waves a CU forward, 12 backward, by their registers), each
 // of one row a wave at least, in the backward, whose partial row of sums costs as much as a row, four.
 int blocks_of(const BlockNormProblem& p, bool backward) {
-  if (p.C > kMostRow) return p.rows < 512 ? p.rows : 512;
+  if (p.C > kMostRow) {
+    const int most = backward ? 256 : 512, want = backward ? (p.rows + 3) / 4 : p.rows;
+    return want < most ? want : most;
+  }
   const int waves = waves_of(p.C), each = waves == 1 ? 4 : 1, size = waves * each;
   const int most = 256 * (backward ? (size < 12 ? 12 / size : 1) : 32 / size);
   const long rows = each * (backward ? 4 : 1), want = (p.rows + rows - 1) / rows;
@@ -519,14 +594,22 @@ void run_parts(const BlockNormProblem& p, bool backward, hipStream_t st) {
     run<E, R, VEC, 2>(p, backward, st);
 }
 
+template <typename E, typename R, int VEC>
+void run_wide(const BlockNormProblem& p, bool backward, hipStream_t st) {
+  const int blocks = blocks_of(p, backward);
+  if (!backward)
+    k_block_norm_wide<E, R, VEC><<<blocks, wide_threads(VEC), 0, st>>>(p);
+  else
+    k_block_norm_wide_bwd<E, R, VEC><<<blocks, wide_threads(VEC), 0, st>>>(p);
+}
+
 template <typename E, typename R>
 void run_types(const BlockNormProblem& p, bool backward, hipStream_t st) {
   if (p.C > kMostRow) {
-    const int blocks = blocks_of(p, backward);
-    if (backward)
-      k_block_norm_wide_bwd<E, R><<<blocks, kWide, 0, st>>>(p);
+    if (vector_of(p) == 8)
+      run_wide<E, R, 8>(p, backward, st);
     else
-      k_block_norm_wide<E, R><<<blocks, kWide, 0, st>>>(p);
+      run_wide<E, R, 1>(p, backward, st);
     return;
   }
   switch (vector_of(p)) {

@@ -408,7 +408,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       x = 0.0;
 #pragma unroll
       for (int w = 0; w < NW; ++w) x += cs[1][w];
-      off += (x - pass) * since;
+      if (since > 0) off += (x - pass) * since;
       x = wave_incl_scan(l < C ? sums[l] : 0.0) + 0.5 * off;
       if (l == 63) b.dgp[unit] = x;
     }

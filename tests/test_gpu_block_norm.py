@@ -257,3 +257,25 @@ def test_rows_past_2_to_31_elements():
     b = gdn.block_norm_bwd(dy[end], None, x[end], h[end], a[2], a[3], post_norm=True)
     for s, t in zip((out, y, r1, r2, dx, dh), (*a, *b[:2])):
         assert torch.equal(s[end], t)
+
+
+@pytest.mark.parametrize("C", [64, 1024, 5120, 9000])
+def test_parameters_at_any_address(C):
+    """Parameters need their element's alignment only: slices of one buffer give the same bits."""
+    import gated_deltanet_chunked_02_amd as gdn
+    g = torch.Generator().manual_seed(C)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    x, h, gate, dy, dx = (n(37, C) for _ in range(5))
+    w = [n(C) for _ in range(3)]
+    buf = torch.zeros(3 * C + 9, device="cuda")
+    odd = [buf[i * (C + 3) + 1:][:C] for i in range(3)]
+    for a, b in zip(odd, w):
+        a.copy_(b)
+    got = []
+    for weight, post, scale in (w, odd):
+        kw = dict(weight=weight, post_norm=True, post_weight=post, gate=gate, activation="silu",
+                  scale=scale)
+        out, y, p, q = gdn.block_norm(x, h, **kw)
+        got.append([out, y, p, q, *gdn.block_norm_bwd(dy, dx, x, h, p, q, **kw)])
+    for i, (a, b) in enumerate(zip(*got)):
+        assert torch.equal(a, b), i

@@ -61,3 +61,26 @@ def test_states_in_one_buffer(T, lens, H, Hg, dtype, head):
         assert torch.equal(a, b), i
     if lens:
         assert torch.equal(one[4][0], t["dht"][0])
+
+
+def test_step_on_a_pool_past_2_to_31_elements():
+    """Lines on either side of 2^31 and 2^32 elements (and bytes) of the pool."""
+    import gated_deltanet_chunked_02_amd as gdn
+    H, D = 32, 128
+    lines = (1 << 32) // (H * D * D) + 3
+    r = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=r, device="cuda")  # noqa: E731
+    at = [0, (1 << 31) // (H * D * D), lines - 2]
+    pool = torch.empty(lines, H, D, D, device="cuda")
+    small = n(3, H, D, D)
+    for i, line in enumerate(at):
+        pool[line] = small[i]
+    q, k, v = (n(3, H, D).bfloat16() for _ in range(3))
+    g = -torch.rand(3, H, generator=r, device="cuda")
+    read = torch.tensor(at, dtype=torch.int32, device="cuda")
+    write = torch.tensor([lines - 1, at[1], 1], dtype=torch.int32, device="cuda")
+    o = gdn.linear_state_update(pool, q, k, v, g, cache_indices=read, out_indices=write)
+    want = gdn.linear_state_update(small, q, k, v, g)
+    assert torch.equal(o, want)
+    for i, line in enumerate((lines - 1, at[1], 1)):
+        assert torch.equal(pool[line], small[i]), line

@@ -167,12 +167,9 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int i = 16 * ti[n] + (lx & 15), j = 16 * tj[n] + 4 * (lx >> 4);
-        const double Gi = d.G[i];
+        const f32x4 w = decays(d, i, j);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x2 = a[n][e] * exp2_f32((float)(Gi - d.G[j + e]));
-          a[n][e] = j + e <= i ? x2 * p.scale : 0.f;
-        }
+        for (int e = 0; e < 4; ++e) a[n][e] = j + e <= i ? a[n][e] * w[e] * p.scale : 0.f;
         Ps.put(i, j, a[n]);
       }
     });

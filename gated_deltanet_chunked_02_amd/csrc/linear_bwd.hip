@@ -221,13 +221,12 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int i = 16 * ti[n] + lc, j = 16 * tj[n] + 4 * lg;
-        const double Gi = d.G[i];
+        const f32x4 w = decays(d, i, j) * p.scale;
         f32x4 pp, mm, ee;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float w = p.scale * exp2_f32((float)(Gi - d.G[j + e]));
-          pp[e] = j + e <= i ? qk[n][e] * w : 0.f;
-          mm[e] = j + e <= i ? ov[n][e] * w : 0.f;
+          pp[e] = j + e <= i ? qk[n][e] * w[e] : 0.f;
+          mm[e] = j + e <= i ? ov[n][e] * w[e] : 0.f;
           ee[e] = j + e < i ? mm[e] * qk[n][e] : 0.f;
         }
         Ps.put(i, j, pp);

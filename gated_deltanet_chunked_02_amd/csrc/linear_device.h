@@ -309,6 +309,19 @@ struct Decays {
   }
 };
 
+// The decays from tokens j .. j + 3 of a chunk to token i, whatever they are for tokens behind i: all
+// four at once, because a compiler that makes each where it is wanted waits for LDS each time.
+template <int C>
+__device__ __forceinline__ f32x4 decays(const Decays<C>& d, int i, int j) {
+  typedef double two __attribute__((ext_vector_type(2)));
+  const double Gi = d.G[i];
+  const two a = *reinterpret_cast<const two*>(d.G + j), b = *reinterpret_cast<const two*>(d.G + j + 2);
+  f32x4 r = {exp2_f32((float)(Gi - a[0])), exp2_f32((float)(Gi - a[1])),
+             exp2_f32((float)(Gi - b[0])), exp2_f32((float)(Gi - b[1]))};
+  opaque(r);
+  return r;
+}
+
 // The log-decay of the lane's token of a chunk that starts at token t0 (0 past its end): always one
 // load, so that the number of loads in flight is known.
 __device__ __forceinline__ float load_decay(const LinearProblem& p, long t0, int len, int h) {

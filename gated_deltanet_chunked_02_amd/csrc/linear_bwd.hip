@@ -82,8 +82,11 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ double rows[TT][C];  // E summed over a tile's columns, by tile column
   __shared__ double cols[TT][C];  // and over its rows, by tile row
-  __shared__ double bs[NW][C], cs[2][NW];  // two anchors may follow each other
-  __shared__ double sums[C];  // of dg over the chunks (head_decay)
+  __shared__ double bs[NW][C];
+  // <dS, S> by waves, two anchors may follow each other: where rows has nothing, in front of its last
+  // tile column's diagonal
+  static_assert(2 * NW <= 16 && TT > 1, "cs fits into a tile's width");
+  double* const cs = rows[TT - 1];
 
   const int unit = unit_of(blockIdx.x, gridDim.x, p.group);
   const int slot = unit / p.H, h = unit - slot * p.H;
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     Ms.clear(threadIdx.x, NTH);
   }
   loads_done();
-  if (wave == 0 && l < C) sums[l] = 0.0;  // this wave alone uses them
+  double sums = 0.0;  // of dg at the lane's place in its chunk (head_decay, wave 0)
   double pass = 0.0;  // <dS, S> at the chunk's end (wave 0)
   // What the carried value turns out to be off by at the next anchor had grown over the tokens since the
   // last: half of it for each of them (head_decay, wave 0)
@@ -178,7 +181,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
 #pragma unroll
         for (int e = 0; e < 4; ++e) x = fma((double)S[t][e], (double)dS[t][e], x);
       x = group_sum(row_sum(x));
-      if (lo == 0) cs[m & 1][wave] = x;
+      if (lo == 0) cs[(m & 1) * NW + wave] = x;
     }
     q.store(Qs, tid);
     k.store(Ks, tid);
@@ -232,8 +235,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
         Ps.put(i, j, pp);
         Ms.put(i, j, mm);
         double r = ((double)ee[0] + ee[1]) + ((double)ee[2] + ee[3]);
-        r += __shfl_xor(r, 16);
-        r += __shfl_xor(r, 32);
+        r = group_sum(r);
         if (lg == 0) rows[tj[n]][i] = r;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -245,12 +247,20 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     const float g = gnext;
     gnext = decay_of(m - 2);
     if (wave == NW - 1) dec[(m - 1) & 1].make(g);
-    // dK from dS and V, a step's operands at a time
+    // dK from dS and V.  Here and below the next step's operands are read before a step's products, and
+    // kept from sinking to their use, where each would be waited for.
     f32x4 acc[TT];
+    frag y[2][TT];
+    auto v_rows = [&](int s) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) y[s & 1][t] = TV::ld_state(Vs, 16 * t, s, lo);
+    };
+    v_rows(0);
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = zero4();
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
+      if (s + 1 < STEPS) v_rows(s + 1);
       sched_fence();
       frag f[TERMS];
       float x[8];
@@ -258,11 +268,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       for (int e = 0; e < EPL; ++e) x[e] = sizeof(E) == 2 ? dS[2 * s + e / 4][e % 4] : dS[s][e % 4];
       split<E>(x, f);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const frag y = TV::ld_state(Vs, 16 * t, s, lo);
+      for (int e = TERMS - 1; e >= 0; --e)
 #pragma unroll
-        for (int e = TERMS - 1; e >= 0; --e) acc[t] = Mx<E>::mma(f[e], y, acc[t]);
-      }
+        for (int t = 0; t < TT; ++t) acc[t] = Mx<E>::mma(f[e], y[s & 1][t], acc[t]);
     }
     sched_fence();
 #pragma unroll
@@ -277,19 +285,32 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     frag own[KS];  // Q transposed: this wave's 16 columns
 #pragma unroll
     for (int s = 0; s < KS; ++s) own[s] = TK::tr(Qs, KF * s, 16 * wave, lo);
+    frag z[2][KS][Ms.TERMS];  // rows 16 t .. of M or P transposed
+    auto columns = [&](const Scores<E, C>& m, int t) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < Ms.TERMS; ++e)
+          if (KF * (s + 1) > 16 * t) z[t & 1][s][e] = TP::tr(m.m[e], KF * s, 16 * t, lo);
+    };
+    auto product = [&](const frag (&x)[KS], int t) {
+#pragma unroll
+      for (int e = Ms.TERMS - 1; e >= 0; --e)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          if (KF * (s + 1) > 16 * t) acc[t] = Mx<E>::mma(x[s], z[t & 1][s][e], acc[t]);
+    };
     {
       const __amdgpu_buffer_rsrc_t rs = rows_of(gp + (long)m * C * sg, sg, p.Dk, len);
       const int col = 16 * wave + 4 * lg;
+      columns(Ms, 0);
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          if (KF * (s + 1) > 16 * t)
-#pragma unroll
-            for (int e = Ms.TERMS - 1; e >= 0; --e)
-              acc[t] = Mx<E>::mma(own[s], TP::tr(Ms.m[e], KF * s, 16 * t, lo), acc[t]);
-        store4<G>(rs, col < p.Dk ? (row_at(16 * t + lc, sg) + col) * (int)sizeof(G)
-                                 : kNoColumn, acc[t]);
+        if (t + 1 < TT) columns(Ms, t + 1);
+        sched_fence();
+        product(own, t);
+        store4<G>(rs, col < p.Dk ? (row_at(16 * t + lc, sg) + col) * (int)sizeof(G) : kNoColumn,
+                  acc[t]);
       }
     }
     // dV
@@ -298,52 +319,66 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     for (int w = 0; w < (VT + NW - 1) / NW; ++w) {
       const int vt = wave + w * NW;
       if (VT % NW != 0 && vt >= VT) break;
+      frag sf[2];
+      auto k_rows = [&](int s) {
+        sf[s & 1] = TV::tr(Ds, KF * s, 16 * vt, lo);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) y[s & 1][t] = TK::ld(Ks, 16 * t, KF * s, lo);
+      };
+      k_rows(0);
 #pragma unroll
       for (int t = 0; t < TT; ++t) acc[t] = zero4();
 #pragma unroll
       for (int s = 0; s < DK / KF; ++s) {
+        if (s + 1 < DK / KF) k_rows(s + 1);
         sched_fence();
-        const frag sf = TV::tr(Ds, KF * s, 16 * vt, lo);
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-          acc[t] = Mx<E>::mma(sf, TK::ld(Ks, 16 * t, KF * s, lo), acc[t]);
+        for (int t = 0; t < TT; ++t) acc[t] = Mx<E>::mma(sf[s & 1], y[s & 1][t], acc[t]);
       }
       frag of[KS];
 #pragma unroll
       for (int s = 0; s < KS; ++s) of[s] = TV::tr(Os, KF * s, 16 * vt, lo);
+      columns(Ps, 0);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[t] *= d.left[16 * t + lc];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        acc[t] *= d.left[16 * t + lc];
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          if (KF * (s + 1) > 16 * t)
-#pragma unroll
-            for (int e = Ps.TERMS - 1; e >= 0; --e)
-              acc[t] = Mx<E>::mma(of[s], TP::tr(Ps.m[e], KF * s, 16 * t, lo), acc[t]);
+        if (t + 1 < TT) columns(Ps, t + 1);
+        sched_fence();
+        product(of, t);
         const int col = 16 * vt + 4 * lg;
-        store4<E>(rs, col < p.Dv ? (row_at(16 * t + lc, so) + col) * (int)sizeof(E)
-                                 : kNoColumn, acc[t]);
+        store4<E>(rs, col < p.Dv ? (row_at(16 * t + lc, so) + col) * (int)sizeof(E) : kNoColumn,
+                  acc[t]);
       }
     }
-    // dS for the chunk before
+    // dS for the chunk before, four tiles at a time
+    constexpr int GROUP = 4, GROUPS = KS * VT / GROUP;
+    frag r[2][GROUP];
+    auto o_rows = [&](int n) {
+#pragma unroll
+      for (int t = 0; t < GROUP; ++t)
+        r[n & 1][t] = TV::tr_state(Os, KF * (n * GROUP / VT), n * GROUP % VT + t, lo);
+    };
+    o_rows(0);
 #pragma unroll
     for (int t = 0; t < VT; ++t) dS[t] *= keep;
+    frag f[TERMS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
+    for (int n = 0; n < GROUPS; ++n) {
+      const int s = n * GROUP / VT, first = n * GROUP % VT;
+      if (n + 1 < GROUPS) o_rows(n + 1);
       sched_fence();
-      float w[8];
+      if (first == 0) {
+        float w[8];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e)
-        w[e] = (float)own[s][e] * (p.scale * d.into[KF * s + EPL * lg + e]);
-      frag f[TERMS];
-      split<E>(w, f);
-#pragma unroll
-      for (int t = 0; t < VT; ++t) {
-        if (t % 4 == 0) sched_fence();
-        const frag r = TV::tr_state(Os, KF * s, t, lo);
-#pragma unroll
-        for (int e = TERMS - 1; e >= 0; --e) dS[t] = Mx<E>::mma(r, f[e], dS[t]);
+        for (int e = 0; e < EPL; ++e)
+          w[e] = (float)own[s][e] * (p.scale * d.into[KF * s + EPL * lg + e]);
+        split<E>(w, f);
       }
+#pragma unroll
+      for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+        for (int t = 0; t < GROUP; ++t) dS[first + t] = Mx<E>::mma(r[n & 1][t], f[e], dS[first + t]);
     }
     __syncthreads();
     // the others go on to the next chunk, whose first barrier comes before its first write of any of these (but cs's other half)
@@ -359,7 +394,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       if (anchor) {
         double x = 0.0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) x += cs[m & 1][w];
+        for (int w = 0; w < NW; ++w) x += cs[(m & 1) * NW + w];
         off += (x - pass) * since;
         pass = x;
         since = 0;
@@ -376,7 +411,7 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       if (d.G[t] - (t > 0 ? d.G[t - 1] : 0.0) < -150.0) x = 0.0;
       if (lo < len) {
         if (p.head_decay)
-          sums[lo] += x;
+          sums += x;
         else if (b.dg)
           b.dg[(c.t0 + (long)m * C + lo) * p.H + h] = (float)x;
       }
@@ -401,14 +436,14 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       for (int e = 0; e < 4; ++e) x = fma((double)s0[e], (double)dS[t][e], x);
     }
     x = group_sum(row_sum(x));
-    if (l == 0) cs[1][wave] = x;  // chunk 0 may be an anchor and has the other half
+    if (l == 0) cs[NW + wave] = x;  // chunk 0 may be an anchor and has the other half
     __syncthreads();
     if (wave == 0) {
       x = 0.0;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) x += cs[1][w];
+      for (int w = 0; w < NW; ++w) x += cs[NW + w];
       if (since > 0) off += (x - pass) * since;
-      x = wave_incl_scan(l < C ? sums[l] : 0.0) + 0.5 * off;
+      x = wave_incl_scan(l < C ? sums : 0.0) + 0.5 * off;
       if (l == 63) b.dgp[unit] = x;
     }
   }

@@ -271,17 +271,26 @@ __device__ __forceinline__ double last_lane(double x) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Sum over the four lane groups that share lane % 16.
+// Sum over the four lane groups that share lane % 16, in all of them, without LDS: the two instructions
+// exchange rows 1, 3 of one operand with 0, 2 of the other, and rows 2, 3 with 0, 1.
 __device__ __forceinline__ float group_sum(float x) {
-  x += __shfl_xor(x, 16);
-  x += __shfl_xor(x, 32);
-  return x;
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
-
 __device__ __forceinline__ double group_sum(double x) {
-  x += __shfl_xor(x, 16);
-  x += __shfl_xor(x, 32);
-  return x;
+  auto join = [](uint32_t lo, uint32_t hi) {
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  };
+  uint64_t u = __builtin_bit_cast(uint64_t, x);
+  auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  x = join(lo[0], hi[0]) + join(lo[1], hi[1]);
+  u = __builtin_bit_cast(uint64_t, x);
+  lo = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+  hi = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  return join(lo[0], hi[0]) + join(lo[1], hi[1]);
 }
 
 // A chunk's decays.  G_t, the sum of log2 decays up to token t, is held in fp64: the decay between

@@ -22,11 +22,11 @@
 // (k and v alone), k_linear_compose turns those into start states in order, and k_linear_fwd runs
 // the segments side by side.
 //
-// Measured (bf16, heads of 128 x 128): 8 x 2048 tokens of 32 heads 155 us in a run of calls, whose loads
-// and stores alone take 113 with this order of accesses (4.7 TB/s), the matrix units busy 22 % and the
+// Measured (bf16, heads of 128 x 128): 8 x 2048 tokens of 32 heads 152 us, whose loads
+// and stores alone take 113 with this order of accesses (4.7 TB/s), the matrix units busy 24 % and the
 // vector units 36 %; 16384 tokens of 32 heads 65 + 12 + 134 us.  Four waves of 32 columns instead of
 // eight of 16 took 170; a single barrier a chunk, with two or three buffers of everything, no less; 64
-// narrow heads (4096 tokens, 64 columns) are one wave a SIMD and wait on each other's results.
+// narrow heads (4 x 4096 tokens, 64 columns) are one wave a SIMD, 206 us.
 #include "linear_device.h"
 
 namespace gdn {

@@ -33,10 +33,9 @@
 // (dV) takes a copy rounded to bf16 from LDS, the one rounding on any way to an output.  M and P go
 // through LDS as two terms.
 //
-// Measured (8 x 2048 tokens, 32 heads of 128 x 128, bf16): dQ's pass 226 us and this one 310 to 320 in a
-// run of calls, a workgroup a CU (140 KB of LDS), vector units busy 40 %, matrix units 19 %, LDS 25 %, the
-// waves waiting 43 % of their cycles.  Left out one at a time, the scores took 37 us of it, dK's product
-// 35, dV's 25, dS's update 55; loads, stores and what goes through LDS 195.
+// Measured (8 x 2048 tokens, 32 heads of 128 x 128, bf16): dQ's pass 219 us and this one 293, a workgroup a
+// CU (141 KB of LDS), vector units busy 46 %, matrix units 23 %, LDS 29 %, the waves waiting 31 % of their
+// cycles (318 us and 43 % with every operand read where it is used).
 #include "linear_device.h"
 
 namespace gdn {

@@ -95,6 +95,17 @@ void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
 
 int slabs_of(const gdn::LinearProblem& p) { return (p.Dv + gdn::kLinearSlab - 1) / gdn::kLinearSlab; }
 
+// Up to this many values of a head's states at the segments' ends, segments make their start states
+// themselves, each from all before it, and no launch composes them (128 x 128: 512 tokens of 32 heads, four
+// segments, 26 us and not 31; 1024 and 2048, eight segments, 32 and not 34, and 53 either way).
+constexpr long long kMostJoined = 8 * 128 * 128;
+
+bool joins(const gdn::LinearProblem& p, bool packed) {
+  if (p.Lc == gdn::kScanNoSplit) return false;
+  const long long most = packed ? p.Ttot / p.Lc + 1 : ((long long)p.T + p.Lc - 1) / p.Lc;
+  return most * p.Dk * p.Dv <= kMostJoined;
+}
+
 constexpr int kFwdFill = 512;
 constexpr int kBwdFill = 256;  // one
 
@@ -230,6 +241,7 @@ gdn_status gdn_linear_attn_fwd(const gdn_linear_desc* d, const void* q, const vo
   p.o = o;
   p.ht = ht;
   p.direct = !h0 || h0 != ht;
+  p.join = p.direct && joins(p, cu_seqlens != nullptr);
   return gdn::launch_linear_fwd(p, stream) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 

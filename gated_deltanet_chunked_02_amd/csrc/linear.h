@@ -36,6 +36,7 @@ struct LinearProblem {
   float* ht;           // [N, H, Dk, Dv] or null
   float* states;       // workspace: [slots, H, Dk, Dv], each segment's own end state, then its start
   bool direct;         // first segments start from h0 itself: no other reads it after ht is written
+  bool join;           // segments make their start states from the own ones of those before them
   float* sums;         // workspace: [slots, H], each segment's sum of log2 decays
 };
 

@@ -20,7 +20,7 @@
 //
 // Few or long sequences are cut into segments: k_linear_state makes each segment's own end state
 // (k and v alone), k_linear_compose turns those into start states in order, and k_linear_fwd runs
-// the segments side by side.
+// the segments side by side.  A few segments make their start states themselves.
 //
 // Measured (bf16, heads of 128 x 128): 8 x 2048 tokens of 32 heads 152 us, whose loads
 // and stores alone take 113 with this order of accesses (4.7 TB/s), the matrix units busy 24 % and the
@@ -72,29 +72,44 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   // The state in memory is [Dk, Dv]: this one's rows (GRAD: its columns) are the first axis.  Rows past
   // the head lie past the buffer, or are sent there.
   f32x4 S[CW][KT];
-  const bool made = p.Lc != kScanNoSplit && (c.i > 0 || !p.direct);
-  const float* from = made   ? p.states + ((long)slot * p.H + h) * cell
-                      : p.h0 ? p.h0 + ((long)c.n * p.H + h) * cell
-                             : nullptr;
-  const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
+  auto load = [&](const float* from, f32x4 (&to)[CW][KT]) {
+    const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
 #pragma unroll
-  for (int w = 0; w < CW; ++w) {
-    const int col = col0 + 16 * w + (l & 15);
+    for (int w = 0; w < CW; ++w) {
+      const int col = col0 + 16 * w + (l & 15);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      if constexpr (GRAD) {
-        S[w][t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-            frs, col < width && tile_row(t, l) < r.Dk
-                     ? (uint32_t)(col * r.Dk + tile_row(t, l)) * 4 : kNoColumn, 0, 0));
-      } else {
+      for (int t = 0; t < KT; ++t) {
+        if constexpr (GRAD) {
+          to[w][t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              frs, col < width && tile_row(t, l) < r.Dk
+                       ? (uint32_t)(col * r.Dk + tile_row(t, l)) * 4 : kNoColumn, 0, 0));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          S[w][t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-              frs, col < width ? (uint32_t)((tile_row(t, l) + i) * r.Dv + v0 + col) * 4 : kNoColumn,
-              0, 0));
+          for (int i = 0; i < 4; ++i)
+            to[w][t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                frs, col < width ? (uint32_t)((tile_row(t, l) + i) * r.Dv + v0 + col) * 4
+                                 : kNoColumn, 0, 0));
+        }
       }
     }
+  };
+  const bool made = p.Lc != kScanNoSplit && !p.join && (c.i > 0 || !p.direct);
+  load(made   ? p.states + ((long)slot * p.H + h) * cell
+       : p.h0 ? p.h0 + ((long)c.n * p.H + h) * cell
+              : nullptr, S);
+  if constexpr (!GRAD) {
+    if (p.join)
+      for (int s = slot - c.i; s < slot; ++s) {
+        const long at = (long)s * p.H + h;
+        const float keep = exp2_f32(p.sums[at]);
+        f32x4 x[CW][KT];
+        load(p.states + at * cell, x);
+#pragma unroll
+        for (int w = 0; w < CW; ++w)
+#pragma unroll
+          for (int t = 0; t < KT; ++t) S[w][t] = S[w][t] * keep + x[w][t];
+      }
   }
 
   const E* qp = static_cast<const E*>(r.q) + c.t0 * r.sq + (long)(h / r.qrep) * r.Dk;
@@ -580,7 +595,7 @@ hipError_t launch_linear_states(const LinearProblem& p, const LinearBwd* b, hipS
   }
   const hipError_t e = p.f32 ? launch_state_e<float>(p, a, b ? &back : nullptr, st)
                              : launch_state_e<bf16>(p, a, b ? &back : nullptr, st);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || p.join) return e;
   const long blocks = ((long)p.Dk * p.Dv / 4 + 255) / 256 * p.N * p.H;
   k_linear_compose<<<dim3((unsigned)blocks, b ? 2 : 1), 256, 0, st>>>(p, ends);
   return hipGetLastError();

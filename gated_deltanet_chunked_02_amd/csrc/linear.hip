@@ -72,7 +72,9 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   // The state in memory is [Dk, Dv]: this one's rows (GRAD: its columns) are the first axis.  Rows past
   // the head lie past the buffer, or are sent there.
   f32x4 S[CW][KT];
-  auto load = [&](const float* from, f32x4 (&to)[CW][KT]) {
+  // every way to a start state adds to what is there: one that loads into S itself took the packed batch of
+  // 12454 tokens from 184 to 189 us
+  auto state = [&](const float* from, float keep) {
     const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
 #pragma unroll
@@ -80,35 +82,35 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
       const int col = col0 + 16 * w + (l & 15);
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
+        f32x4 x;
         if constexpr (GRAD) {
-          to[w][t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
               frs, col < width && tile_row(t, l) < r.Dk
                        ? (uint32_t)(col * r.Dk + tile_row(t, l)) * 4 : kNoColumn, 0, 0));
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            to[w][t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            x[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
                 frs, col < width ? (uint32_t)((tile_row(t, l) + i) * r.Dv + v0 + col) * 4
                                  : kNoColumn, 0, 0));
         }
+        S[w][t] = S[w][t] * keep + x;
       }
     }
   };
+#pragma unroll
+  for (int w = 0; w < CW; ++w)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) S[w][t] = zero4();
   const bool made = p.Lc != kScanNoSplit && !p.join && (c.i > 0 || !p.direct);
-  load(made   ? p.states + ((long)slot * p.H + h) * cell
-       : p.h0 ? p.h0 + ((long)c.n * p.H + h) * cell
-              : nullptr, S);
+  state(made   ? p.states + ((long)slot * p.H + h) * cell
+        : p.h0 ? p.h0 + ((long)c.n * p.H + h) * cell
+               : nullptr, 1.f);
   if constexpr (!GRAD) {
     if (p.join)
       for (int s = slot - c.i; s < slot; ++s) {
         const long at = (long)s * p.H + h;
-        const float keep = exp2_f32(p.sums[at]);
-        f32x4 x[CW][KT];
-        load(p.states + at * cell, x);
-#pragma unroll
-        for (int w = 0; w < CW; ++w)
-#pragma unroll
-          for (int t = 0; t < KT; ++t) S[w][t] = S[w][t] * keep + x[w][t];
+        state(p.states + at * cell, exp2_f32(p.sums[at]));
       }
   }
 

@@ -14,9 +14,10 @@
 // columns, 16 a wave, whose state stays in registers (as tiles that are operands themselves,
 // linear_device.h) from the segment's first chunk to its last.  q, k and v go through LDS, the next
 // chunk's in registers meanwhile; the C x C scores are shared out over the waves and come back as two
-// bf16 terms.  One tensor is rounded to bf16 on the way to o, the state that meets q (its rounding
-// errors average over Dk rows; a second term took 8 x 2048 tokens from 165 to 180 us); the state itself
-// and what is added to it are held to fp32's last bits (v times its decay enters as three bf16 terms).
+// bf16 terms, and so does the state meet q (16 bits or more of each value; with one term, o of a carried
+// state came out 1.25 times as far from the definition as fp32 sums rounded once, and 8 x 2048 tokens took
+// 168 us where they take 182); the state itself and what is added to it are held to fp32's last bits (v
+// times its decay enters as three bf16 terms).
 //
 // Few or long sequences are cut into segments: k_linear_state makes each segment's own end state
 // (k and v alone), k_linear_compose turns those into start states in order, and k_linear_fwd runs
@@ -35,15 +36,15 @@ namespace {
 
 // GRAD: the same pass over other tensors makes dq.  With S^T as the state, whose rows run over the value
 // columns, dq_t = scale S_t dout_t is the recurrence with dout for q, v for k and k for v.  There the
-// state meets dout as three bf16 terms, because the sums q . dq that leave the chunk (a) are terms of dg,
-// an fp32 result; and the state is written out at every kLinearAnchor-th chunk's end for the other half
+// state meets dout as three bf16 terms, not two, because the sums q . dq that leave the chunk (a) are terms of
+// dg, an fp32 result; and the state is written out at every kLinearAnchor-th chunk's end for the other half
 // of the gradient.
 template <typename E, int DK, int DV, int NW, int OCC, bool GRAD, typename G>
 __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, LinearRun r) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
   constexpr int NTH = NW * 64, CW = DV / 16 / NW, KT = DK / 16, TT = C / 16;
   constexpr int KF = Mx<E>::KF, KS = C / KF, TERMS = Mx<E>::TERMS, EPL = Mx<E>::EPL;
-  constexpr int STEPS = sizeof(E) == 2 ? KT / 2 : KT, STERMS = GRAD ? TERMS : 1;
+  constexpr int STEPS = sizeof(E) == 2 ? KT / 2 : KT, STERMS = GRAD || TERMS < 2 ? TERMS : 2;
   // Products are taken a step at a time where waves are short of registers; four waves of a CU's 16 are
   // not, and have the more to gain from reads ahead (4 x 4096 tokens, 64 heads of 64 columns: 249 to 233 us)
   auto fence = [] { if constexpr (NW * OCC >= 16) sched_fence(); };

@@ -30,11 +30,12 @@
 //
 // dS is held by key rows: a wave has 16 of them and all value columns, so the product over the value
 // columns (dK) takes it from registers as three bf16 terms (its b is a term of dg); the one over key rows
-// (dV) takes a copy rounded to bf16 from LDS, the one rounding on any way to an output.  M and P go
-// through LDS as two terms.
+// (dV) takes it from LDS as two, like M and P: 16 bits or more of each value, so that every output is fp32
+// sums rounded once (with one term, dv of a carried gradient came out 1.25 times as far off, and this pass
+// was 4 % shorter).
 //
 // Measured (8 x 2048 tokens, 32 heads of 128 x 128, bf16): dQ's pass 219 us and this one 293, a workgroup a
-// CU (141 KB of LDS), vector units busy 46 %, matrix units 23 %, LDS 29 %, the waves waiting 31 % of their
+// CU (158 KB of LDS), vector units busy 46 %, matrix units 23 %, LDS 29 %, the waves waiting 31 % of their
 // cycles (318 us and 43 % with every operand read where it is used).
 #include "linear_device.h"
 
@@ -76,7 +77,11 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   __shared__ __align__(256) E Ks[C * TK::LD];
   __shared__ __align__(256) E Vs[C * TV::LD];
   __shared__ __align__(256) E Os[C * TV::LD];   // dO
-  __shared__ __align__(256) E Ds[DK * TV::LD];  // dS, rounded
+  // dS as two bf16 terms (or as itself): the second one's first C rows take the place of V, which a
+  // chunk's last products do not read
+  constexpr bool TWO = sizeof(E) == 2;
+  __shared__ __align__(256) E Ds[DK * TV::LD];
+  __shared__ __align__(256) E Dl[TWO && DK > C ? (DK - C) * TV::LD : 1];
   __shared__ Scores<E, C> Ps, Ms;
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ double rows[TT][C];  // E summed over a tile's columns, by tile column
@@ -164,6 +169,13 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
   // last: half of it for each of them (head_decay, wave 0)
   double off = 0.0;
   int since = 0;
+  // what bf16 leaves of this wave's rows of dS, into a tile's rows
+  auto rest = [&](E* m, int row, int l) {
+#pragma unroll
+    for (int t = 0; t < VT; ++t)
+      put4<E, DV>(m, row, tile_row(t, l),
+                  dS[t] - __builtin_convertvector(__builtin_convertvector(dS[t], bf16x4), f32x4));
+  };
 
   for (int m = chunks - 1; m >= 0; --m) {
     const int len = min(C, c.len - m * C);
@@ -188,6 +200,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     o.store(Os, tid);
 #pragma unroll
     for (int t = 0; t < VT; ++t) put4<E, DV>(Ds, 16 * wave + lc, tile_row(t, lo), dS[t]);
+    if constexpr (TWO && DK > C) {
+      if (wave >= C / 16) rest(Dl, 16 * wave - C + lc, lo);
+    }
     __syncthreads();
     // a of this chunk, for its last step
     const __amdgpu_buffer_rsrc_t ars = __builtin_amdgcn_make_buffer_rsrc(
@@ -280,6 +295,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
     }
     __syncthreads();
 
+    if constexpr (TWO) {
+      if (wave < C / 16) rest(Vs, 16 * wave + lc, lo);
+    }
     const float keep = d.into[C - 1];
     frag own[KS];  // Q transposed: this wave's 16 columns
 #pragma unroll
@@ -313,14 +331,18 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       }
     }
     // dV
+    if constexpr (TWO) __syncthreads();
     const __amdgpu_buffer_rsrc_t rs = rows_of(dvp + (long)m * C * so, so, p.Dv, len);
 #pragma unroll
     for (int w = 0; w < (VT + NW - 1) / NW; ++w) {
       const int vt = wave + w * NW;
       if (VT % NW != 0 && vt >= VT) break;
-      frag sf[2];
+      frag sf[2][1 + TWO];
       auto k_rows = [&](int s) {
-        sf[s & 1] = TV::tr(Ds, KF * s, 16 * vt, lo);
+        sf[s & 1][0] = TV::tr(Ds, KF * s, 16 * vt, lo);
+        if constexpr (TWO)
+          sf[s & 1][TWO] = KF * s < C ? TV::tr(Vs, KF * s, 16 * vt, lo)
+                                      : TV::tr(Dl, KF * s - C, 16 * vt, lo);
 #pragma unroll
         for (int t = 0; t < TT; ++t) y[s & 1][t] = TK::ld(Ks, 16 * t, KF * s, lo);
       };
@@ -332,7 +354,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
         if (s + 1 < DK / KF) k_rows(s + 1);
         sched_fence();
 #pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = Mx<E>::mma(sf[s & 1], y[s & 1][t], acc[t]);
+        for (int e = TWO; e >= 0; --e)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) acc[t] = Mx<E>::mma(sf[s & 1][e], y[s & 1][t], acc[t]);
       }
       frag of[KS];
 #pragma unroll

@@ -362,7 +362,8 @@ size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_desc* d, gdn_status* 
  *   dv      [B, T, H, Dv]  dtype, contiguous
  *   dg      g's shape      f32, or NULL (not wanted)
  *   dh0     [N, H, Dk, Dv] f32, or NULL (not written); may be dht's buffer
- * Dk and Dv up to 128 (GDN_ERR_UNSUPPORTED beyond).  Sums have a fixed order (no atomics).  Gradients
+ * Dk and Dv up to 128 (GDN_ERR_UNSUPPORTED beyond).  bf16 gradients are as near as fp32 sums rounded once,
+ * dg and dh0 as exact as fp32 sums.  Sums have a fixed order (no atomics).  Gradients
  * of tokens of a packed batch that no sequence has are not written.
  * The workspace holds a state in fp32 for every 512 tokens of a sequence (256 in f32; half of that with
  * head_decay; fewer where it is split into shorter segments): 4 Dk Dv bytes a value head, sizes rounded

@@ -5,7 +5,7 @@ bf16 tensors are compared with the oracle's values rounded to bf16.  A value off
 rounding comes out on the other side of a half step with probability d / step and is then a step away, so
 the mean square of the difference is at most sum |d| step <= |d|_2 |step|_2, where a step is at most 2^-7
 of its value: the relative L2 difference is at most sqrt(D 2^-7) + D for values off by D before the
-rounding, D the tolerance of the fp32 results (test_gpu_linear).  A single rounding of
+rounding, D the tolerance of the fp32 results (test_gpu_linear, test_gpu_linear_bwd).  A single rounding of
 an operand to bf16 on the way, of 2^-9 at most a value and 1e-3 in the mean, gives sqrt(1e-3 2^-7) = 2.8e-3.
 
 The final state of one chunk is a sum of at most 64 products and a start state: a rounding (2^-24) for
@@ -15,6 +15,7 @@ import pytest
 import torch
 
 from test_gpu_linear import TOL_F32, check, host, make, oracle_fwd, run_fwd
+from test_gpu_linear_bwd import TOL_F32 as TOL_GRAD, oracle_bwd, run_bwd
 
 pytestmark = pytest.mark.gpu
 
@@ -45,6 +46,14 @@ def test_outputs_are_rounded_once(B, T, H, Hg, Dk, Dv, head, h0):
     p = make(B, T, H, Hg, Dk, Dv, "bf16", head, h0, seed=B + T)
     o, _ = run_fwd(p)
     check_rounded("o", o, oracle_fwd(p)[0], TOL_F32)
+
+
+@pytest.mark.parametrize("B,T,H,Hg,Dk,Dv,head,h0", CASES)
+def test_gradients_are_rounded_once(B, T, H, Hg, Dk, Dv, head, h0):
+    p = make(B, T, H, Hg, Dk, Dv, "bf16", head, h0, seed=B + T)
+    got, ref = run_bwd(p), oracle_bwd(p)
+    for x in ("dq", "dk", "dv"):
+        check_rounded(x, got[x], ref[x], TOL_GRAD)
 
 
 @pytest.mark.parametrize("T", [1, 17, 64])

@@ -422,7 +422,9 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
         pass = x;
         since = 0;
       }
-      since += len;
+      // nothing passes a decay that is 0 in fp32, nor of what the carried value is off by (a head's own
+      // decay: every token's)
+      if (!(d.G[0] < -150.0)) since += len;
       up = lo < len ? up : 0.0;
       down = lo < len ? down : 0.0;
       in = lo < len ? in : 0.0;
@@ -430,7 +432,6 @@ __global__ __launch_bounds__(DK * 4, 2) void k_linear_bwd(LinearProblem p, Linea
       const double all = last_lane(prefix);
       double x = (last_lane(suffix) - suffix + up + in) + (prefix - down) + (pass - all);
       pass += last_lane(wave_incl_scan(up)) - all;
-      // nothing passes a decay that is 0 in fp32
       if (d.G[t] - (t > 0 ? d.G[t - 1] : 0.0) < -150.0) x = 0.0;
       if (lo < len) {
         if (p.head_decay)

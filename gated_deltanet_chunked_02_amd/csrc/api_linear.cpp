@@ -59,13 +59,26 @@ gdn_status check_linear(const gdn_linear_desc* d, bool packed, gdn::LinearProble
   return GDN_OK;
 }
 
-// Segment length.  A sequence stays whole where its heads (times the value slabs) give every CU a
-// workgroup: 8 x 2048 tokens of 32 heads take 162 us whole and 212 in two segments each, whose states
-// another pass has to make.  Fewer are cut into as many segments as make `fill` workgroups, of two chunks
-// at least (16384 tokens of 32 heads: 221 us in 16 segments, 270 in 8), but not sequences of fewer than
-// six chunks, whose few steps take less than two more launches.  A packed batch is cut for one head a CU
-// as well, because its sequences are of unlike lengths, and at twice its mean length in any case.
-constexpr int kUnits = 256;  // CUs
+// Segment length.  Short of heads (times the value slabs), sequences are cut into as many segments as make
+// `fill` workgroups, two chunks long at least (16384 tokens of 32 heads: 16 segments, where 8 took a fifth
+// more); but not those of fewer than six chunks, whose few steps take less than two more launches.
+//
+// Segments cost a pass over their states, so that a dense batch is cut where `least` of them fit and is run
+// whole elsewhere.  Forward, 2048 tokens in bf16, whole and cut: 128 (sequence, head) pairs 147 and 119 us,
+// 160 (three segments) 147 and 138, 180 (two) 147 and 179, 224 157 and 193, 256 165 and 208; 1024 tokens in
+// fp32: 128 pairs 191 and 154, 192 193 and 263.  Gradient: 96 (two) 454 and 296, 128 479 and 321.
+//
+// A packed batch's lengths are on the device.  Whole, it takes as long as its longest sequence; cut, about
+// as long whatever they are.  So it is always cut, with `fill` up to `most` pairs and at twice its mean length
+// beyond, where that is as good.  Forward, 12454 tokens in 8 sequences, whole, by `fill` and by the mean: lengths
+// to 2048, 256 pairs 147, 187 and 224 us, 288 161, 223 and 223, 320 169, 255 and 229; one of 8192,
+// 256 pairs 523, 196 and 319, 288 538, 214 and 323, 320 548, 243 and 327.  Gradient: the same lengths, 288 pairs
+// 485, 498 and 497, 320 648, 664 and 663; with one of 8192 1797, 642 and 972, 1821, 753 and 1033 (at 512 pairs
+// both give the same length).
+struct Cut {
+  int fill, least, most;  // most: no more than twice fill, so that two sequences' heads are within it
+};
+constexpr Cut kFwdCut = {512, 3, 288}, kBwdCut = {256, 2, 512};
 
 int slots_of(const gdn::LinearProblem& p, bool packed) {
   return p.N == 0 ? 0
@@ -73,18 +86,19 @@ int slots_of(const gdn::LinearProblem& p, bool packed) {
                   : p.N * (int)(p.T > p.Lc ? ((long long)p.T + p.Lc - 1) / p.Lc : 1);
 }
 
-void plan(gdn::LinearProblem* p, bool packed, int slabs, int fill) {
+void plan(gdn::LinearProblem* p, bool packed, int slabs, const Cut& cut) {
   p->Lc = gdn::kScanNoSplit;
   const int C = gdn::linear_chunk(p->f32);
   const long long longest = packed ? p->Ttot : p->T;
   if (p->N > 0 && longest >= 6 * C) {
     const long long units = (long long)p->H * slabs;
+    const bool unlike = packed && p->N > 1;  // a packed batch of one has one length
     long long L = longest;
-    if (units * p->N < (packed ? kUnits + 1 : kUnits)) {
-      const long long each = packed ? fill / units : fill / (units * p->N);
-      L = each > 0 ? (longest + each - 1) / each : longest;
-    } else if (packed) {
+    if (unlike && units * p->N > cut.most) {
       L = 2LL * ((p->Ttot + p->N - 1) / p->N);
+    } else {
+      const long long each = unlike ? cut.fill / units : cut.fill / (units * p->N);
+      if (unlike || each >= cut.least) L = (longest + each - 1) / each;
     }
     if (L < 2 * C) L = 2 * C;
     L = (L + gdn::kLinearChunk - 1) / gdn::kLinearChunk * gdn::kLinearChunk;
@@ -109,12 +123,9 @@ bool joins(const gdn::LinearProblem& p, bool packed) {
   return most <= kMostSegments && most * p.Dk * p.Dv <= kMostJoined;
 }
 
-constexpr int kFwdFill = 512;
-constexpr int kBwdFill = 256;  // one
-
-void plan_fwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, slabs_of(*p), kFwdFill); }
+void plan_fwd(gdn::LinearProblem* p, bool packed) { plan(p, packed, slabs_of(*p), kFwdCut); }
 void plan_bwd(gdn::LinearProblem* p, bool packed) {
-  plan(p, packed, 1, kBwdFill);
+  plan(p, packed, 1, kBwdCut);
   // a segment holds whole spans between the states kept for the gradient, or is one
   const int span = gdn::linear_anchor(*p) * gdn::linear_chunk(p->f32);
   if (p->Lc != gdn::kScanNoSplit && p->Lc > span) {

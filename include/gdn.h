@@ -326,7 +326,8 @@ gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const fl
  * meets q keep 16 bits or more on their way to it), ht as exact as fp32 sums.  Few or long sequences are split into segments
  * that run in parallel, so results depend on the descriptor in their last bits, never on scheduling.
  * An infinity or a NaN in q, k, v or g reaches its own head (its q/k head's value heads) of its own
- * sequence, from the chunk it is in: the outputs of that chunk's earlier tokens may be NaN too. */
+ * sequence, from the chunk it is in: the outputs of that chunk's earlier tokens may be NaN too.  One in h0
+ * reaches its own head of its own sequence.  In bf16 an infinity in v or in a state may come out as a NaN. */
 typedef struct gdn_linear_desc {
   int32_t B, T;         /* dense [B, T, ...]; packed: B = 1, T = total tokens               */
   int32_t N;            /* sequences: B (or 0) for a dense batch, len(cu_seqlens) - 1       */
@@ -363,7 +364,9 @@ size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_desc* d, gdn_status* 
  *   dg      g's shape      f32, or NULL (not wanted)
  *   dh0     [N, H, Dk, Dv] f32, or NULL (not written); may be dht's buffer
  * Dk and Dv up to 128 (GDN_ERR_UNSUPPORTED beyond).  bf16 gradients are as near as fp32 sums rounded once,
- * dg and dh0 as exact as fp32 sums.  Sums have a fixed order (no atomics).  Gradients
+ * dg and dh0 as exact as fp32 sums; dg is a difference of sums over the tokens around it, so that its error is
+ * an fp32 rounding of theirs: all of it where a token's decay leaves less than 2^-24 of the state, down to
+ * decays of 2^-150, from where it is 0.  Sums have a fixed order (no atomics).  Gradients
  * of tokens of a packed batch that no sequence has are not written.
  * The workspace holds a state in fp32 for every 512 tokens of a sequence (256 in f32; half of that with
  * head_decay; fewer where it is split into shorter segments): 4 Dk Dv bytes a value head, sizes rounded

@@ -112,9 +112,9 @@ int slabs_of(const gdn::LinearProblem& p) { return (p.Dv + gdn::kLinearSlab - 1)
 // A few segments make their start states themselves, each from all before it, and no launch composes them.
 // Every one of those is a read that the next waits for, and all of them together grow with the square of the
 // segments.  So no more than this many values of a head's states at the segments' ends (128 x 128: 512
-// tokens of 32 heads, four segments, 26 us and not 31; 1024 and 2048, eight segments, 32 and not 34, and
-// 53 either way), and no more segments than 16 (64 x 64: 2048 tokens of 32 heads, 16 segments, 28 us and not
-// 30; 4096 of 16, 32 segments, 35 and 33 composed; 32 x 32, 16384 tokens of a head, 128 segments, 65 and 41).
+// tokens of 32 heads, four segments, 28 us and not 33; 1024 and 2048, eight segments, 35 and not 37, and
+// 56 either way), and no more segments than 16 (64 x 64: 2048 tokens of 32 heads, 16 segments, 29 us and not
+// 31; 4096 of 16, 32 segments, 35 and 34 composed; 32 x 32, 16384 tokens of a head, 128 segments, 67 and 42).
 constexpr long long kMostJoined = 8 * 128 * 128, kMostSegments = 16;
 
 bool joins(const gdn::LinearProblem& p, bool packed) {

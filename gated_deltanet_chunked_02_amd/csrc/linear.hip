@@ -23,11 +23,11 @@
 // (k and v alone), k_linear_compose turns those into start states in order, and k_linear_fwd runs
 // the segments side by side.  A few segments make their start states themselves.
 //
-// Measured (bf16, heads of 128 x 128): 8 x 2048 tokens of 32 heads 152 us, whose loads
-// and stores alone take 113 with this order of accesses (4.7 TB/s), the matrix units busy 24 % and the
-// vector units 36 %; 16384 tokens of 32 heads 65 + 12 + 134 us.  Four waves of 32 columns instead of
-// eight of 16 took 170; a single barrier a chunk, with two or three buffers of everything, no less; 64
-// narrow heads (4 x 4096 tokens, 64 columns) are one wave a SIMD, 206 us.
+// Measured (bf16, heads of 128 x 128): 8 x 2048 tokens of 32 heads 167 to 182 us, whose loads
+// and stores alone take 113 with this order of accesses (4.7 TB/s), the matrix units busy 27 % and the
+// vector units 41 %; 16384 tokens of 32 heads 64 + 12 + 141 us.  Four waves of 32 columns instead of
+// eight of 16 took 8 % longer; a single barrier a chunk, with two or three buffers of everything, no less; 64
+// narrow heads (4 x 4096 tokens, 64 columns) are one wave a SIMD, 227 us.
 #include "linear_device.h"
 
 namespace gdn {
@@ -37,8 +37,8 @@ namespace {
 // GRAD: the same pass over other tensors makes dq.  With S^T as the state, whose rows run over the value
 // columns, dq_t = scale S_t dout_t is the recurrence with dout for q, v for k and k for v.  There the
 // state meets dout as three bf16 terms, not two, because the sums q . dq that leave the chunk (a) are terms of
-// dg, an fp32 result; and the state is written out at every kLinearAnchor-th chunk's end for the other half
-// of the gradient.
+// dg, an fp32 result; and the state is written out at every r.every-th chunk's end, and the segment's, for the
+// other half of the gradient.
 template <typename E, int DK, int DV, int NW, int OCC, bool GRAD, typename G>
 __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, LinearRun r) {
   constexpr int C = sizeof(E) == 2 ? kLinearChunk : kLinearChunkF32;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   constexpr int KF = Mx<E>::KF, KS = C / KF, TERMS = Mx<E>::TERMS, EPL = Mx<E>::EPL;
   constexpr int STEPS = sizeof(E) == 2 ? KT / 2 : KT, STERMS = GRAD || TERMS < 2 ? TERMS : 2;
   // Products are taken a step at a time where waves are short of registers; four waves of a CU's 16 are
-  // not, and have the more to gain from reads ahead (4 x 4096 tokens, 64 heads of 64 columns: 249 to 233 us)
+  // not, and have the more to gain from reads ahead (4 x 4096 tokens, 64 heads of 64 columns: 6 % less)
   auto fence = [] { if constexpr (NW * OCC >= 16) sched_fence(); };
   typedef typename Mx<E>::frag frag;
   typedef Tile<E, DK> TK;
@@ -73,8 +73,8 @@ __global__ __launch_bounds__(NW * 64, OCC) void k_linear_fwd(LinearProblem p, Li
   // The state in memory is [Dk, Dv]: this one's rows (GRAD: its columns) are the first axis.  Rows past
   // the head lie past the buffer, or are sent there.
   f32x4 S[CW][KT];
-  // every way to a start state adds to what is there: one that loads into S itself took the packed batch of
-  // 12454 tokens from 184 to 189 us
+  // every way to a start state adds to what is there: one that loads into S itself took 3 % longer over a
+  // packed batch of 12454 tokens
   auto state = [&](const float* from, float keep) {
     const __amdgpu_buffer_rsrc_t frs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<float*>(from), 0, from ? (int)cell * 4 : 0, 0x00020000);
@@ -536,6 +536,8 @@ hipError_t launch_dq(const LinearProblem& p, const LinearRun& r, hipStream_t st)
   const int blocks = p.slots * p.H;
   LinearProblem q = p;
   q.group = group_of(p, 1, blocks);
+  // Four waves a SIMD where registers allow: two workgroups a CU in fp32 (75 KB of LDS each).  In bf16 (88 KB)
+  // one fits whatever the registers, and a budget for two waves takes no less (534 us the gradient, and 536).
   constexpr int NW = DV / 16, OCC = DK == 128 && DV == 128 ? 4 : 2;
   if (p.H != p.Hg)
     k_linear_fwd<E, DK, DV, NW, OCC, true, float><<<blocks, NW * 64, 0, st>>>(q, r);

@@ -19,7 +19,7 @@
 //
 //   e^{G_C} <dS, S_start> = <dS, S_end> - sum b,    <dS, S>_start = <dS, S>_end + sum a - sum b,
 //
-// carried in fp64 from chunk to chunk and taken afresh at the anchors (every 8 chunks), where the forward
+// carried in fp64 from chunk to chunk and taken afresh at the anchors (every 8 chunks at most), where the forward
 // pass leaves its state: a difference of sums over 512 tokens at most, each term good to fp32's last
 // bits, so dg keeps fp32's accuracy.  A head's own decay sums all of a sequence's dg, and with it one error
 // many times over: there anchors are twice as many, and what the carried value is off by at each is
@@ -31,12 +31,12 @@
 // dS is held by key rows: a wave has 16 of them and all value columns, so the product over the value
 // columns (dK) takes it from registers as three bf16 terms (its b is a term of dg); the one over key rows
 // (dV) takes it from LDS as two, like M and P: 16 bits or more of each value, so that every output is fp32
-// sums rounded once (with one term, dv of a carried gradient came out 1.25 times as far off, and this pass
-// was 4 % shorter).
+// sums rounded once (with one term, dv of a carried gradient came out 1.25 times as far off, and the
+// gradient took 4 % less).
 //
-// Measured (8 x 2048 tokens, 32 heads of 128 x 128, bf16): dQ's pass 219 us and this one 293, a workgroup a
-// CU (158 KB of LDS), vector units busy 46 %, matrix units 23 %, LDS 29 %, the waves waiting 31 % of their
-// cycles (318 us and 43 % with every operand read where it is used).
+// Measured (8 x 2048 tokens, 32 heads of 128 x 128, bf16): dQ's pass 223 us and this one 326, a workgroup a
+// CU (158 KB of LDS), vector units busy 47 %, matrix units 23 %, LDS 30 %, the waves waiting 29 % of their
+// cycles (43 % and a twelfth longer with every operand read where it is used).
 #include "linear_device.h"
 
 namespace gdn {

@@ -323,8 +323,9 @@ gdn_status gdn_causal_conv1d_bwd(const gdn_conv_desc* d, const void* x, const fl
  * q, k, v, g, o are required unless B*T = 0.  h0 and ht may be the same buffer; no other output may
  * overlap an input.  o of tokens of a packed batch that no sequence has is not written.
  * States and sums are fp32.  In bf16, o is as near as fp32 sums rounded once (scores and the state that
- * meets q keep 16 bits or more on their way to it), ht as exact as fp32 sums.  Few or long sequences are split into segments
- * that run in parallel, so results depend on the descriptor in their last bits, never on scheduling.
+ * meets q keep 16 bits or more on their way to it), ht as exact as fp32 sums.  Few or long sequences are
+ * split into segments that run in parallel, so results depend on the descriptor in their last bits, never
+ * on scheduling.
  * An infinity or a NaN in q, k, v or g reaches its own head (its q/k head's value heads) of its own
  * sequence, from the chunk it is in: the outputs of that chunk's earlier tokens may be NaN too.  One in h0
  * reaches its own head of its own sequence.  In bf16 an infinity in v or in a state may come out as a NaN. */
